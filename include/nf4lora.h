@@ -246,6 +246,125 @@ int nf4_repeat_kv_fwd(const uint16_t* v, int64_t T, int64_t q, int64_t kv, int64
 int nf4_repeat_kv_bwd(const uint16_t* da, int64_t T, int64_t q, int64_t kv, int64_t head_dim, uint16_t* dv,
                       nf4_stream stream);
 
+/* ------------------------------------------------------------------ decoder layer
+ * What a decoder layer's training step needs beside the linears and the glue above:
+ * rotary positions, softmax attention forward and backward, and the gradients' global
+ * norm with clipping. Activations are device bf16, row-major and densely packed like
+ * everywhere in this header: q [T][hq*head_dim], k and v [T][hkv*head_dim], head after
+ * head in a row. Results are deterministic; nothing here allocates.
+ */
+
+/*
+ * Rotary positions on q and k in one launch. Pair i of a head is its elements i and
+ * i + head_dim/2 (i < head_dim/2). Each pair belongs to one of n_axes position axes:
+ * the first sections[0] pairs to axis 0, the next sections[1] to axis 1, and so on (one
+ * axis: a text decoder; three: time, height and width of images and video).
+ *     phi = pos[axis][t] * inv_freq[i]   (fp64, whole turns removed before rounding)
+ *     lo' = RNbf(lo cos phi - hi sin phi),  hi' = RNbf(hi cos phi + lo sin phi)
+ *   q, k       device bf16 (k or q may be NULL when its head count is 0)
+ *   pos        device int32 [n_axes][T], any values
+ *   inv_freq   device fp64 [head_dim/2], radians a position (for plain rotary embeddings
+ *              theta^(-2i/head_dim); scaled variants pass their own)
+ *   sections   HOST int array [n_axes], each >= 1, sum = head_dim/2; n_axes in 1..4
+ *   inverse    0, or 1 to rotate by -phi: the backward (dq, dk from the rotated ones)
+ *   q_out, k_out  device bf16; each may be its input itself (not a shifted overlap)
+ * head_dim a multiple of 16 up to 256; hq, hkv <= 1024; T <= 2^23; T == 0 is a no-op.
+ * q, k and the outputs 16-byte, inv_freq 8-byte aligned.
+ */
+int nf4_rope(const uint16_t* q, const uint16_t* k, int64_t T, int64_t hq, int64_t hkv, int64_t head_dim,
+             const int32_t* pos, const double* inv_freq, const int* sections, int n_axes, int inverse,
+             uint16_t* q_out, uint16_t* k_out, nf4_stream stream);
+
+/*
+ * Softmax attention over packed sequences, grouped queries: query head i reads kv head
+ * i / (hq/hkv). For row i of a sequence, over the rows j of the same sequence (j <= i when
+ * causal):
+ *     S_ij = scale * q_i . k_j
+ *     lse_i = log sum_j e^(S_ij)                    (fp32, saved for the backward)
+ *     o_i = RNbf( sum_j e^(S_ij - lse_i) v_j )
+ *   cu_seqlens  device int32 [n_seqs + 1], non-decreasing, within 0..T: sequence s is rows
+ *               cu[s] .. cu[s+1]-1 (empty ones allowed). NULL: one sequence of all T rows
+ *               (n_seqs 0 or 1). Rows outside every sequence are neither read into results
+ *               nor written. Values outside 0..T are clamped.
+ *   causal      0 or 1
+ *   scale       finite, > 0 (usually 1/sqrt(head_dim))
+ *   o           device bf16 [T][hq*head_dim] (written)
+ *   lse         device fp32 [hq][T] (written)
+ * The probabilities are rounded to bf16 for their product with v. A value of k or v that is
+ * not finite makes rows of its own sequence not finite (also rows that a causal mask hides
+ * it from), never rows of another. head_dim 32, 64 or 128; hkv | hq <= 1024; T <= 2^23;
+ * n_seqs <= 2^20; T == 0 is a no-op. q, k, v, o 16-byte aligned; o must not overlap q, k, v.
+ */
+int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t T, int64_t hq, int64_t hkv,
+                 int64_t head_dim, const int32_t* cu_seqlens, int64_t n_seqs, int causal, float scale, uint16_t* o,
+                 float* lse, nf4_stream stream);
+
+/* Bytes of device workspace nf4_attn_bwd needs for these sizes (n_seqs 0 or 1: no cu_seqlens). */
+size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, int64_t n_seqs);
+
+/*
+ * Backward of the same attention; the probabilities are recomputed from lse:
+ *     P_ij = e^(S_ij - lse_i),  delta_i = do_i . o_i,  dS_ij = P_ij (do_i . v_j - delta_i)
+ *     dq_i = RNbf( scale sum_j dS_ij k_j )
+ *     dk_j = RNbf( scale sum_i dS_ij q_i ),  dv_j = RNbf( sum_i P_ij do_i )
+ * with dk and dv summed (in fp32, fixed order) over the query heads of each kv head too.
+ *   o, lse      as nf4_attn_fwd wrote them
+ *   dO          device bf16 [T][hq*head_dim]
+ *   dq, dk, dv  device bf16 like q, k, v (overwritten; rows outside every sequence are
+ *               left as they were); they must not overlap the inputs
+ *   ws          device workspace of at least nf4_attn_bwd_workspace() bytes, 256-byte
+ *               aligned; its contents on entry are ignored. Calls that may run at the same
+ *               time (two streams, two graphs) need one each.
+ * P and dS are rounded to bf16 for their products. Other arguments, limits and errors as
+ * nf4_attn_fwd.
+ */
+int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
+                 const uint16_t* dO, int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, const int32_t* cu_seqlens,
+                 int64_t n_seqs, int causal, float scale, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws,
+                 size_t ws_bytes, nf4_stream stream);
+
+/*
+ * Global norm of many gradient tensors, and clipping to it:
+ *     n = sqrt( sum over all elements g of all tensors of g^2 )     (sums in fp64)
+ *     out = RN( g * min(1, max_norm / (n + 1e-6)) )                 (RN to the tensor's type)
+ * A list is made once over the gradient buffers of a training program and used every
+ * step; the buffers must outlive it, and so must the table, device memory of the caller
+ * that holds the list's description (nf4_grad_list_table() bytes, 256-byte aligned).
+ * nf4_grad_list_create copies the description there on `stream` and waits for the copy.
+ *   tensors  HOST array of n descriptions (read during the call only); dtype bf16 or fp32,
+ *            mixed freely; pointers aligned to their elements; count 0 allowed (pointers
+ *            then ignored); out == grad scales in place
+ * NF4_E_ARG when a tensor's out overlaps any other range of the list (the same tensor
+ * twice, a shifted overlap with its own grad). n <= 2^20, count <= 2^36.
+ */
+typedef struct {
+    const void* grad; /* device */
+    void* out;        /* device; where the scaled gradient goes, may be grad */
+    int64_t count;    /* elements */
+    int dtype;        /* NF4_DTYPE_BF16 or NF4_DTYPE_F32, of both */
+} nf4_grad_tensor;
+
+typedef struct nf4_grad_list nf4_grad_list;
+
+size_t nf4_grad_list_table(const nf4_grad_tensor* tensors, int n); /* 0 for arguments that create refuses */
+int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, size_t table_bytes, nf4_stream stream,
+                         nf4_grad_list** out);
+/* Frees the handle (host memory only); calls already enqueued keep using the table. */
+int nf4_grad_list_destroy(nf4_grad_list* list);
+
+/* Bytes of device workspace of the two calls below (256-byte aligned; one per call that may run at the same time). */
+size_t nf4_grad_workspace(void);
+
+/* *norm (device fp32) = n; the outs are not touched. An empty list gives 0. */
+int nf4_grad_norm(const nf4_grad_list* list, float* norm, void* ws, size_t ws_bytes, nf4_stream stream);
+
+/* *norm = n (before clipping) and every out written; a tensor in place is left alone when
+ * nothing has to be scaled. max_norm finite, >= 0. When a gradient is not finite,
+ * neither is *norm, and the gradients are passed on unscaled: the caller sees it and skips
+ * its step. */
+int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* ws, size_t ws_bytes,
+                  nf4_stream stream);
+
 /*
  * Instrumentation for measurement: the next nf4_lora_linear_fwd or
  * nf4_lora_linear_bwd call made by this host thread records `start` (a

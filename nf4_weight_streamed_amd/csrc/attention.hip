@@ -1,0 +1,731 @@
+// Grouped-query softmax attention over packed sequences, forward and backward, for the
+// decoder stack's training step. With q [T][hq*D], k, v [T][hkv*D] in bf16, G = hq / hkv
+// query heads per kv head, s = scale, and for row i of a sequence the keys j of the same
+// sequence (j <= i when causal):
+//   S_ij = s q_i . k_j      lse_i = log sum_j e^{S_ij}      o_i = sum_j e^{S_ij - lse_i} v_j
+//   P = e^{S - lse}   delta_i = do_i . o_i   dS_ij = P_ij (do_i . v_j - delta_i)
+//   dv_j = sum_i P_ij do_i   dq_i = s sum_j dS_ij k_j   dk_j = s sum_i dS_ij q_i
+// (dk, dv also summed over the G query heads of a kv head). Scores are never stored: the
+// backward recomputes P from lse. Everything is fp32 except the operands of the second
+// products, which are P and dS rounded to bf16 for the bf16 MFMA: a relative error of at
+// most 2^-8 per term, of the size of the rounding of the bf16 results.
+//
+// MFMA layout used throughout (32x32x16): an accumulator lane l holds column l % 32 and
+// rows 8 (e / 4) + 4 (l / 32) + e % 4; an operand lane holds one row (or column) and 8
+// contraction indices. Each first product is formed with the later contraction index as
+// accumulator row, so that elements 8g .. 8g + 7 of the accumulator, rounded, are the
+// lane's operand of the second product as they stand, with the contraction order
+//   lane half h, slot j  <->  index 16 g + 8 (j / 4) + 4 h + j % 4,
+// and the other operand is read from row-major LDS in that same order by two transposing
+// reads (ds_read_b64_tr_b16). P and dS never cross lanes or go through LDS.
+#include <cmath>
+
+#include "../../include/nf4lora.h"
+#include "common.h"
+#include "device.h"
+
+namespace nf4 {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 64;  // rows of a staged tile (keys in fwd and dq, queries in dkv)
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+struct AttnArgs {
+    const uint16_t *q, *k, *v, *o, *dO;
+    const float* lse_in;
+    uint16_t *out, *dq, *dk, *dv;
+    float *lse, *delta, *part;  // delta [hq][T]; part: fp32 shares of dk then dv, [split][T][hkv*D] each
+    const int32_t* cu;
+    int T, n_seqs, hq, hkv, causal, tiles, splits;
+    float scale;
+};
+
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+struct Tile {
+    int begin, len, row0;  // first row and length of the sequence; first row of the tile within it
+};
+
+// Tile number g of the sequences' tiles of BM rows, numbered sequence after sequence: one
+// wave scans 64 sequences at a time. The bounds read from the device are clamped to
+// [0, T] and to non-negative lengths, so that no value of theirs leads outside the
+// tensors. False when there are fewer tiles.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int bm, int g, Tile& t) {
+    if (!a.cu) {
+        t = {0, a.T, g * bm};
+        return t.row0 < a.T;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+        const int s = min(s0 + lane, a.n_seqs - 1);
+        const int b = min(max(a.cu[s], 0), a.T);
+        const int e = min(max(a.cu[s + 1], b), a.T);
+        const int n = s0 + lane < a.n_seqs ? (e - b + bm - 1) / bm : 0;
+        int incl = n;
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += v;
+        }
+        const int first = before + incl - n;
+        const uint64_t hit = __ballot(g >= first && g < first + n);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            t.begin = uni(__shfl(b, l, 64));
+            t.len = uni(__shfl(e - b, l, 64));
+            t.row0 = uni((g - __shfl(first, l, 64)) * bm);
+            return true;
+        }
+        before += uni(__shfl(incl, 63, 64));
+    }
+    return false;
+}
+
+// Workgroup id -> (kv head, item of that head). Items of one kv head share its K and V (or
+// its queries' dO), so they are kept on as few XCDs as the head count allows: the XCD of a
+// workgroup is its id mod 8, and each L2 then holds the operands of hkv / 8 heads at a time.
+// False past the last item. Grids: attn_grid.
+__device__ __forceinline__ bool pick_item(uint32_t b, int hkv, int items, int& head, int& item) {
+    if (hkv % 8 == 0) {
+        const int x = b % 8, l = b / 8;
+        head = x * (hkv / 8) + l / items;
+        item = l % items;
+        return true;
+    }
+    if (8 % hkv == 0) {
+        const int x = b % 8, l = b / 8, n = 8 / hkv;
+        head = x / n;
+        item = l * n + x % n;
+        return item < items;
+    }
+    head = b % hkv;
+    item = b / hkv;
+    return true;
+}
+
+int64_t attn_grid(int hkv, int64_t items) {
+    if (hkv % 8 != 0 && 8 % hkv == 0) return 8 * cdiv(items, 8 / hkv);
+    return hkv * items;
+}
+
+// LDS image of a staged tile: rows of D bf16, the 16-byte chunk c of row r at chunk
+// c ^ swz(r). The 256-byte bank line holds 128 / D rows; the XOR spreads the remaining row
+// bits over the chunks so that both readers cover all banks: 16 rows of one chunk
+// (ds_read_b128 of an operand) and 8 rows x 2 chunk pairs (transposing reads).
+template <int D>
+__device__ __forceinline__ int swz(int r) {
+    constexpr int S = D == 128 ? 0 : D == 64 ? 1 : 2;
+    return (((r >> S) & (D / 16 - 1)) << 1) | ((r >> 3) & 1);
+}
+
+// Per-lane byte offsets into a staged tile.
+template <int D>
+struct LdsMap {
+    int row_chunk[D / 16];    // operand read: row l % 32, chunk 2 s + l / 32 (contraction step s)
+    int tr[D / 32][2];        // transposing read: column block nb, rows 8 j + 4 (l / 32) + (l % 16) / 4
+    __device__ __forceinline__ LdsMap(int lane) {
+        const int r = lane & 31, h = lane >> 5, i = lane & 15, g = (lane >> 4) & 1;
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s) row_chunk[s] = r * 2 * D + ((2 * s + h) ^ swz<D>(r)) * 16;
+#pragma unroll
+        for (int nb = 0; nb < D / 32; ++nb)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = 8 * j + 4 * h + (i >> 2);
+                tr[nb][j] = row * 2 * D + ((4 * nb + 2 * g + ((i >> 1) & 1)) ^ swz<D>(row)) * 16 + (i & 1) * 8;
+            }
+    }
+};
+
+__device__ __forceinline__ bf16x8 lds_frag(const char* p) { return as_bf16x8(*reinterpret_cast<const u32x4*>(p)); }
+
+// 8 contraction indices (two groups of 4 rows) of one column, from row-major LDS.
+__device__ __forceinline__ bf16x8 lds_frag_tr(const char* p0, const char* p1) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return as_bf16x8(u32x4{x.x, x.y, y.x, y.y});
+}
+
+__device__ __forceinline__ bf16x8 pack8(const f32x16& v, int g) {
+    return as_bf16x8(u32x4{pack_bf16x2(v[8 * g], v[8 * g + 1]), pack_bf16x2(v[8 * g + 2], v[8 * g + 3]),
+                           pack_bf16x2(v[8 * g + 4], v[8 * g + 5]), pack_bf16x2(v[8 * g + 6], v[8 * g + 7])});
+}
+
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.0f;
+    return z;
+}
+
+// The other half-wave's value (lane l ^ 32) combined with this lane's.
+__device__ __forceinline__ float max_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Global -> LDS copy of a tile by the W waves of the workgroup, 16 bytes a lane and
+// instruction: LDS is written linearly, so the swizzle is applied to the global chunk.
+template <int D, int W>
+struct TileCopy {
+    static constexpr int kRounds = kTile * 2 * D / (W * 1024);
+    static_assert(kRounds * W * 1024 == kTile * 2 * D, "the waves' copies cover the tile");
+    uint32_t off[kRounds];
+    __device__ __forceinline__ TileCopy(int wave, int lane, int ld) {
+#pragma unroll
+        for (int n = 0; n < kRounds; ++n) {
+            const int p = (n * W + wave) * 1024 + lane * 16;
+            const int row = p / (2 * D), ch = (p / 16) % (D / 8);
+            off[n] = uint32_t(row) * uint32_t(ld) * 2u + uint32_t(ch ^ swz<D>(row)) * 16u;
+        }
+    }
+    // rows >= `rows` read as zeros
+    __device__ __forceinline__ void issue(const uint16_t* base, int rows, int ld, char* lds, int wave) const {
+        const auto r = make_rsrc(base, rows > 0 ? uint32_t(min(rows, kTile) - 1) * uint32_t(ld) * 2u + 2u * D : 0u);
+#pragma unroll
+        for (int n = 0; n < kRounds; ++n) buf_load16_lds(r, off[n], lds + (n * W + wave) * 1024);
+    }
+};
+
+// ------------------------------------------------------------------ forward
+
+// One workgroup: W waves x 32 queries of one head; K and V in tiles of 64 keys, double
+// buffered in LDS. S^T = K Q^T puts a query in a lane, so the softmax statistics are one
+// register each. The running maximum is raised, and o and the sum rescaled, only when some
+// row's tile maximum exceeds it by more than 8 (in log2 units): p then stays below 2^8.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
+    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
+    __shared__ __align__(1024) char sK[2][kTile * 2 * D];
+    __shared__ __align__(1024) char sV[2][kTile * 2 * D];
+    const int G = a.hq / a.hkv;
+    int kvh, item;
+    if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
+    const int head = kvh * G + item % G;
+    Tile t;
+    if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;  // longest rows first
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int ldq = a.hq * D, ldk = a.hkv * D;
+    const int q_row = t.row0 + 32 * wave + (lane & 31);
+    const float c = a.scale * kLog2e;
+
+    bf16x8 qf[KS];
+    {
+        const int rows = t.len - t.row0;
+        const auto r = make_rsrc(a.q + (size_t(t.begin) + t.row0) * ldq + head * D,
+                                 uint32_t(min(rows, BM) - 1) * uint32_t(ldq) * 2u + 2u * D);
+        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) qf[s] = as_bf16x8(buf_load16(r, o + 32u * s));
+    }
+    const LdsMap<D> map(lane);
+    const TileCopy<D, W> copy(wave, lane, ldk);
+    const uint16_t* kb = a.k + size_t(t.begin) * ldk + kvh * D;
+    const uint16_t* vb = a.v + size_t(t.begin) * ldk + kvh * D;
+
+    f32x16 acc[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[nb] = zero16();
+    float m = -INFINITY, l = 0.0f;
+    const int q_lo = t.row0 + 32 * wave;
+    const int keys = a.causal ? min(t.len, t.row0 + BM) : t.len;
+    const int n = (keys + kTile - 1) / kTile;
+
+    auto stage = [&](int j, char* k, char* v) {
+        copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
+        copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
+    };
+    stage(0, sK[0], sV[0]);
+    for (int j = 0; j < n; ++j) {
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (j + 1 < n) stage(j + 1, sK[(j + 1) & 1], sV[(j + 1) & 1]);
+        const int k0 = j * kTile;
+        if (a.causal && k0 > q_lo + 31) continue;  // nothing of this tile for the wave's rows
+        const char* k = sK[j & 1];
+        const char* v = sV[j & 1];
+        f32x16 s[2] = {zero16(), zero16()};
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                s[b] = mfma32x32x16(lds_frag(k + b * 64 * D + map.row_chunk[i]), qf[i], s[b]);
+        if (k0 + kTile > t.len || (a.causal && k0 + kTile - 1 > q_lo)) {
+            const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (32 * b + 8 * (e / 4) + e % 4 > last) s[b][e] = -INFINITY;
+        }
+        float mt = s[0][0];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) mt = fmaxf(mt, s[b][e]);
+        mt = max_halves(mt) * c;
+        if (__any(mt > m + 8.0f)) {
+            const float mn = fmaxf(m, mt);
+            const float f = exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[nb][e] *= f;
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], c, -m));
+                l += s[b][e];
+            }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const bf16x8 p = pack8(s[g / 2], g % 2);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                acc[nb] = mfma32x32x16(lds_frag_tr(v + g * 32 * D + map.tr[nb][0], v + g * 32 * D + map.tr[nb][1]), p,
+                                       acc[nb]);
+        }
+    }
+    l = sum_halves(l);
+    if (q_row < t.len) {
+        const size_t row = size_t(t.begin) + q_row;
+        const float inv = 1.0f / l;
+        uint16_t* out = a.out + row * ldq + head * D;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<u32x2*>(out + 32 * nb + 2 * e + 4 * h) =
+                    u32x2{pack_bf16x2(acc[nb][e] * inv, acc[nb][e + 1] * inv),
+                          pack_bf16x2(acc[nb][e + 2] * inv, acc[nb][e + 3] * inv)};
+        if (h == 0) a.lse[size_t(head) * a.T + row] = (m + log2f(l)) * kLn2;
+    }
+}
+
+// ------------------------------------------------------------------ backward: dq (and delta)
+
+// As the forward, with dO beside Q in registers: per 64-key tile S^T = K Q^T,
+// dP^T = V dO^T, dS^T in place, dq^T += K^T dS^T. delta is formed here first (the dk/dv
+// kernel behind this one reads it).
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
+    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
+    __shared__ __align__(1024) char sK[2][kTile * 2 * D];
+    __shared__ __align__(1024) char sV[2][kTile * 2 * D];
+    const int G = a.hq / a.hkv;
+    int kvh, item;
+    if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
+    const int head = kvh * G + item % G;
+    Tile t;
+    if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int ldq = a.hq * D, ldk = a.hkv * D;
+    const int q_row = t.row0 + 32 * wave + (lane & 31);
+    const float c = a.scale * kLog2e;
+
+    const TileCopy<D, W> copy(wave, lane, ldk);
+    const uint16_t* kb = a.k + size_t(t.begin) * ldk + kvh * D;
+    const uint16_t* vb = a.v + size_t(t.begin) * ldk + kvh * D;
+    auto stage = [&](int j, char* k, char* v) {
+        copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
+        copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
+    };
+    stage(0, sK[0], sV[0]);
+
+    bf16x8 qf[KS], df[KS];
+    float delta = 0.0f;
+    {
+        const int rows = t.len - t.row0;
+        const size_t at = (size_t(t.begin) + t.row0) * ldq + head * D;
+        const uint32_t bytes = uint32_t(min(rows, BM) - 1) * uint32_t(ldq) * 2u + 2u * D;
+        const auto rq = make_rsrc(a.q + at, bytes), rd = make_rsrc(a.dO + at, bytes), ro = make_rsrc(a.o + at, bytes);
+        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            qf[s] = as_bf16x8(buf_load16(rq, o + 32u * s));
+            df[s] = as_bf16x8(buf_load16(rd, o + 32u * s));
+            const bf16x8 of = as_bf16x8(buf_load16(ro, o + 32u * s));
+#pragma unroll
+            for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(float(df[s][e]), float(of[e]), delta);
+        }
+        delta = sum_halves(delta);
+    }
+    float lse2 = 0.0f;
+    if (q_row < t.len) {
+        const size_t at = size_t(head) * a.T + t.begin + q_row;
+        lse2 = a.lse_in[at] * kLog2e;
+        if (h == 0) a.delta[at] = delta;
+    }
+    const LdsMap<D> map(lane);
+
+    f32x16 acc[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[nb] = zero16();
+    const int q_lo = t.row0 + 32 * wave;
+    const int keys = a.causal ? min(t.len, t.row0 + BM) : t.len;
+    const int n = (keys + kTile - 1) / kTile;
+    for (int j = 0; j < n; ++j) {
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (j + 1 < n) stage(j + 1, sK[(j + 1) & 1], sV[(j + 1) & 1]);
+        const int k0 = j * kTile;
+        if (a.causal && k0 > q_lo + 31) continue;
+        const char* k = sK[j & 1];
+        const char* v = sV[j & 1];
+        const bool edge = k0 + kTile > t.len || (a.causal && k0 + kTile - 1 > q_lo);
+        const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                s = mfma32x32x16(lds_frag(k + b * 64 * D + map.row_chunk[i]), qf[i], s);
+                dp = mfma32x32x16(lds_frag(v + b * 64 * D + map.row_chunk[i]), df[i], dp);
+            }
+            if (edge) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (32 * b + 8 * (e / 4) + e % 4 > last) s[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2)) * (dp[e] - delta);
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const bf16x8 ds = pack8(s, g);
+                const char* kg = k + (2 * b + g) * 32 * D;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    acc[nb] = mfma32x32x16(lds_frag_tr(kg + map.tr[nb][0], kg + map.tr[nb][1]), ds, acc[nb]);
+            }
+        }
+    }
+    if (q_row < t.len) {
+        uint16_t* out = a.dq + (size_t(t.begin) + q_row) * ldq + head * D;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<u32x2*>(out + 32 * nb + 2 * e + 4 * h) =
+                    u32x2{pack_bf16x2(acc[nb][e] * a.scale, acc[nb][e + 1] * a.scale),
+                          pack_bf16x2(acc[nb][e + 2] * a.scale, acc[nb][e + 3] * a.scale)};
+    }
+}
+
+// ------------------------------------------------------------------ backward: dk, dv
+
+// One workgroup: W waves x 32 keys of one kv head, K and V fragments in registers; the
+// queries of the G heads pass through LDS in tiles of 64 (Q, dO, lse, delta). Per 32
+// queries S = Q K^T, dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
+// With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
+// workgroup, whose fp32 shares k_attn_bwd_join adds in order.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
+    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
+    __shared__ __align__(1024) char sQ[2][kTile * 2 * D];
+    __shared__ __align__(1024) char sD[2][kTile * 2 * D];
+    __shared__ __align__(16) float sL[2][2][kTile];  // [buffer][lse * log2 e, delta]
+    const int G = a.hq / a.hkv;
+    int kvh, item;
+    if (!pick_item(blockIdx.x, a.hkv, a.tiles * a.splits, kvh, item)) return;
+    const int split = item % a.splits;
+    Tile t;
+    if (!find_tile(a, BM, item / a.splits, t)) return;  // causal: the first keys have the most queries
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int ldq = a.hq * D, ldk = a.hkv * D;
+    const int key = t.row0 + 32 * wave + (lane & 31);
+    const int k_lo = t.row0 + 32 * wave;
+    const float c = a.scale * kLog2e;
+
+    // (head, query tile) pairs: nq tiles a head, from the first that sees a key of this tile
+    const int tile_lo = a.causal ? t.row0 / kTile : 0;
+    const int nq = (t.len + kTile - 1) / kTile - tile_lo;
+    const int total = G * nq;
+    const int i0 = int(int64_t(split) * total / a.splits), i1 = int(int64_t(split + 1) * total / a.splits);
+
+    bf16x8 kf[KS], vf[KS];
+    {
+        const size_t at = (size_t(t.begin) + t.row0) * ldk + kvh * D;
+        const uint32_t bytes = uint32_t(min(t.len - t.row0, BM) - 1) * uint32_t(ldk) * 2u + 2u * D;
+        const auto rk = make_rsrc(a.k + at, bytes), rv = make_rsrc(a.v + at, bytes);
+        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
+            vf[s] = as_bf16x8(buf_load16(rv, o + 32u * s));
+        }
+    }
+    const LdsMap<D> map(lane);
+    const TileCopy<D, W> copy(wave, lane, ldq);
+    float stat = 0.0f;  // this thread's lse or delta of the tile being staged
+    auto stage = [&](int i, int buf) {
+        const int head = kvh * G + i / nq, q0 = (tile_lo + i % nq) * kTile;
+        const size_t at = (size_t(t.begin) + q0) * ldq + head * D;
+        copy.issue(a.q + at, t.len - q0, ldq, sQ[buf], wave);
+        copy.issue(a.dO + at, t.len - q0, ldq, sD[buf], wave);
+        if (threadIdx.x < 2 * kTile) {
+            const int r = threadIdx.x & (kTile - 1), which = threadIdx.x / kTile;
+            // rows past the sequence: lse = +inf makes their P zero
+            stat = which ? 0.0f : INFINITY;
+            if (q0 + r < t.len) {
+                const size_t s = size_t(head) * a.T + t.begin + q0 + r;
+                stat = which ? a.delta[s] : a.lse_in[s] * kLog2e;
+            }
+        }
+    };
+    auto put_stat = [&](int buf) {
+        if (threadIdx.x < 2 * kTile) sL[buf][threadIdx.x / kTile][threadIdx.x & (kTile - 1)] = stat;
+    };
+
+    f32x16 dk[NB], dv[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) dk[nb] = zero16(), dv[nb] = zero16();
+    if (i0 < i1) stage(i0, 0);
+    for (int i = i0; i < i1; ++i) {
+        const int buf = (i - i0) & 1;
+        put_stat(buf);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (i + 1 < i1) stage(i + 1, buf ^ 1);
+        const int q0 = (tile_lo + i % nq) * kTile;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int qb = q0 + 32 * b;
+            if (a.causal && qb + 31 < k_lo) continue;
+            const char* q = sQ[buf] + b * 64 * D;
+            const char* d = sD[buf] + b * 64 * D;
+            f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+            for (int e = 0; e < KS; ++e) {
+                s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), kf[e], s);
+                dp = mfma32x32x16(lds_frag(d + map.row_chunk[e]), vf[e], dp);
+            }
+            if (a.causal && qb < k_lo + 31) {
+                const int first = key - qb - 4 * h;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (8 * (e / 4) + e % 4 < first) s[e] = -INFINITY;
+            }
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const f32x4 ls = *reinterpret_cast<const f32x4*>(&sL[buf][0][32 * b + 2 * e + 4 * h]);
+                const f32x4 dl = *reinterpret_cast<const f32x4*>(&sL[buf][1][32 * b + 2 * e + 4 * h]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    s[e + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + x], c, -ls[x]));
+                    dp[e + x] = s[e + x] * (dp[e + x] - dl[x]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const bf16x8 p = pack8(s, g), ds = pack8(dp, g);
+                const char *dg = d + g * 32 * D, *qg = q + g * 32 * D;
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+                    dv[nb] = mfma32x32x16(lds_frag_tr(dg + map.tr[nb][0], dg + map.tr[nb][1]), p, dv[nb]);
+                    dk[nb] = mfma32x32x16(lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]), ds, dk[nb]);
+                }
+            }
+        }
+    }
+    if (key >= t.len) return;
+    const size_t row = size_t(t.begin) + key;
+    if (a.splits == 1) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const size_t at = row * ldk + kvh * D + 32 * nb + 2 * e + 4 * h;
+                *reinterpret_cast<u32x2*>(a.dk + at) =
+                    u32x2{pack_bf16x2(dk[nb][e] * a.scale, dk[nb][e + 1] * a.scale),
+                          pack_bf16x2(dk[nb][e + 2] * a.scale, dk[nb][e + 3] * a.scale)};
+                *reinterpret_cast<u32x2*>(a.dv + at) =
+                    u32x2{pack_bf16x2(dv[nb][e], dv[nb][e + 1]), pack_bf16x2(dv[nb][e + 2], dv[nb][e + 3])};
+            }
+        return;
+    }
+    const size_t all = size_t(a.T) * ldk;
+    float* pk = a.part + size_t(split) * all + row * ldk + kvh * D;
+    float* pv = pk + size_t(a.splits) * all;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const int at = 32 * nb + 2 * e + 4 * h;
+            *reinterpret_cast<f32x4*>(pk + at) = f32x4{dk[nb][e], dk[nb][e + 1], dk[nb][e + 2], dk[nb][e + 3]};
+            *reinterpret_cast<f32x4*>(pv + at) = f32x4{dv[nb][e], dv[nb][e + 1], dv[nb][e + 2], dv[nb][e + 3]};
+        }
+}
+
+// dk = RNbf(scale * sum of the shares), dv = RNbf(sum of the shares), in split order, over
+// the rows of the sequences; 4 elements a thread.
+__global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a, int ldk) {
+    const size_t all = size_t(a.T) * ldk;
+    int lo = 0, hi = a.T;
+    if (a.cu) {
+        lo = min(max(a.cu[0], 0), a.T);
+        hi = min(max(a.cu[a.n_seqs], lo), a.T);
+    }
+    const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (i < size_t(lo) * ldk || i >= size_t(hi) * ldk) return;
+    const float* p = a.part + (blockIdx.y ? size_t(a.splits) * all : 0) + i;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int z = 0; z < a.splits; ++z) s += *reinterpret_cast<const f32x4*>(p + size_t(z) * all);
+    const float f = blockIdx.y ? 1.0f : a.scale;
+    *reinterpret_cast<u32x2*>((blockIdx.y ? a.dv : a.dk) + i) =
+        u32x2{pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f)};
+}
+
+constexpr int kWaves = 4;
+
+int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
+    return cu ? T / bm + n_seqs : cdiv(T, bm);
+}
+
+// Shares of dk and dv: enough workgroups for two a CU where the keys alone give fewer.
+int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G) {
+    const int64_t wgs = cdiv(T, 32 * kWaves) * hkv;
+    const int64_t most = std::min<int64_t>(16, G * cdiv(T, kTile));
+    return int(std::max<int64_t>(1, std::min<int64_t>(most, cdiv(512, wgs))));
+}
+
+bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
+
+int check_attn(const char* fn, int64_t T, int64_t hq, int64_t hkv, int64_t D, const int32_t* cu, int64_t n_seqs,
+               int causal, float scale) {
+    if (D != 32 && D != 64 && D != 128)
+        return fail(NF4_E_SHAPE, "%s: head_dim must be 32, 64 or 128 (got %lld)", fn, (long long)D);
+    if (T < 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024)
+        return fail(NF4_E_SHAPE, "%s: need 0 <= T <= 2^23 and hkv | hq <= 1024 (got T=%lld hq=%lld hkv=%lld)", fn,
+                    (long long)T, (long long)hq, (long long)hkv);
+    if (cu ? (n_seqs < 1 || n_seqs > (int64_t(1) << 20)) : (n_seqs != 0 && n_seqs != 1))
+        return fail(NF4_E_SHAPE, "%s: need 1 <= n_seqs <= 2^20 with cu_seqlens, 0 or 1 without (got %lld)", fn,
+                    (long long)n_seqs);
+    if (causal != 0 && causal != 1) return fail(NF4_E_ARG, "%s: causal must be 0 or 1 (got %d)", fn, causal);
+    if (!std::isfinite(scale) || scale <= 0.0f)
+        return fail(NF4_E_ARG, "%s: scale must be finite and positive (got %g)", fn, double(scale));
+    if (cu && reinterpret_cast<uintptr_t>(cu) % 4 != 0)
+        return fail(NF4_E_ARG, "%s: cu_seqlens must be 4-byte aligned", fn);
+    return NF4_OK;
+}
+
+struct AttnBwdPlan {
+    int splits;
+    size_t delta_bytes, part_bytes;
+};
+
+AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs) {
+    AttnBwdPlan p{};
+    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv));
+    p.delta_bytes = (size_t(T) * hq * 4 + 255) & ~size_t(255);
+    p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * T * hkv * D * 4 : 0;
+    return p;
+}
+
+// Workgroups of a launch, refused where they would pass the 31-bit grid.
+int check_grid(const char* fn, int64_t wgs) {
+    if (wgs > 0x7FFFFFFF) return fail(NF4_E_SHAPE, "%s: too many tiles (%lld workgroups)", fn, (long long)wgs);
+    return NF4_OK;
+}
+
+template <int D>
+int run_fwd(const AttnArgs& in, hipStream_t stream) {
+    AttnArgs a = in;
+    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kWaves));
+    const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
+    if (int st = check_grid("nf4_attn_fwd", wgs); st != NF4_OK) return st;
+    hipLaunchKernelGGL((k_attn_fwd<D, kWaves>), dim3(unsigned(wgs)), dim3(64 * kWaves), 0, stream, a);
+    return check_launch("nf4_attn_fwd");
+}
+
+template <int D>
+int run_bwd(const AttnArgs& in, hipStream_t stream) {
+    AttnArgs a = in;
+    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kWaves));
+    const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
+    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
+    if (int st = check_grid("nf4_attn_bwd", std::max(wgs, wgs_kv)); st != NF4_OK) return st;
+    hipLaunchKernelGGL((k_attn_bwd_dq<D, kWaves>), dim3(unsigned(wgs)), dim3(64 * kWaves), 0, stream, a);
+    hipLaunchKernelGGL((k_attn_bwd_dkv<D, kWaves>), dim3(unsigned(wgs_kv)), dim3(64 * kWaves), 0, stream, a);
+    if (a.splits > 1) {
+        const int ldk = a.hkv * D;
+        hipLaunchKernelGGL(k_attn_bwd_join, dim3(unsigned(cdiv(int64_t(a.T) * ldk, 1024)), 2), dim3(256), 0, stream, a,
+                           ldk);
+    }
+    return check_launch("nf4_attn_bwd");
+}
+
+}  // namespace
+
+}  // namespace nf4
+
+using namespace nf4;
+
+extern "C" {
+
+int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t T, int64_t hq, int64_t hkv,
+                 int64_t head_dim, const int32_t* cu_seqlens, int64_t n_seqs, int causal, float scale, uint16_t* o,
+                 float* lse, nf4_stream stream) {
+    const char* fn = "nf4_attn_fwd";
+    int st = check_attn(fn, T, hq, hkv, head_dim, cu_seqlens, n_seqs, causal, scale);
+    if (st != NF4_OK) return st;
+    if (T == 0) return NF4_OK;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !lse ||
+        reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+        return fail(NF4_E_ARG, "%s: q, k, v and o must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
+    AttnArgs a{};
+    a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.cu = cu_seqlens;
+    a.T = int(T), a.n_seqs = int(n_seqs), a.hq = int(hq), a.hkv = int(hkv), a.causal = causal, a.scale = scale;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return head_dim == 128 ? run_fwd<128>(a, s) : head_dim == 64 ? run_fwd<64>(a, s) : run_fwd<32>(a, s);
+}
+
+size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, int64_t n_seqs) {
+    if (T <= 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024 || n_seqs < 0 ||
+        (head_dim != 32 && head_dim != 64 && head_dim != 128))
+        return 0;
+    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs);
+    return p.delta_bytes + p.part_bytes;
+}
+
+int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
+                 const uint16_t* dO, int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, const int32_t* cu_seqlens,
+                 int64_t n_seqs, int causal, float scale, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* ws,
+                 size_t ws_bytes, nf4_stream stream) {
+    const char* fn = "nf4_attn_bwd";
+    int st = check_attn(fn, T, hq, hkv, head_dim, cu_seqlens, n_seqs, causal, scale);
+    if (st != NF4_OK) return st;
+    if (T == 0) return NF4_OK;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
+        !aligned16(dk) || !aligned16(dv) || !lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+        return fail(NF4_E_ARG, "%s: tensors must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
+    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs);
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.delta_bytes + p.part_bytes)
+        return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
+                    p.delta_bytes + p.part_bytes, ws_bytes);
+    AttnArgs a{};
+    a.q = q, a.k = k, a.v = v, a.o = o, a.dO = dO, a.lse_in = lse, a.dq = dq, a.dk = dk, a.dv = dv, a.cu = cu_seqlens;
+    a.T = int(T), a.n_seqs = int(n_seqs), a.hq = int(hq), a.hkv = int(hkv), a.causal = causal, a.scale = scale;
+    a.splits = p.splits;
+    a.delta = static_cast<float*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.delta_bytes);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return head_dim == 128 ? run_bwd<128>(a, s) : head_dim == 64 ? run_bwd<64>(a, s) : run_bwd<32>(a, s);
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@ There is no fallback: if the library is missing, importing this module raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -33,6 +34,10 @@ class Nf4Error(RuntimeError):
 
 class HostBlock(C.Structure):
     _fields_ = [("host", C.c_void_p), ("bytes", C.c_size_t)]
+
+
+class GradTensor(C.Structure):
+    _fields_ = [("grad", C.c_void_p), ("out", C.c_void_p), ("count", C.c_int64), ("dtype", C.c_int)]
 
 
 class PoolTiming(C.Structure):
@@ -86,6 +91,16 @@ def _load() -> C.CDLL:
         "nf4_silu_mul_bwd": (i32, [vp, vp, vp, i64, vp, vp, vp]),
         "nf4_repeat_kv_fwd": (i32, [vp, i64, i64, i64, i64, vp, vp]),
         "nf4_repeat_kv_bwd": (i32, [vp, i64, i64, i64, i64, vp, vp]),
+        "nf4_rope": (i32, [vp, vp, i64, i64, i64, i64, vp, vp, C.POINTER(i32), i32, i32, vp, vp, vp]),
+        "nf4_attn_fwd": (i32, [vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, f32, vp, vp, vp]),
+        "nf4_attn_bwd_workspace": (sz, [i64, i64, i64, i64, i64]),
+        "nf4_attn_bwd": (i32, [vp, vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, f32, vp, vp, vp, vp, sz, vp]),
+        "nf4_grad_list_table": (sz, [C.POINTER(GradTensor), i32]),
+        "nf4_grad_list_create": (i32, [C.POINTER(GradTensor), i32, vp, sz, vp, C.POINTER(vp)]),
+        "nf4_grad_list_destroy": (i32, [vp]),
+        "nf4_grad_workspace": (sz, []),
+        "nf4_grad_norm": (i32, [vp, vp, vp, sz, vp]),
+        "nf4_grad_clip": (i32, [vp, f32, vp, vp, sz, vp]),
         "stream_pool_create": (i32, [C.POINTER(HostBlock), i32, vp, sz, i32, vp, C.POINTER(vp)]),
         "stream_pool_prefetch": (i32, [vp, i32]),
         "stream_pool_acquire": (i32, [vp, i32, vp, C.POINTER(vp)]),
@@ -485,6 +500,170 @@ def repeat_kv_bwd(da, kv: int, head_dim: int, out=None, stream=None):
     _need(out, "out", torch.bfloat16, (t, kv))
     _check(_lib.nf4_repeat_kv_bwd(_ptr(da), t, q, kv, head_dim, _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- decoder layer: positions, attention, clipping
+
+@contextlib.contextmanager
+def _on(*tensors):
+    """The tensors' device made the current one for the enclosed call (all must share it)."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.index == torch.cuda.current_device():
+        yield
+        return
+    with torch.cuda.device(dev):
+        yield
+
+
+def rope_inv_freq(head_dim: int, theta: float = 1e6, device="cuda") -> torch.Tensor:
+    """theta^(-2i/head_dim), i < head_dim/2, fp64: the frequencies of plain rotary positions."""
+    return float(theta) ** (-torch.arange(0, head_dim, 2, dtype=torch.float64, device=device) / head_dim)
+
+
+def rope(q, k, head_dim: int, pos, inv_freq, sections=None, inverse: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [T, hq * head_dim] and k [T, hkv * head_dim] (bf16; k may be None)
+    at the int32 positions pos [n_axes, T] (or [T]); sections: pairs of each axis (default: all
+    on one). inverse=True is the backward. Outputs may be the inputs. Returns (q_out, k_out)."""
+    t = q.shape[0]
+    if pos.dim() == 1:
+        pos = pos.unsqueeze(0)
+    sections = (head_dim // 2,) if sections is None else tuple(sections)
+    hq, hkv = _head_count(q, "q", head_dim), 0 if k is None else _head_count(k, "k", head_dim)
+    q_out = torch.empty_like(q) if q_out is None else q_out
+    k_out = torch.empty_like(k) if k is not None and k_out is None else k_out
+    for name, x, like in (("q", q, q), ("q_out", q_out, q)) + ((("k", k, k), ("k_out", k_out, k)) if hkv else ()):
+        _need(x, name, torch.bfloat16, (t, like.shape[1]))
+    _need(pos, "pos", torch.int32, (len(sections), t))
+    _need(inv_freq, "inv_freq", torch.float64, (head_dim // 2,))
+    arr = (C.c_int * len(sections))(*[int(v) for v in sections])
+    with _on(q, q_out, pos, inv_freq, *((k, k_out) if hkv else ())):
+        _check(_lib.nf4_rope(_ptr(q), _ptr(k), t, hq, hkv, head_dim, _ptr(pos), _ptr(inv_freq), arr, len(sections),
+                             int(bool(inverse)), _ptr(q_out), _ptr(k_out), _stream(stream)))
+    return q_out, k_out
+
+
+def _head_count(x, name: str, head_dim: int) -> int:
+    if x.dim() != 2 or head_dim < 1 or x.shape[1] % head_dim:
+        raise ValueError(f"{name} must be [T, heads * {head_dim}], got {tuple(x.shape)}")
+    return x.shape[1] // head_dim
+
+
+def _attn_args(q, k, v, head_dim, cu_seqlens, scale):
+    t = q.shape[0]
+    hq, hkv = _head_count(q, "q", head_dim), _head_count(k, "k", head_dim)
+    _need(q, "q", torch.bfloat16, (t, hq * head_dim))
+    _need(k, "k", torch.bfloat16, (t, hkv * head_dim))
+    _need(v, "v", torch.bfloat16, (t, hkv * head_dim))
+    n_seqs = 0
+    if cu_seqlens is not None:
+        n_seqs = cu_seqlens.numel() - 1
+        _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seqs + 1,))
+    return t, hq, hkv, n_seqs, head_dim ** -0.5 if scale is None else float(scale)
+
+
+def attn_bwd_workspace_bytes(T: int, hq: int, hkv: int, head_dim: int, n_seqs: int = 0) -> int:
+    return int(_lib.nf4_attn_bwd_workspace(T, hq, hkv, head_dim, n_seqs))
+
+
+def attn_fwd(q, k, v, head_dim: int, cu_seqlens=None, causal: bool = True, scale=None, o=None, lse=None, stream=None):
+    """Softmax attention of q [T, hq * head_dim] over k, v [T, hkv * head_dim] (bf16), within the
+    sequences cu_seqlens (int32 [n + 1]; None: one sequence). Returns (o like q, lse fp32 [hq, T]);
+    rows outside every sequence are not written."""
+    t, hq, hkv, n_seqs, scale = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((hq, t), dtype=torch.float32, device=q.device) if lse is None else lse
+    _need(o, "o", torch.bfloat16, (t, hq * head_dim))
+    _need(lse, "lse", torch.float32, (hq, t))
+    with _on(q, k, v, o, lse, *(() if cu_seqlens is None else (cu_seqlens,))):
+        _check(_lib.nf4_attn_fwd(_ptr(q), _ptr(k), _ptr(v), t, hq, hkv, head_dim, _ptr(cu_seqlens), n_seqs,
+                                 int(bool(causal)), scale, _ptr(o), _ptr(lse), _stream(stream)))
+    return o, lse
+
+
+def attn_bwd(q, k, v, o, lse, do, head_dim: int, cu_seqlens=None, causal: bool = True, scale=None, dq=None, dk=None,
+             dv=None, ws=None, stream=None):
+    """Backward of attn_fwd from its o and lse: returns (dq, dk, dv)."""
+    t, hq, hkv, n_seqs, scale = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for name, x, heads in (("o", o, hq), ("do", do, hq), ("dq", dq, hq), ("dk", dk, hkv), ("dv", dv, hkv)):
+        _need(x, name, torch.bfloat16, (t, heads * head_dim))
+    _need(lse, "lse", torch.float32, (hq, t))
+    if ws is None:
+        ws = workspace(attn_bwd_workspace_bytes(t, hq, hkv, head_dim, n_seqs), q.device)
+    with _on(q, k, v, o, lse, do, dq, dk, dv, ws, *(() if cu_seqlens is None else (cu_seqlens,))):
+        _check(_lib.nf4_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), t, hq, hkv, head_dim,
+                                 _ptr(cu_seqlens), n_seqs, int(bool(causal)), scale, _ptr(dq), _ptr(dk), _ptr(dv),
+                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    return dq, dk, dv
+
+
+class GradList:
+    """A training program's gradient tensors (bf16 or fp32, mixed freely) as one list for the
+    global norm and clipping (nf4_grad_list_*): made once over the buffers, used every step.
+    outs: where the scaled gradients go (default: in place). The tensors are kept alive."""
+
+    def __init__(self, grads, outs=None, stream=None):
+        self._h = None
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if not self.grads:
+            raise ValueError("GradList needs at least one tensor")
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} grads but {len(self.outs)} outs")
+        arr = (GradTensor * len(self.grads))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            dtype = {torch.bfloat16: NF4_DTYPE_BF16, torch.float32: NF4_DTYPE_F32}.get(g.dtype)
+            if dtype is None:
+                raise TypeError(f"grads[{i}] must be bfloat16 or float32, got {g.dtype}")
+            _need(g, f"grads[{i}]", g.dtype, tuple(g.shape))
+            if o is not g:
+                _need(o, f"outs[{i}]", g.dtype, tuple(g.shape))
+            arr[i] = GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), dtype)
+        self.device = self.grads[0].device
+        nbytes = int(_lib.nf4_grad_list_table(arr, len(self.grads)))
+        if not nbytes:
+            raise Nf4Error(NF4_E_ARG, last_error())
+        h = C.c_void_p()
+        with _on(*self.grads, *self.outs):
+            self._table = workspace(nbytes, self.device)
+            _check(_lib.nf4_grad_list_create(arr, len(self.grads), _ptr(self._table), self._table.numel(),
+                                             _stream(stream), C.byref(h)))
+        self._h = h
+        self._ws_bytes = int(_lib.nf4_grad_workspace())
+
+    def _run(self, call, norm, ws, stream, *args):
+        if self._h is None:
+            raise Nf4Error(NF4_E_STATE, "the gradient list is closed")
+        norm = torch.empty(1, dtype=torch.float32, device=self.device) if norm is None else norm
+        _need(norm, "norm", torch.float32, (1,))
+        ws = workspace(self._ws_bytes, self.device) if ws is None else ws
+        with _on(norm, ws, self._table):
+            _check(call(self._h, *args, _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        return norm
+
+    def norm(self, norm=None, ws=None, stream=None):
+        """The global norm, fp32 [1] on the device; the gradients are only read."""
+        return self._run(_lib.nf4_grad_norm, norm, ws, stream)
+
+    def clip(self, max_norm: float, norm=None, ws=None, stream=None):
+        """outs = grads * min(1, max_norm / (norm + 1e-6)); returns the norm before clipping."""
+        return self._run(_lib.nf4_grad_clip, norm, ws, stream, float(max_norm))
+
+    def close(self) -> None:
+        if getattr(self, "_h", None):
+            _check(_lib.nf4_grad_list_destroy(self._h))
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 def block_layout(shapes, layers: int, dense: bool = False):

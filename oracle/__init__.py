@@ -11,3 +11,4 @@ Pinning status of every function is listed in the module header of
 """
 
 from .nf4_oracle import *  # noqa: F401,F403
+from .decoder_oracle import *  # noqa: F401,F403

@@ -1,0 +1,125 @@
+"""Host-side argument checks of the decoder operators' C ABI, without a GPU: every call
+fails (or is a no-op) before anything reaches the device."""
+
+import ctypes as C
+
+import pytest
+
+FAKE = C.c_void_p(0x10000)      # aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    from nf4_weight_streamed_amd import lib
+
+    return lib
+
+
+def _err(L, rc, code, needle):
+    assert rc == code and needle in L.last_error(), (rc, L.last_error())
+
+
+def _fwd(L, q=FAKE, T=4, hq=4, hkv=2, D=64, cu=None, n=0, causal=1, scale=0.125, o=FAKE, lse=FAKE):
+    return L.raw().nf4_attn_fwd(q, FAKE, FAKE, T, hq, hkv, D, cu, n, causal, scale, o, lse, None)
+
+
+def _bwd(L, q=FAKE, T=4, hq=4, hkv=2, D=64, cu=None, n=0, causal=1, scale=0.125, do=FAKE, ws=FAKE, ws_bytes=1 << 40):
+    return L.raw().nf4_attn_bwd(q, FAKE, FAKE, FAKE, FAKE, do, T, hq, hkv, D, cu, n, causal, scale, FAKE, FAKE, FAKE, ws,
+                                ws_bytes, None)
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_attention_validation(L, call):
+    for D in (0, 16, 48, 96, 256):
+        _err(L, call(L, D=D), L.NF4_E_SHAPE, "head_dim")
+    for kw in ({"T": -1}, {"T": (1 << 23) + 1}, {"hq": 5}, {"hkv": 0}, {"hq": 0}, {"hq": 2048}, {"hq": -4, "hkv": -2}):
+        _err(L, call(L, **kw), L.NF4_E_SHAPE, "hkv | hq")
+    for kw in ({"n": 2}, {"n": -1}, {"cu": FAKE, "n": 0}, {"cu": FAKE, "n": (1 << 20) + 1}):
+        _err(L, call(L, **kw), L.NF4_E_SHAPE, "n_seqs")
+    _err(L, call(L, causal=2), L.NF4_E_ARG, "causal")
+    for scale in (0.0, -1.0, float("inf"), float("nan")):
+        _err(L, call(L, scale=scale), L.NF4_E_ARG, "scale")
+    _err(L, call(L, cu=C.c_void_p(0x10002), n=1), L.NF4_E_ARG, "cu_seqlens")
+    _err(L, call(L, q=None), L.NF4_E_ARG, "NULL")
+    _err(L, call(L, q=C.c_void_p(0x10008)), L.NF4_E_ARG, "aligned")
+    assert call(L, T=0, q=None) == 0
+
+
+def test_attention_output_and_workspace_validation(L):
+    _err(L, _fwd(L, o=None), L.NF4_E_ARG, "NULL")
+    _err(L, _fwd(L, lse=None), L.NF4_E_ARG, "lse")
+    _err(L, _bwd(L, do=C.c_void_p(0x10002)), L.NF4_E_ARG, "aligned")
+    need = L.attn_bwd_workspace_bytes(512, 28, 4, 128)
+    assert need >= 512 * 28 * 4 and need % 256 == 0
+    _err(L, _bwd(L, T=512, hq=28, hkv=4, D=128, ws_bytes=need - 1), L.NF4_E_ARG, str(need))
+    _err(L, _bwd(L, ws=None), L.NF4_E_ARG, "workspace")
+    _err(L, _bwd(L, ws=C.c_void_p(0x10010)), L.NF4_E_ARG, "256-byte")
+    assert L.attn_bwd_workspace_bytes(512, 28, 4, 100) == 0 and L.attn_bwd_workspace_bytes(0, 4, 4, 64) == 0
+    assert L.attn_bwd_workspace_bytes(512, 5, 2, 64) == 0
+
+
+def _rope(L, q=FAKE, k=FAKE, T=4, hq=4, hkv=2, D=64, pos=FAKE, inv=FAKE, sections=(32,), n=None, inverse=0, out=FAKE):
+    arr = None if sections is None else (C.c_int * max(1, len(sections)))(*sections)
+    return L.raw().nf4_rope(q, k, T, hq, hkv, D, pos, inv, arr, len(sections or ()) if n is None else n, inverse, out,
+                            out, None)
+
+
+def test_rope_validation(L):
+    for kw in ({"T": -1}, {"T": (1 << 23) + 1}, {"hq": -1}, {"hkv": 1025}):
+        _err(L, _rope(L, **kw), L.NF4_E_SHAPE, "T")
+    for D in (0, 8, 40, 272):
+        _err(L, _rope(L, D=D), L.NF4_E_SHAPE, "head_dim")
+    _err(L, _rope(L, sections=None, n=1), L.NF4_E_ARG, "sections")
+    _err(L, _rope(L, sections=(8,) * 5), L.NF4_E_ARG, "n_axes=5")
+    _err(L, _rope(L, sections=()), L.NF4_E_ARG, "n_axes=0")
+    _err(L, _rope(L, sections=(33, -1)), L.NF4_E_ARG, "section 1")
+    _err(L, _rope(L, sections=(16, 15)), L.NF4_E_ARG, "31 pairs")
+    _err(L, _rope(L, inverse=2), L.NF4_E_ARG, "inverse")
+    _err(L, _rope(L, k=None), L.NF4_E_ARG, "NULL")
+    _err(L, _rope(L, out=C.c_void_p(0x10008)), L.NF4_E_ARG, "aligned")
+    _err(L, _rope(L, pos=None), L.NF4_E_ARG, "pos")
+    _err(L, _rope(L, inv=C.c_void_p(0x10004)), L.NF4_E_ARG, "inv_freq")
+    assert _rope(L, T=0, q=None) == 0 and _rope(L, hq=0, hkv=0) == 0
+
+
+def _list(L, entries, table=FAKE, table_bytes=1 << 30):
+    arr = (L.GradTensor * max(1, len(entries)))(*[L.GradTensor(*e) for e in entries])
+    h = C.c_void_p()
+    rc = L.raw().nf4_grad_list_create(arr, len(entries), table, table_bytes, None, C.byref(h))
+    return rc, h
+
+
+def test_grad_list_validation(L):
+    f32 = L.NF4_DTYPE_F32
+    ok = (0x20000, 0x20000, 64, f32)
+    for entry, code, needle in (((0x20000, 0x20000, 64, 7), L.NF4_E_ARG, "dtype"),
+                                ((0x20000, 0x20000, -1, f32), L.NF4_E_SHAPE, "count"),
+                                ((0x20000, 0x20000, (1 << 36) + 1, f32), L.NF4_E_SHAPE, "count"),
+                                ((0, 0x20000, 64, f32), L.NF4_E_ARG, "NULL"),
+                                ((0x20002, 0x20002, 64, f32), L.NF4_E_ARG, "aligned"),
+                                ((0x20000, 0x20080, 64, f32), L.NF4_E_ARG, "overlaps"),
+                                ((0x20010, 0x30000, 1, f32), L.NF4_E_ARG, "overlaps"),
+                                ((0x30000, 0x20010, 1, f32), L.NF4_E_ARG, "overlaps"),
+                                (ok, L.NF4_E_ARG, "overlaps")):
+        rc, _ = _list(L, [ok, entry])
+        _err(L, rc, code, needle)
+    _err(L, _list(L, [ok], table=None)[0], L.NF4_E_ARG, "table")
+    _err(L, _list(L, [ok], table_bytes=8)[0], L.NF4_E_ARG, "table")
+    rc = L.raw().nf4_grad_list_create(None, 2, FAKE, 1 << 20, None, C.byref(C.c_void_p()))
+    _err(L, rc, L.NF4_E_ARG, "tensors")
+    rc = L.raw().nf4_grad_list_create(None, 0, FAKE, 1 << 20, None, None)
+    _err(L, rc, L.NF4_E_ARG, "out is NULL")
+
+
+def test_empty_grad_list_and_call_validation(L):
+    rc, h = _list(L, [(None, None, 0, L.NF4_DTYPE_F32)])     # nothing to copy: no device needed
+    assert rc == 0 and h.value
+    raw, ws = L.raw(), L.raw().nf4_grad_workspace()
+    for bad in (-1.0, float("inf"), float("nan")):
+        _err(L, raw.nf4_grad_clip(h, bad, FAKE, FAKE, ws, None), L.NF4_E_ARG, "max_norm")
+    _err(L, raw.nf4_grad_clip(None, 1.0, FAKE, FAKE, ws, None), L.NF4_E_ARG, "NULL list")
+    _err(L, raw.nf4_grad_norm(h, None, FAKE, ws, None), L.NF4_E_ARG, "norm")
+    _err(L, raw.nf4_grad_norm(h, FAKE, FAKE, ws - 1, None), L.NF4_E_ARG, str(ws))
+    _err(L, raw.nf4_grad_norm(h, FAKE, C.c_void_p(0x10010), ws, None), L.NF4_E_ARG, "256-byte")
+    assert raw.nf4_grad_list_destroy(h) == 0
+    _err(L, raw.nf4_grad_list_destroy(None), L.NF4_E_ARG, "NULL list")

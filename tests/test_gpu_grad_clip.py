@@ -1,0 +1,155 @@
+"""The gradients' global norm and clipping through the C ABI against fp64."""
+
+import math
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+def _tensors(sizes, seed=0, std=1.0):
+    """fp32 and bf16 in turn, each cut from a larger buffer at an odd element offset."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    out = []
+    for i, n in enumerate(sizes):
+        dtype = torch.float32 if i % 2 == 0 else torch.bfloat16
+        buf = (torch.randn(n + 16, generator=g, device="cuda") * std).to(dtype)
+        out.append(buf[i % 9:i % 9 + n])
+    return out
+
+
+def _norm64(ts):
+    return math.sqrt(sum(float(t.double().square().sum()) for t in ts))
+
+
+def _ulp(dtype):
+    return torch.finfo(dtype).eps / 2            # half a step, relative
+
+
+SIZES = [[1], [3, 5], [0, 7, 0, 4096], [16384, 32768, 16385, 32769, 16383], [100_003, 999_999, 8, 1_000_001],
+         [33] * 300]
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("in_place", [True, False])
+def test_norm_and_scaling(gpu_lib, sizes, in_place):
+    lib = gpu_lib
+    grads = _tensors(sizes)
+    before = [t.clone() for t in grads]
+    outs = None if in_place else [torch.full_like(t, 9.0) for t in grads]
+    gl = lib.GradList(grads, outs)
+    want = _norm64(before)
+    n = gl.norm()
+    torch.cuda.synchronize()
+    assert abs(n.item() - want) <= 2 * 2.0 ** -24 * want       # fp64 sums; one rounding to fp32
+    assert all(torch.equal(a, b) for a, b in zip(grads, before))
+    for max_norm in (2 * want + 1.0, 0.37 * want, 0.0):
+        for t, b in zip(grads, before):
+            t.copy_(b)
+        n = gl.clip(max_norm)
+        torch.cuda.synchronize()
+        assert abs(n.item() - want) <= 2 * 2.0 ** -24 * want
+        f = min(1.0, max_norm / (want + 1e-6))
+        for b, t, o in zip(before, grads, gl.outs):
+            exact = b.double() * f
+            # the factor rounded to fp32, the product, and the product's rounding to the type
+            lim = exact.abs() * (3 * 2.0 ** -24 + _ulp(b.dtype)) + 1e-44
+            assert torch.all((o.double() - exact).abs() <= lim)
+            if f == 1.0:
+                assert torch.equal(o, b)
+            if not in_place:
+                assert torch.equal(t, b)
+    gl.close()
+
+
+def test_stack_sized_list_of_one_type(gpu_lib):
+    """1120 aligned fp32 tensors (the adapters of 80 layers), more pieces than shares."""
+    lib = gpu_lib
+    flat = torch.randn(80 * 14 * 120_000, device="cuda")
+    gl = lib.GradList(list(flat.split(120_000)), list(torch.empty_like(flat).split(120_000)))
+    n = gl.clip(1.0)
+    want = _norm64([flat])
+    assert abs(n.item() - want) <= 2 * 2.0 ** -24 * want
+    got = torch.cat(gl.outs)
+    assert torch.all((got.double() - flat.double() / (want + 1e-6)).abs() <= 4 * 2.0 ** -24 * flat.double().abs() + 1e-44)
+
+
+def test_huge_tiny_and_non_finite_values(gpu_lib):
+    lib = gpu_lib
+    for v in (1e30, 1e-30):                       # squares outside fp32
+        t = torch.full((1000,), v, device="cuda")
+        gl = lib.GradList([t])
+        assert gl.norm().item() == pytest.approx(_norm64([t]), rel=1e-6)
+    big = torch.full((4,), 3e38, device="cuda")   # the norm itself is past fp32
+    gl = lib.GradList([big])
+    assert math.isinf(gl.clip(1.0).item())
+    assert big[0].item() == pytest.approx(0.5, rel=1e-6)
+    for bad in (float("inf"), float("nan")):
+        t = torch.ones(100, device="cuda")
+        t[7] = bad
+        o = torch.zeros_like(t)
+        n = lib.GradList([t], [o]).clip(1.0)
+        assert not math.isfinite(n.item())
+        assert torch.equal(o.isnan(), t.isnan()) and torch.equal(o.nan_to_num(), t.nan_to_num())
+    z = torch.zeros(100, device="cuda")
+    gl = lib.GradList([z])
+    assert gl.clip(1.0).item() == 0.0 and not z.any()
+    assert lib.GradList([torch.empty(0, device="cuda")]).clip(1.0).item() == 0.0
+
+
+def test_same_bits_again_on_another_stream_and_in_graphs(gpu_lib):
+    lib = gpu_lib
+    grads = _tensors([50_001, 70_000, 33, 16_384], seed=3)
+    outs = [torch.empty_like(t) for t in grads]
+    gl = lib.GradList(grads, outs)
+    ref_n = gl.clip(1.5).clone()
+    ref = [o.clone() for o in outs]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    n = gl.clip(1.5, stream=side)
+    side.synchronize()
+    assert torch.equal(n, ref_n) and all(torch.equal(a, b) for a, b in zip(outs, ref))
+    norm, ws = torch.empty(1, device="cuda"), lib.workspace(gl._ws_bytes)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gl.clip(1.5, norm=norm, ws=ws)
+    for rep in range(3):
+        grads[0].mul_(1.25)
+        ref_n = gl.clip(1.5).clone()
+        ref = [o.clone() for o in outs]
+        ws.fill_(0xFF)
+        for o in outs:
+            o.fill_(rep)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(norm, ref_n) and all(torch.equal(a, b) for a, b in zip(outs, ref)), rep
+
+
+def test_python_refusals(gpu_lib):
+    lib = gpu_lib
+    a, b = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    with pytest.raises(ValueError, match="at least one"):
+        lib.GradList([])
+    with pytest.raises(ValueError, match="outs"):
+        lib.GradList([a, b], [a])
+    with pytest.raises(TypeError, match="bfloat16 or float32"):
+        lib.GradList([a.half()])
+    with pytest.raises(ValueError, match="contiguous"):
+        lib.GradList([torch.zeros(8, 8, device="cuda").t()])
+    with pytest.raises(lib.Nf4Error, match="overlaps"):
+        lib.GradList([a, b, a])
+    with pytest.raises(lib.Nf4Error, match="overlaps"):
+        lib.GradList([a[:32]], [a[16:48]])
+    with pytest.raises(lib.Nf4Error, match="overlaps"):
+        lib.GradList([a, b], [b, torch.empty_like(b)])
+    gl = lib.GradList([a, b])
+    for bad in (-1.0, float("nan"), float("inf")):
+        with pytest.raises(lib.Nf4Error, match="max_norm"):
+            gl.clip(bad)
+    with pytest.raises(lib.Nf4Error, match="workspace"):
+        gl.clip(1.0, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    gl.close()
+    with pytest.raises(lib.Nf4Error, match="closed"):
+        gl.norm()
