@@ -31,7 +31,9 @@ calls, owns buffers (torch allocations) and the two streams.
 Layer (attention mixing replaced by the identity): h_a = RMSNorm(h);
 q, k, v = L_q/L_k/L_v(h_a); a = repeat_kv(v); h' = h + L_o(a); h_m = RMSNorm(h');
 h'' = h' + L_down(SiLU(L_gate(h_m)) * L_up(h_m)). q and k are computed and
-receive a zero gradient.
+receive a zero gradient. With mixing="attention" the layer is a whole decoder layer:
+a = attention(rope(q), rope(k), v), causal within each of the batch's packed sequences
+(seq_lens), and every projection receives its gradient.
 """
 
 from __future__ import annotations
@@ -258,9 +260,17 @@ class NF4Stack:
 
     def __init__(self, base: HostNF4Base, lora: LoraParams, tokens: int, alpha: float = 32.0,
                  mode: str = "streamed", n_slots: int = 2, prefetch: bool = True, remat: bool = False,
-                 layer_parts: bool = True, max_ahead: int = 2):
+                 layer_parts: bool = True, max_ahead: int = 2, mixing: str = "identity", seq_lens=None,
+                 rope_theta: float = 1e6):
         if mode not in ("streamed", "resident"):
             raise ValueError("mode must be 'streamed' or 'resident'")
+        if mixing not in ("identity", "attention"):
+            raise ValueError("mixing must be 'identity' or 'attention'")
+        if seq_lens is not None and mixing == "identity":
+            raise ValueError("seq_lens needs mixing='attention'")
+        if seq_lens is not None and (sum(seq_lens) != tokens or not seq_lens or min(seq_lens) < 0):
+            raise ValueError(f"seq_lens must be non-negative and add up to {tokens} tokens")
+        self.mixing = mixing
         self.base, self.lora, self.T, self.alpha = base, lora, tokens, alpha
         self.mode, self.prefetch, self.remat = mode, prefetch, remat
         # layer_parts: each layer of a block is a part of its own (copied separately,
@@ -316,6 +326,9 @@ class NF4Stack:
                 "rs_h1": torch.empty(T, dtype=torch.float32, device=dev),
                 "u": {name: torch.empty(T, r, dtype=torch.float32, device=dev) for name in PROJS},
             })
+            if mixing == "attention":    # rotated q and k, and the softmax statistics, for the backward
+                a.update({"q": torch.empty(T, d.q, **bf), "k": torch.empty(T, d.kv, **bf),
+                          "lse": torch.empty(d.q // d.head_dim, T, dtype=torch.float32, device=dev)})
         # scratch reused by every layer (stream order makes reuse safe)
         self.tmp = {
             "q": torch.empty(T, d.q, **bf), "k": torch.empty(T, d.kv, **bf), "o": torch.empty(T, d.hidden, **bf),
@@ -328,6 +341,18 @@ class NF4Stack:
             "dha_k": torch.empty(T, d.hidden, **bf), "dha": torch.empty(T, d.hidden, **bf),
             "zq": torch.zeros(T, d.q, **bf), "zkv": torch.zeros(T, d.kv, **bf),
         }
+        self.seqs = {"cu": None, "n": 0}
+        if mixing == "attention":
+            lens = [T] if seq_lens is None else [int(n) for n in seq_lens]
+            self.inv_freq = lib.rope_inv_freq(d.head_dim, rope_theta)
+            self.pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]).to(dev)   # restart in each sequence
+            if seq_lens is not None:
+                ends = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+                self.seqs = {"cu": ends.to(dev), "n": len(lens)}
+            self.ws_a = lib.workspace(lib.attn_bwd_workspace_bytes(T, d.q // d.head_dim, d.kv // d.head_dim, d.head_dim,
+                                                                   self.seqs["n"]))
+            self.tmp.update({"dq": torch.empty(T, d.q, **bf), "dk": torch.empty(T, d.kv, **bf)})
+        self._grad_list = None
         self.dh = [torch.empty(T, d.hidden, **bf) for _ in range(2)]
         self.grads = [{name: (torch.empty(r, shapes[name][1], dtype=torch.float32, device=dev),
                               torch.empty(shapes[name][0], r, dtype=torch.float32, device=dev)) for name in PROJS}
@@ -416,11 +441,17 @@ class NF4Stack:
     def _layer_forward(self, li: int, w):
         d, A, t = self.dims, self._act(li), self.tmp
         self._layer = li
+        attention = self.mixing == "attention"
+        q, k = (A["q"], A["k"]) if attention else (t["q"], t["k"])
         lib.rmsnorm_fwd(A["h"], RMS_EPS, out=A["ha"], rstd=A["rs_h"])
-        self._fwd(w, "q", A["ha"], t["q"], A["u"]["q"])
-        self._fwd(w, "k", A["ha"], t["k"], A["u"]["k"])
+        self._fwd(w, "q", A["ha"], q, A["u"]["q"])
+        self._fwd(w, "k", A["ha"], k, A["u"]["k"])
         self._fwd(w, "v", A["ha"], A["v"], A["u"]["v"])
-        lib.repeat_kv_fwd(A["v"], d.q, d.head_dim, out=A["a"])
+        if attention:
+            lib.rope(q, k, d.head_dim, self.pos, self.inv_freq, q_out=q, k_out=k)
+            lib.attn_fwd(q, k, A["v"], d.head_dim, self.seqs["cu"], o=A["a"], lse=A["lse"])
+        else:
+            lib.repeat_kv_fwd(A["v"], d.q, d.head_dim, out=A["a"])
         self._fwd(w, "o", A["a"], t["o"], A["u"]["o"])
         lib.add_bf16(A["h"], t["o"], out=A["h1"])
         lib.rmsnorm_fwd(A["h1"], RMS_EPS, out=A["hm"], rstd=A["rs_h1"])
@@ -440,10 +471,17 @@ class NF4Stack:
         lib.add_bf16(t["dhm_g"], t["dhm_u"], out=t["dhm"])
         lib.rmsnorm_bwd(A["h1"], A["rs_h1"], t["dhm"], dres=dh_out, out=t["dh1"])
         self._bwd(w, "o", A["a"], A["u"]["o"], t["dh1"], t["da"])
-        lib.repeat_kv_bwd(t["da"], d.kv, d.head_dim, out=t["dv"])
+        if self.mixing == "attention":
+            dq, dk = t["dq"], t["dk"]
+            lib.attn_bwd(A["q"], A["k"], A["v"], A["a"], A["lse"], t["da"], d.head_dim, self.seqs["cu"], dq=dq, dk=dk,
+                         dv=t["dv"], ws=self.ws_a)
+            lib.rope(dq, dk, d.head_dim, self.pos, self.inv_freq, inverse=True, q_out=dq, k_out=dk)
+        else:
+            lib.repeat_kv_bwd(t["da"], d.kv, d.head_dim, out=t["dv"])
+            dq, dk = t["zq"], t["zkv"]                                    # identity mixing: zero gradient
         self._bwd(w, "v", A["ha"], A["u"]["v"], t["dv"], t["dha_v"])
-        self._bwd(w, "q", A["ha"], A["u"]["q"], t["zq"], t["dha_q"])      # identity mixing: zero gradient
-        self._bwd(w, "k", A["ha"], A["u"]["k"], t["zkv"], t["dha_k"])
+        self._bwd(w, "q", A["ha"], A["u"]["q"], dq, t["dha_q"])
+        self._bwd(w, "k", A["ha"], A["u"]["k"], dk, t["dha_k"])
         lib.add_bf16(t["dha_v"], t["dha_q"], t["dha_k"], out=t["dha"])
         lib.rmsnorm_bwd(A["h"], A["rs_h"], t["dha"], dres=t["dh1"], out=dh_in)
 
@@ -521,6 +559,15 @@ class NF4Stack:
                 cur, k = nxt, 1 - k
             self.pool.release(b)
         return cur
+
+    def clip_grads(self, max_norm: float) -> torch.Tensor:
+        """Scale every adapter gradient of the last backward in place by
+        min(1, max_norm / (norm + 1e-6)); returns their global norm before that (fp32 [1],
+        on the device)."""
+        with self._on_compute():
+            if self._grad_list is None:
+                self._grad_list = lib.GradList([t for layer in self.grads for name in PROJS for t in layer[name]])
+            return self._grad_list.clip(max_norm)
 
     def step(self, h0, dh):
         out = self.forward(h0)
