@@ -198,6 +198,34 @@ struct TileCopy {
     }
 };
 
+// Tiles [j0, j1) through two pairs of LDS buffers: tile j + 1 is copied while tile j is
+// used. Tile j0 has been issued to (a0, b0) by the caller. The four buffers have to be
+// __shared__ variables of their own: the compiler then knows that a read of one does not
+// depend on the outstanding copies to the others, and does not wait for them.
+template <typename Stage, typename Compute, typename Arrive>
+__device__ __forceinline__ void double_buffered(int j0, int j1, char* a0, char* b0, char* a1, char* b1, Stage&& stage,
+                                                Compute&& compute, Arrive&& arrive) {
+    for (int j = j0; j < j1; ++j) {
+        arrive(j);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (j + 1 < j1) stage(j + 1, a1, b1);
+        compute(j, a0, b0);
+        if (++j >= j1) break;
+        arrive(j);
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (j + 1 < j1) stage(j + 1, a0, b0);
+        compute(j, a1, b1);
+    }
+}
+
+template <typename Stage, typename Compute>
+__device__ __forceinline__ void double_buffered(int j0, int j1, char* a0, char* b0, char* a1, char* b1, Stage&& stage,
+                                                Compute&& compute) {
+    double_buffered(j0, j1, a0, b0, a1, b1, stage, compute, [](int) {});
+}
+
 // ------------------------------------------------------------------ forward
 
 // One workgroup: W waves x 32 queries of one head; K and V in tiles of 64 keys, double
@@ -207,8 +235,8 @@ struct TileCopy {
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
     constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sK[2][kTile * 2 * D];
-    __shared__ __align__(1024) char sV[2][kTile * 2 * D];
+    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D];
+    __shared__ __align__(1024) char sK1[kTile * 2 * D], sV1[kTile * 2 * D];
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
@@ -246,15 +274,10 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
         copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
         copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
     };
-    stage(0, sK[0], sV[0]);
-    for (int j = 0; j < n; ++j) {
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (j + 1 < n) stage(j + 1, sK[(j + 1) & 1], sV[(j + 1) & 1]);
+    stage(0, sK0, sV0);
+    auto compute = [&](int j, const char* k, const char* v) {
         const int k0 = j * kTile;
-        if (a.causal && k0 > q_lo + 31) continue;  // nothing of this tile for the wave's rows
-        const char* k = sK[j & 1];
-        const char* v = sV[j & 1];
+        if (a.causal && k0 > q_lo + 31) return;  // nothing of this tile for the wave's rows
         f32x16 s[2] = {zero16(), zero16()};
 #pragma unroll
         for (int i = 0; i < KS; ++i)
@@ -300,7 +323,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
                 acc[nb] = mfma32x32x16(lds_frag_tr(v + g * 32 * D + map.tr[nb][0], v + g * 32 * D + map.tr[nb][1]), p,
                                        acc[nb]);
         }
-    }
+    };
+    double_buffered(0, n, sK0, sV0, sK1, sV1, stage, compute);
     l = sum_halves(l);
     if (q_row < t.len) {
         const size_t row = size_t(t.begin) + q_row;
@@ -325,8 +349,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
     constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sK[2][kTile * 2 * D];
-    __shared__ __align__(1024) char sV[2][kTile * 2 * D];
+    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D];
+    __shared__ __align__(1024) char sK1[kTile * 2 * D], sV1[kTile * 2 * D];
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
@@ -345,7 +369,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
         copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
         copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
     };
-    stage(0, sK[0], sV[0]);
+    stage(0, sK0, sV0);
 
     bf16x8 qf[KS], df[KS];
     float delta = 0.0f;
@@ -379,14 +403,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
     const int q_lo = t.row0 + 32 * wave;
     const int keys = a.causal ? min(t.len, t.row0 + BM) : t.len;
     const int n = (keys + kTile - 1) / kTile;
-    for (int j = 0; j < n; ++j) {
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (j + 1 < n) stage(j + 1, sK[(j + 1) & 1], sV[(j + 1) & 1]);
+    auto compute = [&](int j, const char* k, const char* v) {
         const int k0 = j * kTile;
-        if (a.causal && k0 > q_lo + 31) continue;
-        const char* k = sK[j & 1];
-        const char* v = sV[j & 1];
+        if (a.causal && k0 > q_lo + 31) return;
         const bool edge = k0 + kTile > t.len || (a.causal && k0 + kTile - 1 > q_lo);
         const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
 #pragma unroll
@@ -414,7 +433,8 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
                     acc[nb] = mfma32x32x16(lds_frag_tr(kg + map.tr[nb][0], kg + map.tr[nb][1]), ds, acc[nb]);
             }
         }
-    }
+    };
+    double_buffered(0, n, sK0, sV0, sK1, sV1, stage, compute);
     if (q_row < t.len) {
         uint16_t* out = a.dq + (size_t(t.begin) + q_row) * ldq + head * D;
 #pragma unroll
@@ -437,9 +457,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
     constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sQ[2][kTile * 2 * D];
-    __shared__ __align__(1024) char sD[2][kTile * 2 * D];
-    __shared__ __align__(16) float sL[2][2][kTile];  // [buffer][lse * log2 e, delta]
+    __shared__ __align__(1024) char sQ0[kTile * 2 * D], sD0[kTile * 2 * D];
+    __shared__ __align__(1024) char sQ1[kTile * 2 * D], sD1[kTile * 2 * D];
+    __shared__ __align__(16) float sL[2][2][kTile];  // [tile parity][lse * log2 e, delta]
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * a.splits, kvh, item)) return;
@@ -473,42 +493,38 @@ __global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
     const LdsMap<D> map(lane);
     const TileCopy<D, W> copy(wave, lane, ldq);
     float stat = 0.0f;  // this thread's lse or delta of the tile being staged
-    auto stage = [&](int i, int buf) {
+    auto stage = [&](int i, char* q, char* d) {
         const int head = kvh * G + i / nq, q0 = (tile_lo + i % nq) * kTile;
         const size_t at = (size_t(t.begin) + q0) * ldq + head * D;
-        copy.issue(a.q + at, t.len - q0, ldq, sQ[buf], wave);
-        copy.issue(a.dO + at, t.len - q0, ldq, sD[buf], wave);
+        copy.issue(a.q + at, t.len - q0, ldq, q, wave);
+        copy.issue(a.dO + at, t.len - q0, ldq, d, wave);
         if (threadIdx.x < 2 * kTile) {
             const int r = threadIdx.x & (kTile - 1), which = threadIdx.x / kTile;
             // rows past the sequence: lse = +inf makes their P zero
             stat = which ? 0.0f : INFINITY;
             if (q0 + r < t.len) {
                 const size_t s = size_t(head) * a.T + t.begin + q0 + r;
-                stat = which ? a.delta[s] : a.lse_in[s] * kLog2e;
+                stat = which ? a.delta[s] : a.lse_in[s];  // first used behind the tile's wait
             }
         }
     };
-    auto put_stat = [&](int buf) {
-        if (threadIdx.x < 2 * kTile) sL[buf][threadIdx.x / kTile][threadIdx.x & (kTile - 1)] = stat;
+    auto put_stat = [&](int i) {
+        if (threadIdx.x < 2 * kTile) sL[i & 1][threadIdx.x / kTile][threadIdx.x & (kTile - 1)] = threadIdx.x < kTile ? stat * kLog2e : stat;
     };
 
     f32x16 dk[NB], dv[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) dk[nb] = zero16(), dv[nb] = zero16();
-    if (i0 < i1) stage(i0, 0);
-    for (int i = i0; i < i1; ++i) {
-        const int buf = (i - i0) & 1;
-        put_stat(buf);
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (i + 1 < i1) stage(i + 1, buf ^ 1);
+    if (i0 < i1) stage(i0, sQ0, sD0);
+    auto compute = [&](int i, const char* sq, const char* sd) {
+        const int buf = i & 1;
         const int q0 = (tile_lo + i % nq) * kTile;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int qb = q0 + 32 * b;
             if (a.causal && qb + 31 < k_lo) continue;
-            const char* q = sQ[buf] + b * 64 * D;
-            const char* d = sD[buf] + b * 64 * D;
+            const char* q = sq + b * 64 * D;
+            const char* d = sd + b * 64 * D;
             f32x16 s = zero16(), dp = zero16();
 #pragma unroll
             for (int e = 0; e < KS; ++e) {
@@ -542,7 +558,8 @@ __global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
                 }
             }
         }
-    }
+    };
+    double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute, put_stat);
     if (key >= t.len) return;
     const size_t row = size_t(t.begin) + key;
     if (a.splits == 1) {
