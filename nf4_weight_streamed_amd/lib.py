@@ -8,7 +8,6 @@ There is no fallback: if the library is missing, importing this module raises.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -157,6 +156,9 @@ def _ptr(t) -> C.c_void_p | None:
 
 
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> None:
+    # one test for the usual case (0.3 us against 0.6): small calls cost less than their checks
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
@@ -504,18 +506,25 @@ def repeat_kv_bwd(da, kv: int, head_dim: int, out=None, stream=None):
 
 # ---------------------------------------------------------------- decoder layer: positions, attention, clipping
 
-@contextlib.contextmanager
-def _on(*tensors):
-    """The tensors' device made the current one for the enclosed call (all must share it)."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.index == torch.cuda.current_device():
-        yield
-        return
-    with torch.cuda.device(dev):
-        yield
+def _device(t, *more) -> int:
+    """The index of the tensors' device, which all must share."""
+    dev = t.get_device()
+    for x in more:
+        if x is not None and x.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {x.device}")
+    return dev
+
+
+def _enqueue(dev: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current, on its current stream by default."""
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _enqueue(dev, stream, fn, *args)
+    if stream is None:
+        raw_stream = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        raw_stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    _check(fn(*args, raw_stream))
 
 
 def rope_inv_freq(head_dim: int, theta: float = 1e6, device="cuda") -> torch.Tensor:
@@ -533,15 +542,18 @@ def rope(q, k, head_dim: int, pos, inv_freq, sections=None, inverse: bool = Fals
     sections = (head_dim // 2,) if sections is None else tuple(sections)
     hq, hkv = _head_count(q, "q", head_dim), 0 if k is None else _head_count(k, "k", head_dim)
     q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = torch.empty_like(k) if k is not None and k_out is None else k_out
-    for name, x, like in (("q", q, q), ("q_out", q_out, q)) + ((("k", k, k), ("k_out", k_out, k)) if hkv else ()):
-        _need(x, name, torch.bfloat16, (t, like.shape[1]))
+    k_out = None if k is None else torch.empty_like(k) if k_out is None else k_out
+    _need(q, "q", torch.bfloat16, (t, hq * head_dim))
+    _need(q_out, "q_out", torch.bfloat16, (t, hq * head_dim))
+    if k is not None:
+        _need(k, "k", torch.bfloat16, (t, hkv * head_dim))
+        _need(k_out, "k_out", torch.bfloat16, (t, hkv * head_dim))
     _need(pos, "pos", torch.int32, (len(sections), t))
     _need(inv_freq, "inv_freq", torch.float64, (head_dim // 2,))
-    arr = (C.c_int * len(sections))(*[int(v) for v in sections])
-    with _on(q, q_out, pos, inv_freq, *((k, k_out) if hkv else ())):
-        _check(_lib.nf4_rope(_ptr(q), _ptr(k), t, hq, hkv, head_dim, _ptr(pos), _ptr(inv_freq), arr, len(sections),
-                             int(bool(inverse)), _ptr(q_out), _ptr(k_out), _stream(stream)))
+    arr = (C.c_int * len(sections))(*sections)
+    _enqueue(_device(q, q_out, pos, inv_freq, k, k_out), stream, _lib.nf4_rope, q.data_ptr(),
+             None if k is None else k.data_ptr(), t, hq, hkv, head_dim, pos.data_ptr(), inv_freq.data_ptr(), arr,
+             len(sections), int(bool(inverse)), q_out.data_ptr(), None if k is None else k_out.data_ptr())
     return q_out, k_out
 
 
@@ -577,9 +589,9 @@ def attn_fwd(q, k, v, head_dim: int, cu_seqlens=None, causal: bool = True, scale
     lse = torch.empty((hq, t), dtype=torch.float32, device=q.device) if lse is None else lse
     _need(o, "o", torch.bfloat16, (t, hq * head_dim))
     _need(lse, "lse", torch.float32, (hq, t))
-    with _on(q, k, v, o, lse, *(() if cu_seqlens is None else (cu_seqlens,))):
-        _check(_lib.nf4_attn_fwd(_ptr(q), _ptr(k), _ptr(v), t, hq, hkv, head_dim, _ptr(cu_seqlens), n_seqs,
-                                 int(bool(causal)), scale, _ptr(o), _ptr(lse), _stream(stream)))
+    _enqueue(_device(q, k, v, o, lse, cu_seqlens), stream, _lib.nf4_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), t,
+             hq, hkv, head_dim, None if cu_seqlens is None else cu_seqlens.data_ptr(), n_seqs, int(bool(causal)), scale,
+             o.data_ptr(), lse.data_ptr())
     return o, lse
 
 
@@ -590,15 +602,19 @@ def attn_bwd(q, k, v, o, lse, do, head_dim: int, cu_seqlens=None, causal: bool =
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    for name, x, heads in (("o", o, hq), ("do", do, hq), ("dq", dq, hq), ("dk", dk, hkv), ("dv", dv, hkv)):
-        _need(x, name, torch.bfloat16, (t, heads * head_dim))
+    q_shape, k_shape = (t, hq * head_dim), (t, hkv * head_dim)
+    _need(o, "o", torch.bfloat16, q_shape)
+    _need(do, "do", torch.bfloat16, q_shape)
     _need(lse, "lse", torch.float32, (hq, t))
+    _need(dq, "dq", torch.bfloat16, q_shape)
+    _need(dk, "dk", torch.bfloat16, k_shape)
+    _need(dv, "dv", torch.bfloat16, k_shape)
     if ws is None:
         ws = workspace(attn_bwd_workspace_bytes(t, hq, hkv, head_dim, n_seqs), q.device)
-    with _on(q, k, v, o, lse, do, dq, dk, dv, ws, *(() if cu_seqlens is None else (cu_seqlens,))):
-        _check(_lib.nf4_attn_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(do), t, hq, hkv, head_dim,
-                                 _ptr(cu_seqlens), n_seqs, int(bool(causal)), scale, _ptr(dq), _ptr(dk), _ptr(dv),
-                                 _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    _enqueue(_device(q, k, v, o, lse, do, dq, dk, dv, ws, cu_seqlens), stream, _lib.nf4_attn_bwd, q.data_ptr(),
+             k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), t, hq, hkv, head_dim,
+             None if cu_seqlens is None else cu_seqlens.data_ptr(), n_seqs, int(bool(causal)), scale, dq.data_ptr(),
+             dk.data_ptr(), dv.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size())
     return dq, dk, dv
 
 
@@ -616,23 +632,24 @@ class GradList:
         if len(self.outs) != len(self.grads):
             raise ValueError(f"{len(self.grads)} grads but {len(self.outs)} outs")
         arr = (GradTensor * len(self.grads))()
-        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
-            dtype = {torch.bfloat16: NF4_DTYPE_BF16, torch.float32: NF4_DTYPE_F32}.get(g.dtype)
-            if dtype is None:
+        types = {torch.bfloat16: NF4_DTYPE_BF16, torch.float32: NF4_DTYPE_F32}
+        for i, (g, o, a) in enumerate(zip(self.grads, self.outs, arr)):
+            a.dtype = types.get(g.dtype, -1)
+            if a.dtype < 0:
                 raise TypeError(f"grads[{i}] must be bfloat16 or float32, got {g.dtype}")
-            _need(g, f"grads[{i}]", g.dtype, tuple(g.shape))
+            _need(g, "grads[%d]" % i, g.dtype, g.shape)
             if o is not g:
-                _need(o, f"outs[{i}]", g.dtype, tuple(g.shape))
-            arr[i] = GradTensor(g.data_ptr(), o.data_ptr(), g.numel(), dtype)
+                _need(o, "outs[%d]" % i, g.dtype, g.shape)
+            a.grad, a.out, a.count = g.data_ptr(), o.data_ptr(), g.numel()
         self.device = self.grads[0].device
+        dev = _device(*self.grads, *self.outs)
         nbytes = int(_lib.nf4_grad_list_table(arr, len(self.grads)))
         if not nbytes:
             raise Nf4Error(NF4_E_ARG, last_error())
         h = C.c_void_p()
-        with _on(*self.grads, *self.outs):
-            self._table = workspace(nbytes, self.device)
-            _check(_lib.nf4_grad_list_create(arr, len(self.grads), _ptr(self._table), self._table.numel(),
-                                             _stream(stream), C.byref(h)))
+        self._table = workspace(nbytes, self.device)
+        _enqueue(dev, stream, lambda s: _lib.nf4_grad_list_create(arr, len(self.grads), _ptr(self._table),
+                                                                  self._table.numel(), s, C.byref(h)))
         self._h = h
         self._ws_bytes = int(_lib.nf4_grad_workspace())
 
@@ -642,8 +659,8 @@ class GradList:
         norm = torch.empty(1, dtype=torch.float32, device=self.device) if norm is None else norm
         _need(norm, "norm", torch.float32, (1,))
         ws = workspace(self._ws_bytes, self.device) if ws is None else ws
-        with _on(norm, ws, self._table):
-            _check(call(self._h, *args, _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+        _enqueue(_device(self._table, norm, ws), stream, call, self._h, *args, norm.data_ptr(), ws.data_ptr(),
+                 ws.numel() * ws.element_size())
         return norm
 
     def norm(self, norm=None, ws=None, stream=None):
