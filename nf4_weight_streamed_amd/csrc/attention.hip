@@ -115,13 +115,15 @@ int64_t attn_grid(int hkv, int64_t items) {
 }
 
 // LDS image of a staged tile: rows of D bf16, the 16-byte chunk c of row r at chunk
-// c ^ swz(r). The 256-byte bank line holds 128 / D rows; the XOR spreads the remaining row
-// bits over the chunks so that both readers cover all banks: 16 rows of one chunk
-// (ds_read_b128 of an operand) and 8 rows x 2 chunk pairs (transposing reads).
+// c ^ swz(r). LDS serves 256 bytes a cycle: 16 lanes of a 16-byte read, 32 of an 8-byte one.
+// The operand read takes one chunk of 16 rows (all 16 chunks of the 256-byte line then have
+// to differ: 128 / D rows share a line, swz maps the other row bits one to one), the
+// transposing read two neighbouring chunk pairs of 4 rows (the rows' low bits have to move
+// whole pairs of pairs).
 template <int D>
 __device__ __forceinline__ int swz(int r) {
-    constexpr int S = D == 128 ? 0 : D == 64 ? 1 : 2;
-    return (((r >> S) & (D / 16 - 1)) << 1) | ((r >> 3) & 1);
+    const int high = D == 128 ? (r & 3) << 2 : D == 64 ? ((r >> 1) & 1) << 2 : 0;
+    return high | ((r >> 2) & 3);
 }
 
 // Per-lane byte offsets into a staged tile.
@@ -177,10 +179,10 @@ __device__ __forceinline__ float sum_halves(float v) {
 
 // Global -> LDS copy of a tile by the W waves of the workgroup, 16 bytes a lane and
 // instruction: LDS is written linearly, so the swizzle is applied to the global chunk.
-template <int D, int W>
+template <int D, int W, int kRows = kTile>
 struct TileCopy {
-    static constexpr int kRounds = kTile * 2 * D / (W * 1024);
-    static_assert(kRounds * W * 1024 == kTile * 2 * D, "the waves' copies cover the tile");
+    static constexpr int kRounds = (kRows * 2 * D + W * 1024 - 1) / (W * 1024);  // the last may need only some waves
+    static constexpr int kPieces = kRows * 2 * D / 1024;
     uint32_t off[kRounds];
     __device__ __forceinline__ TileCopy(int wave, int lane, int ld) {
 #pragma unroll
@@ -192,9 +194,10 @@ struct TileCopy {
     }
     // rows >= `rows` read as zeros
     __device__ __forceinline__ void issue(const uint16_t* base, int rows, int ld, char* lds, int wave) const {
-        const auto r = make_rsrc(base, rows > 0 ? uint32_t(min(rows, kTile) - 1) * uint32_t(ld) * 2u + 2u * D : 0u);
+        const auto r = make_rsrc(base, rows > 0 ? uint32_t(min(rows, kRows) - 1) * uint32_t(ld) * 2u + 2u * D : 0u);
 #pragma unroll
-        for (int n = 0; n < kRounds; ++n) buf_load16_lds(r, off[n], lds + (n * W + wave) * 1024);
+        for (int n = 0; n < kRounds; ++n)
+            if (kRounds * W == kPieces || n * W + wave < kPieces) buf_load16_lds(r, off[n], lds + (n * W + wave) * 1024);
     }
 };
 
@@ -410,7 +413,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
         const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            f32x16 s = zero16(), dp = zero16();
+            f32x16 s = zero16(), dp;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) dp[e] = -delta;  // dP - delta straight from the accumulator
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 s = mfma32x32x16(lds_frag(k + b * 64 * D + map.row_chunk[i]), qf[i], s);
@@ -423,7 +428,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2)) * (dp[e] - delta);
+                s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -lse2)) * dp[e];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
                 const bf16x8 ds = pack8(s, g);
@@ -449,17 +454,19 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
 
 // ------------------------------------------------------------------ backward: dk, dv
 
-// One workgroup: W waves x 32 keys of one kv head, K and V fragments in registers; the
-// queries of the G heads pass through LDS in tiles of 64 (Q, dO, lse, delta). Per 32
-// queries S = Q K^T, dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
+// One workgroup: W waves x 32 keys of one kv head. K fragments stay in registers, V in LDS
+// (both in registers would leave room for one wave a SIMD only); the queries of the G heads
+// pass through LDS in tiles of 32 (Q, dO, lse, delta). Per tile S = Q K^T, dP = dO V^T (a key
+// in a lane), dv^T += dO^T P, dk^T += Q^T dS.
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
 template <int D, int W>
-__global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
-    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sQ0[kTile * 2 * D], sD0[kTile * 2 * D];
-    __shared__ __align__(1024) char sQ1[kTile * 2 * D], sD1[kTile * 2 * D];
-    __shared__ __align__(16) float sL[2][2][kTile];  // [tile parity][lse * log2 e, delta]
+__global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dkv(AttnArgs a) {
+    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32, BQ = 32;
+    __shared__ __align__(1024) char sV[BM * 2 * D];
+    __shared__ __align__(1024) char sQ0[BQ * 2 * D], sD0[BQ * 2 * D];
+    __shared__ __align__(1024) char sQ1[BQ * 2 * D], sD1[BQ * 2 * D];
+    __shared__ __align__(16) float sL[2][2][BQ];  // [tile parity][lse * log2 e, delta]
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * a.splits, kvh, item)) return;
@@ -472,34 +479,35 @@ __global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
     const int k_lo = t.row0 + 32 * wave;
     const float c = a.scale * kLog2e;
 
-    // (head, query tile) pairs: nq tiles a head, from the first that sees a key of this tile
-    const int tile_lo = a.causal ? t.row0 / kTile : 0;
-    const int nq = (t.len + kTile - 1) / kTile - tile_lo;
-    const int total = G * nq;
+    // (query tile, head) pairs: the tiles from the last down to the first that sees a key of
+    // this workgroup, and the heads of each. The workgroups of a kv head run side by side on
+    // one XCD: in this order all of them want the same Q and dO at about the same time, and
+    // find them in its L2.
+    const int tile_lo = a.causal ? t.row0 / BQ : 0, tile_hi = (t.len - 1) / BQ;
+    const int total = G * (tile_hi + 1 - tile_lo);
     const int i0 = int(int64_t(split) * total / a.splits), i1 = int(int64_t(split + 1) * total / a.splits);
 
-    bf16x8 kf[KS], vf[KS];
+    bf16x8 kf[KS];
     {
         const size_t at = (size_t(t.begin) + t.row0) * ldk + kvh * D;
-        const uint32_t bytes = uint32_t(min(t.len - t.row0, BM) - 1) * uint32_t(ldk) * 2u + 2u * D;
-        const auto rk = make_rsrc(a.k + at, bytes), rv = make_rsrc(a.v + at, bytes);
+        const int rows = min(t.len - t.row0, BM);
+        const auto rk = make_rsrc(a.k + at, uint32_t(rows - 1) * uint32_t(ldk) * 2u + 2u * D);
         const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
-            vf[s] = as_bf16x8(buf_load16(rv, o + 32u * s));
-        }
+        for (int s = 0; s < KS; ++s) kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
+        TileCopy<D, W, BM>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
     }
     const LdsMap<D> map(lane);
-    const TileCopy<D, W> copy(wave, lane, ldq);
+    const TileCopy<D, W, BQ> copy(wave, lane, ldq);
     float stat = 0.0f;  // this thread's lse or delta of the tile being staged
-    auto stage = [&](int i, char* q, char* d) {
-        const int head = kvh * G + i / nq, q0 = (tile_lo + i % nq) * kTile;
+    int next = tile_hi - i0 / G, g_next = i0 % G;  // of the tile to be staged
+    auto stage = [&](int, char* q, char* d) {
+        const int q0 = next * BQ, head = kvh * G + g_next;
         const size_t at = (size_t(t.begin) + q0) * ldq + head * D;
         copy.issue(a.q + at, t.len - q0, ldq, q, wave);
         copy.issue(a.dO + at, t.len - q0, ldq, d, wave);
-        if (threadIdx.x < 2 * kTile) {
-            const int r = threadIdx.x & (kTile - 1), which = threadIdx.x / kTile;
+        if (threadIdx.x < 2 * BQ) {
+            const int r = threadIdx.x & (BQ - 1), which = threadIdx.x / BQ;
             // rows past the sequence: lse = +inf makes their P zero
             stat = which ? 0.0f : INFINITY;
             if (q0 + r < t.len) {
@@ -507,59 +515,63 @@ __global__ __launch_bounds__(64 * W, 1) void k_attn_bwd_dkv(AttnArgs a) {
                 stat = which ? a.delta[s] : a.lse_in[s];  // first used behind the tile's wait
             }
         }
+        if (++g_next == G) g_next = 0, --next;
     };
     auto put_stat = [&](int i) {
-        if (threadIdx.x < 2 * kTile) sL[i & 1][threadIdx.x / kTile][threadIdx.x & (kTile - 1)] = threadIdx.x < kTile ? stat * kLog2e : stat;
+        if (threadIdx.x < 2 * BQ)
+            sL[i & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = threadIdx.x < BQ ? stat * kLog2e : stat;
     };
 
     f32x16 dk[NB], dv[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) dk[nb] = zero16(), dv[nb] = zero16();
     if (i0 < i1) stage(i0, sQ0, sD0);
-    auto compute = [&](int i, const char* sq, const char* sd) {
-        const int buf = i & 1;
-        const int q0 = (tile_lo + i % nq) * kTile;
+    int cur = tile_hi - i0 / G, g_cur = i0 % G;
+    auto compute = [&](int i, const char* q, const char* d) {
+        const int buf = i & 1, q0 = cur * BQ;
+        if (++g_cur == G) g_cur = 0, --cur;
+        if (a.causal && q0 + BQ - 1 < k_lo) return;  // all its queries come before the wave's keys
+        f32x16 s = zero16(), dp;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int qb = q0 + 32 * b;
-            if (a.causal && qb + 31 < k_lo) continue;
-            const char* q = sq + b * 64 * D;
-            const char* d = sd + b * 64 * D;
-            f32x16 s = zero16(), dp = zero16();
+        for (int e = 0; e < 16; e += 4) {  // dP - delta straight from the accumulator
+            const f32x4 dl = *reinterpret_cast<const f32x4*>(&sL[buf][1][2 * e + 4 * h]);
 #pragma unroll
-            for (int e = 0; e < KS; ++e) {
-                s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), kf[e], s);
-                dp = mfma32x32x16(lds_frag(d + map.row_chunk[e]), vf[e], dp);
+            for (int x = 0; x < 4; ++x) dp[e + x] = -dl[x];
+        }
+        const char* v = sV + wave * 64 * D;
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+            s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), kf[e], s);
+            dp = mfma32x32x16(lds_frag(d + map.row_chunk[e]), lds_frag(v + map.row_chunk[e]), dp);
+        }
+        if (a.causal && q0 < k_lo + 31) {
+            const int first = key - q0 - 4 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (8 * (e / 4) + e % 4 < first) s[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e += 4) {
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(&sL[buf][0][2 * e + 4 * h]);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                s[e + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + x], c, -ls[x]));
+                dp[e + x] *= s[e + x];
             }
-            if (a.causal && qb < k_lo + 31) {
-                const int first = key - qb - 4 * h;
+        }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (8 * (e / 4) + e % 4 < first) s[e] = -INFINITY;
-            }
+        for (int g = 0; g < 2; ++g) {
+            const bf16x8 p = pack8(s, g), ds = pack8(dp, g);
+            const char *dg = d + g * 32 * D, *qg = q + g * 32 * D;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const f32x4 ls = *reinterpret_cast<const f32x4*>(&sL[buf][0][32 * b + 2 * e + 4 * h]);
-                const f32x4 dl = *reinterpret_cast<const f32x4*>(&sL[buf][1][32 * b + 2 * e + 4 * h]);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    s[e + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + x], c, -ls[x]));
-                    dp[e + x] = s[e + x] * (dp[e + x] - dl[x]);
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const bf16x8 p = pack8(s, g), ds = pack8(dp, g);
-                const char *dg = d + g * 32 * D, *qg = q + g * 32 * D;
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    dv[nb] = mfma32x32x16(lds_frag_tr(dg + map.tr[nb][0], dg + map.tr[nb][1]), p, dv[nb]);
-                    dk[nb] = mfma32x32x16(lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]), ds, dk[nb]);
-                }
+            for (int nb = 0; nb < NB; ++nb) {
+                dv[nb] = mfma32x32x16(lds_frag_tr(dg + map.tr[nb][0], dg + map.tr[nb][1]), p, dv[nb]);
+                dk[nb] = mfma32x32x16(lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]), ds, dk[nb]);
             }
         }
     };
     double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute, put_stat);
+    wait_vmcnt<0>();  // without a tile to use it, V's copy is still under way
     if (key >= t.len) return;
     const size_t row = size_t(t.begin) + key;
     if (a.splits == 1) {
@@ -614,11 +626,14 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
     return cu ? T / bm + n_seqs : cdiv(T, bm);
 }
 
-// Shares of dk and dv: enough workgroups for two a CU where the keys alone give fewer.
-int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G) {
-    const int64_t wgs = cdiv(T, 32 * kWaves) * hkv;
+// Shares of dk and dv. Two workgroups fit a CU: 512 keep the card busy when all are equally
+// long; under a causal mask the first keys have the most queries, and twice as many let the
+// short ones fill up behind the long ones (8192 tokens, 64/8 heads: 4.43 ms without shares,
+// 3.43 ms with 2; 2048 tokens, 40/8, not causal: 313 us with 512 workgroups, 334 with 1024).
+int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int causal) {
+    const int64_t wgs = std::max(cdiv(T, 32 * kWaves), n_seqs) * hkv;
     const int64_t most = std::min<int64_t>(16, G * cdiv(T, kTile));
-    return int(std::max<int64_t>(1, std::min<int64_t>(most, cdiv(512, wgs))));
+    return int(std::max<int64_t>(1, std::min<int64_t>(most, cdiv(causal ? 1024 : 512, wgs))));
 }
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
@@ -646,9 +661,9 @@ struct AttnBwdPlan {
     size_t delta_bytes, part_bytes;
 };
 
-AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs) {
+AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs, int causal) {
     AttnBwdPlan p{};
-    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv));
+    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv), causal);
     p.delta_bytes = (size_t(T) * hq * 4 + 255) & ~size_t(255);
     p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * T * hkv * D * 4 : 0;
     return p;
@@ -716,7 +731,7 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
     if (T <= 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024 || n_seqs < 0 ||
         (head_dim != 32 && head_dim != 64 && head_dim != 128))
         return 0;
-    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs);
+    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 1);  // never fewer shares than without a mask
     return p.delta_bytes + p.part_bytes;
 }
 
@@ -731,7 +746,7 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) || !aligned16(dq) ||
         !aligned16(dk) || !aligned16(dv) || !lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
         return fail(NF4_E_ARG, "%s: tensors must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
-    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs);
+    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, causal);
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.delta_bytes + p.part_bytes)
         return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
                     p.delta_bytes + p.part_bytes, ws_bytes);
