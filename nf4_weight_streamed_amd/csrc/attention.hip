@@ -30,7 +30,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTile = 64;  // rows of a staged tile (keys in fwd and dq, queries in dkv)
+constexpr int kKeyWaves = 4;  // blocks of 32 keys of a dk/dv workgroup
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
@@ -40,7 +40,7 @@ struct AttnArgs {
     const uint16_t *q, *k, *v, *o, *dO;
     const float* lse_in;
     uint16_t *out, *dq, *dk, *dv;
-    float *lse, *delta, *part;  // delta [hq][T]; part: fp32 shares of dk then dv, [split][T][hkv*D] each
+    float *lse, *stats, *part;  // stats [2][hq][T]: lse * log2 e, delta; part: fp32 shares of dk and dv
     const int32_t* cu;
     int T, n_seqs, hq, hkv, causal, tiles, splits;
     float scale;
@@ -179,15 +179,17 @@ __device__ __forceinline__ float sum_halves(float v) {
 
 // Global -> LDS copy of a tile by the W waves of the workgroup, 16 bytes a lane and
 // instruction: LDS is written linearly, so the swizzle is applied to the global chunk.
-template <int D, int W, int kRows = kTile>
+template <int D, int kRows, int W>
 struct TileCopy {
-    static constexpr int kRounds = (kRows * 2 * D + W * 1024 - 1) / (W * 1024);  // the last may need only some waves
     static constexpr int kPieces = kRows * 2 * D / 1024;
+    static constexpr int kRounds = (kPieces + W - 1) / W;
     uint32_t off[kRounds];
+    // with fewer pieces than waves some are copied twice, the same bytes
+    static __device__ __forceinline__ int piece(int n, int wave) { return (n * W + wave) % kPieces; }
     __device__ __forceinline__ TileCopy(int wave, int lane, int ld) {
 #pragma unroll
         for (int n = 0; n < kRounds; ++n) {
-            const int p = (n * W + wave) * 1024 + lane * 16;
+            const int p = piece(n, wave) * 1024 + lane * 16;
             const int row = p / (2 * D), ch = (p / 16) % (D / 8);
             off[n] = uint32_t(row) * uint32_t(ld) * 2u + uint32_t(ch ^ swz<D>(row)) * 16u;
         }
@@ -196,50 +198,74 @@ struct TileCopy {
     __device__ __forceinline__ void issue(const uint16_t* base, int rows, int ld, char* lds, int wave) const {
         const auto r = make_rsrc(base, rows > 0 ? uint32_t(min(rows, kRows) - 1) * uint32_t(ld) * 2u + 2u * D : 0u);
 #pragma unroll
-        for (int n = 0; n < kRounds; ++n)
-            if (kRounds * W == kPieces || n * W + wave < kPieces) buf_load16_lds(r, off[n], lds + (n * W + wave) * 1024);
+        for (int n = 0; n < kRounds; ++n) buf_load16_lds(r, off[n], lds + piece(n, wave) * 1024);
     }
 };
 
 // Tiles [j0, j1) through two pairs of LDS buffers: tile j + 1 is copied while tile j is
-// used. Tile j0 has been issued to (a0, b0) by the caller. The four buffers have to be
-// __shared__ variables of their own: the compiler then knows that a read of one does not
-// depend on the outstanding copies to the others, and does not wait for them.
-template <typename Stage, typename Compute, typename Arrive>
-__device__ __forceinline__ void double_buffered(int j0, int j1, char* a0, char* b0, char* a1, char* b1, Stage&& stage,
-                                                Compute&& compute, Arrive&& arrive) {
-    for (int j = j0; j < j1; ++j) {
-        arrive(j);
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (j + 1 < j1) stage(j + 1, a1, b1);
-        compute(j, a0, b0);
-        if (++j >= j1) break;
-        arrive(j);
-        wait_vmcnt<0>();
-        __syncthreads();
-        if (j + 1 < j1) stage(j + 1, a0, b0);
-        compute(j, a1, b1);
-    }
-}
-
+// used. The four buffers have to be __shared__ variables of their own: the compiler then
+// knows that a read of one does not depend on the outstanding copies to the others, and does
+// not wait for them. Measured and left out: four pairs, three tiles ahead (512 tokens of 28/4
+// heads 12.0 -> 14.4 us, fewer workgroups fit a CU), and the copy instructions spread between
+// the first products (12.1 -> 12.5 us, more registers).
 template <typename Stage, typename Compute>
 __device__ __forceinline__ void double_buffered(int j0, int j1, char* a0, char* b0, char* a1, char* b1, Stage&& stage,
                                                 Compute&& compute) {
-    double_buffered(j0, j1, a0, b0, a1, b1, stage, compute, [](int) {});
+    if (j0 < j1) stage(j0, a0, b0);
+    auto step = [&](int j, char* a, char* b, char* a_free, char* b_free) {
+        wait_vmcnt<0>();
+        __syncthreads();  // every wave's share of tile j is there; the freed pair has no reader left
+        if (j + 1 < j1) stage(j + 1, a_free, b_free);
+        compute(j, a, b);
+    };
+    for (int j = j0; j < j1; j += 2) {
+        step(j, a0, b0, a1, b1);
+        if (j + 1 < j1) step(j + 1, a1, b1, a0, b0);
+    }
+}
+
+// Where one of several waves' shares of 32 x D fp32 sums lies in the (then free) staging
+// buffers, 16 bytes a lane and step. Every access strides 1 KB: lane-contiguous.
+template <int D>
+__device__ __forceinline__ f32x4* share_slot(int i, int buffer_bytes, char* a0, char* a1, char* b0, char* b1, int lane) {
+    const int fit = buffer_bytes / (128 * D), n = i / fit;
+    char* b = n == 0 ? a0 : n == 1 ? a1 : n == 2 ? b0 : b1;
+    return reinterpret_cast<f32x4*>(b + i % fit * (128 * D)) + lane;
+}
+
+template <int NB>
+__device__ __forceinline__ void put_share(f32x4* p, const f32x16 (&x)[NB]) {
+#pragma unroll
+    for (int n = 0; n < 4 * NB; ++n) {
+        const int e = n % 4 * 4;
+        p[64 * n] = f32x4{x[n / 4][e], x[n / 4][e + 1], x[n / 4][e + 2], x[n / 4][e + 3]};
+    }
+}
+
+// x = x * f + share * g
+template <int NB>
+__device__ __forceinline__ void add_share(f32x16 (&x)[NB], const f32x4* p, float f, float g) {
+#pragma unroll
+    for (int n = 0; n < 4 * NB; ++n) {
+        const f32x4 v = p[64 * n];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n / 4][n % 4 * 4 + e] = x[n / 4][n % 4 * 4 + e] * f + v[e] * g;
+    }
 }
 
 // ------------------------------------------------------------------ forward
 
-// One workgroup: W waves x 32 queries of one head; K and V in tiles of 64 keys, double
-// buffered in LDS. S^T = K Q^T puts a query in a lane, so the softmax statistics are one
-// register each. The running maximum is raised, and o and the sum rescaled, only when some
-// row's tile maximum exceeds it by more than 8 (in log2 units): p then stays below 2^8.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
-    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D];
-    __shared__ __align__(1024) char sK1[kTile * 2 * D], sV1[kTile * 2 * D];
+// One workgroup: R rows of waves x C waves, 32 queries of one head a row; K and V in tiles of
+// 64 keys, double buffered in LDS. R = 4, C = 1: a row is one wave, which takes both 32-key
+// blocks of a tile. R = 2, C = 2: its two waves take one block each and meet at the end: twice
+// the workgroups, each half as long, for calls too small to fill the card. S^T = K Q^T puts a
+// query in a lane, so the softmax statistics are one register each. The running maximum is
+// raised, and o and the sum rescaled, only when some row's tile maximum exceeds it by more than
+// 8 (in log2 units): p then stays below 2^8.
+template <int D, int R, int C>
+__global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
+    constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
+    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D], sK1[kTile * 2 * D], sV1[kTile * 2 * D];
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
@@ -247,8 +273,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
     Tile t;
     if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;  // longest rows first
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int wr = wave % R, wc = C == 1 ? 0 : wave / R, b0 = B * wc;  // row, place in it, first key block
     const int ldq = a.hq * D, ldk = a.hkv * D;
-    const int q_row = t.row0 + 32 * wave + (lane & 31);
+    const int q_lo = t.row0 + 32 * wr, q_row = q_lo + (lane & 31);
     const float c = a.scale * kLog2e;
 
     bf16x8 qf[KS];
@@ -256,20 +283,21 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
         const int rows = t.len - t.row0;
         const auto r = make_rsrc(a.q + (size_t(t.begin) + t.row0) * ldq + head * D,
                                  uint32_t(min(rows, BM) - 1) * uint32_t(ldq) * 2u + 2u * D);
-        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
+        const uint32_t o = uint32_t(32 * wr + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
 #pragma unroll
         for (int s = 0; s < KS; ++s) qf[s] = as_bf16x8(buf_load16(r, o + 32u * s));
     }
     const LdsMap<D> map(lane);
-    const TileCopy<D, W> copy(wave, lane, ldk);
+    const TileCopy<D, kTile, R * C> copy(wave, lane, ldk);
     const uint16_t* kb = a.k + size_t(t.begin) * ldk + kvh * D;
     const uint16_t* vb = a.v + size_t(t.begin) * ldk + kvh * D;
 
     f32x16 acc[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[nb] = zero16();
-    float m = -INFINITY, l = 0.0f;
-    const int q_lo = t.row0 + 32 * wave;
+    // m: running maximum (-inf before the first key); base: what exponents are taken from, m
+    // or 0 while there is none
+    float m = -INFINITY, base = 0.0f, l = 0.0f;
     const int keys = a.causal ? min(t.len, t.row0 + BM) : t.len;
     const int n = (keys + kTile - 1) / kTile;
 
@@ -277,34 +305,38 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
         copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
         copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
     };
-    stage(0, sK0, sV0);
     auto compute = [&](int j, const char* k, const char* v) {
-        const int k0 = j * kTile;
-        if (a.causal && k0 > q_lo + 31) return;  // nothing of this tile for the wave's rows
-        f32x16 s[2] = {zero16(), zero16()};
+        const int k0 = j * kTile + 32 * b0;
+        if (a.causal && k0 > q_lo + 31) return;  // nothing of these keys for the wave's rows
+        k += b0 * 64 * D;
+        v += b0 * 64 * D;
+        f32x16 s[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) s[b] = zero16();
 #pragma unroll
         for (int i = 0; i < KS; ++i)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < B; ++b)
                 s[b] = mfma32x32x16(lds_frag(k + b * 64 * D + map.row_chunk[i]), qf[i], s[b]);
-        if (k0 + kTile > t.len || (a.causal && k0 + kTile - 1 > q_lo)) {
+        if (k0 + 32 * B > t.len || (a.causal && k0 + 32 * B - 1 > q_lo)) {
             const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     if (32 * b + 8 * (e / 4) + e % 4 > last) s[b][e] = -INFINITY;
         }
         float mt = s[0][0];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int e = 0; e < 16; ++e) mt = fmaxf(mt, s[b][e]);
         mt = max_halves(mt) * c;
         if (__any(mt > m + 8.0f)) {
-            const float mn = fmaxf(m, mt);
-            const float f = exp2f(m - mn);
-            m = mn;
+            m = fmaxf(m, mt);
+            const float to = m > -INFINITY ? m : 0.0f;
+            const float f = exp2f(base - to);
+            base = to;
             l *= f;
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -312,14 +344,14 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
                 for (int e = 0; e < 16; ++e) acc[nb][e] *= f;
         }
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], c, -m));
+                s[b][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][e], c, -base));
                 l += s[b][e];
             }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2 * B; ++g) {
             const bf16x8 p = pack8(s[g / 2], g % 2);
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
@@ -329,6 +361,26 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
     };
     double_buffered(0, n, sK0, sV0, sK1, sV1, stage, compute);
     l = sum_halves(l);
+    if constexpr (C > 1) {  // the waves of a row hand their shares to its first
+        __shared__ float sML[R * C][2][64];  // the exponents' base and the sum; no share without a key
+        __syncthreads();
+        if (wc > 0) {
+            put_share(share_slot<D>((wc - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), acc);
+            sML[wave][0][lane] = m > -INFINITY ? base : -INFINITY;
+            sML[wave][1][lane] = l;
+        }
+        __syncthreads();
+        if (wc > 0) return;
+#pragma unroll
+        for (int i = 1; i < C; ++i) {
+            const float other = sML[i * R + wr][0][lane];
+            const float to = fmaxf(base, other);  // the first wave has seen key 0: finite
+            const float f0 = exp2f(base - to), f1 = exp2f(other - to);
+            base = to;
+            l = l * f0 + sML[i * R + wr][1][lane] * f1;
+            add_share(acc, share_slot<D>((i - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), f0, f1);
+        }
+    }
     if (q_row < t.len) {
         const size_t row = size_t(t.begin) + q_row;
         const float inv = 1.0f / l;
@@ -340,7 +392,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
                 *reinterpret_cast<u32x2*>(out + 32 * nb + 2 * e + 4 * h) =
                     u32x2{pack_bf16x2(acc[nb][e] * inv, acc[nb][e + 1] * inv),
                           pack_bf16x2(acc[nb][e + 2] * inv, acc[nb][e + 3] * inv)};
-        if (h == 0) a.lse[size_t(head) * a.T + row] = (m + log2f(l)) * kLn2;
+        if (h == 0) a.lse[size_t(head) * a.T + row] = (base + log2f(l)) * kLn2;
     }
 }
 
@@ -348,12 +400,11 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_fwd(AttnArgs a) {
 
 // As the forward, with dO beside Q in registers: per 64-key tile S^T = K Q^T,
 // dP^T = V dO^T, dS^T in place, dq^T += K^T dS^T. delta is formed here first (the dk/dv
-// kernel behind this one reads it).
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
-    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D];
-    __shared__ __align__(1024) char sK1[kTile * 2 * D], sV1[kTile * 2 * D];
+// kernel behind this one reads it). R, C and B as in the forward.
+template <int D, int R, int C>
+__global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
+    constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
+    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D], sK1[kTile * 2 * D], sV1[kTile * 2 * D];
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
@@ -361,18 +412,18 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
     Tile t;
     if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int wr = wave % R, wc = C == 1 ? 0 : wave / R, b0 = B * wc;
     const int ldq = a.hq * D, ldk = a.hkv * D;
-    const int q_row = t.row0 + 32 * wave + (lane & 31);
+    const int q_lo = t.row0 + 32 * wr, q_row = q_lo + (lane & 31);
     const float c = a.scale * kLog2e;
 
-    const TileCopy<D, W> copy(wave, lane, ldk);
+    const TileCopy<D, kTile, R * C> copy(wave, lane, ldk);
     const uint16_t* kb = a.k + size_t(t.begin) * ldk + kvh * D;
     const uint16_t* vb = a.v + size_t(t.begin) * ldk + kvh * D;
     auto stage = [&](int j, char* k, char* v) {
         copy.issue(kb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, k, wave);
         copy.issue(vb + size_t(j) * kTile * ldk, t.len - j * kTile, ldk, v, wave);
     };
-    stage(0, sK0, sV0);
 
     bf16x8 qf[KS], df[KS];
     float delta = 0.0f;
@@ -381,7 +432,7 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
         const size_t at = (size_t(t.begin) + t.row0) * ldq + head * D;
         const uint32_t bytes = uint32_t(min(rows, BM) - 1) * uint32_t(ldq) * 2u + 2u * D;
         const auto rq = make_rsrc(a.q + at, bytes), rd = make_rsrc(a.dO + at, bytes), ro = make_rsrc(a.o + at, bytes);
-        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
+        const uint32_t o = uint32_t(32 * wr + (lane & 31)) * uint32_t(ldq) * 2u + 16u * h;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             qf[s] = as_bf16x8(buf_load16(rq, o + 32u * s));
@@ -396,23 +447,27 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
     if (q_row < t.len) {
         const size_t at = size_t(head) * a.T + t.begin + q_row;
         lse2 = a.lse_in[at] * kLog2e;
-        if (h == 0) a.delta[at] = delta;
+        if (h == 0 && wc == 0) {
+            a.stats[at] = lse2;
+            a.stats[size_t(a.hq) * a.T + at] = delta;
+        }
     }
     const LdsMap<D> map(lane);
 
     f32x16 acc[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) acc[nb] = zero16();
-    const int q_lo = t.row0 + 32 * wave;
     const int keys = a.causal ? min(t.len, t.row0 + BM) : t.len;
     const int n = (keys + kTile - 1) / kTile;
     auto compute = [&](int j, const char* k, const char* v) {
-        const int k0 = j * kTile;
+        const int k0 = j * kTile + 32 * b0;
         if (a.causal && k0 > q_lo + 31) return;
-        const bool edge = k0 + kTile > t.len || (a.causal && k0 + kTile - 1 > q_lo);
+        k += b0 * 64 * D;
+        v += b0 * 64 * D;
+        const bool edge = k0 + 32 * B > t.len || (a.causal && k0 + 32 * B - 1 > q_lo);
         const int last = (a.causal ? min(q_row, t.len - 1) : t.len - 1) - k0 - 4 * h;
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < B; ++b) {
             f32x16 s = zero16(), dp;
 #pragma unroll
             for (int e = 0; e < 16; ++e) dp[e] = -delta;  // dP - delta straight from the accumulator
@@ -440,6 +495,15 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
         }
     };
     double_buffered(0, n, sK0, sV0, sK1, sV1, stage, compute);
+    if constexpr (C > 1) {  // the waves of a row hand their shares to its first
+        __syncthreads();
+        if (wc > 0) put_share(share_slot<D>((wc - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), acc);
+        __syncthreads();
+        if (wc > 0) return;
+#pragma unroll
+        for (int i = 1; i < C; ++i)
+            add_share(acc, share_slot<D>((i - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), 1.0f, 1.0f);
+    }
     if (q_row < t.len) {
         uint16_t* out = a.dq + (size_t(t.begin) + q_row) * ldq + head * D;
 #pragma unroll
@@ -454,29 +518,37 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dq(AttnArgs a) {
 
 // ------------------------------------------------------------------ backward: dk, dv
 
-// One workgroup: W waves x 32 keys of one kv head. K fragments stay in registers, V in LDS
-// (both in registers would leave room for one wave a SIMD only); the queries of the G heads
-// pass through LDS in tiles of 32 (Q, dO, lse, delta). Per tile S = Q K^T, dP = dO V^T (a key
-// in a lane), dv^T += dO^T P, dk^T += Q^T dS.
+// Where a workgroup's share of dk and dv begins in the workspace, in 16-byte units.
+template <int D>
+__device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const AttnArgs& a) {
+    return ((size_t(tile) * a.hkv + kvh) * a.splits + split) * (2 * kKeyWaves * 8 * D);
+}
+
+// One workgroup: 8 waves, KW blocks of 32 keys of one kv head x QW = 8 / KW. K fragments stay
+// in registers, V in LDS (both in registers would leave room for one wave a SIMD only); the
+// queries of the G heads pass through LDS in tiles of 32 QW (Q, dO, lse, delta), 32 to each of
+// the QW waves of a key block, whose sums meet at the end. Per 32 queries S = Q K^T,
+// dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dkv(AttnArgs a) {
-    constexpr int BM = 32 * W, KS = D / 16, NB = D / 32, BQ = 32;
+template <int D>
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
+    constexpr int KW = kKeyWaves, QW = 8 / KW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = 32 * QW;
     __shared__ __align__(1024) char sV[BM * 2 * D];
-    __shared__ __align__(1024) char sQ0[BQ * 2 * D], sD0[BQ * 2 * D];
-    __shared__ __align__(1024) char sQ1[BQ * 2 * D], sD1[BQ * 2 * D];
-    __shared__ __align__(16) float sL[2][2][BQ];  // [tile parity][lse * log2 e, delta]
+    // a tile's Q, and its dO with the rows' lse * log2 e and delta behind it
+    constexpr int QB = BQ * 2 * D, SB = BQ < 64 ? 256 : BQ * 4, DB = QB + 2 * SB;
+    __shared__ __align__(1024) char sQ0[QB], sD0[DB], sQ1[QB], sD1[DB];
     const int G = a.hq / a.hkv;
     int kvh, item;
     if (!pick_item(blockIdx.x, a.hkv, a.tiles * a.splits, kvh, item)) return;
     const int split = item % a.splits;
     Tile t;
-    if (!find_tile(a, BM, item / a.splits, t)) return;  // causal: the first keys have the most queries
+    const int tile = item / a.splits;
+    if (!find_tile(a, BM, tile, t)) return;  // causal: the first keys have the most queries
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
     const int ldq = a.hq * D, ldk = a.hkv * D;
-    const int key = t.row0 + 32 * wave + (lane & 31);
-    const int k_lo = t.row0 + 32 * wave;
+    const int kw = wave % KW, qw = wave / KW;
+    const int k_lo = t.row0 + 32 * kw, key = k_lo + (lane & 31);
     const float c = a.scale * kLog2e;
 
     // (query tile, head) pairs: the tiles from the last down to the first that sees a key of
@@ -492,53 +564,45 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dkv(AttnArgs a) {
         const size_t at = (size_t(t.begin) + t.row0) * ldk + kvh * D;
         const int rows = min(t.len - t.row0, BM);
         const auto rk = make_rsrc(a.k + at, uint32_t(rows - 1) * uint32_t(ldk) * 2u + 2u * D);
-        const uint32_t o = uint32_t(32 * wave + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
+        const uint32_t o = uint32_t(32 * kw + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
 #pragma unroll
         for (int s = 0; s < KS; ++s) kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
-        TileCopy<D, W, BM>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
+        TileCopy<D, BM, 8>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
     }
     const LdsMap<D> map(lane);
-    const TileCopy<D, W, BQ> copy(wave, lane, ldq);
-    float stat = 0.0f;  // this thread's lse or delta of the tile being staged
+    const TileCopy<D, BQ, 8> copy(wave, lane, ldq);
     int next = tile_hi - i0 / G, g_next = i0 % G;  // of the tile to be staged
     auto stage = [&](int, char* q, char* d) {
-        const int q0 = next * BQ, head = kvh * G + g_next;
+        const int q0 = next * BQ, head = kvh * G + g_next, rows = t.len - q0;
         const size_t at = (size_t(t.begin) + q0) * ldq + head * D;
-        copy.issue(a.q + at, t.len - q0, ldq, q, wave);
-        copy.issue(a.dO + at, t.len - q0, ldq, d, wave);
-        if (threadIdx.x < 2 * BQ) {
-            const int r = threadIdx.x & (BQ - 1), which = threadIdx.x / BQ;
-            // rows past the sequence: lse = +inf makes their P zero
-            stat = which ? 0.0f : INFINITY;
-            if (q0 + r < t.len) {
-                const size_t s = size_t(head) * a.T + t.begin + q0 + r;
-                stat = which ? a.delta[s] : a.lse_in[s];  // first used behind the tile's wait
-            }
+        copy.issue(a.q + at, rows, ldq, q, wave);
+        copy.issue(a.dO + at, rows, ldq, d, wave);
+        // rows past the sequence read as zeros, like their q and dO: P = 1 then multiplies zeros only
+        if (wave < 2 * SB / 256) {
+            constexpr int per = SB / 256;  // waves for each of lse and delta
+            const int x = wave / per, r0 = wave % per * 64;
+            const auto r = make_rsrc(a.stats + (size_t(x) * a.hq + head) * a.T + t.begin + q0,
+                                     uint32_t(min(rows, BQ)) * 4u);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)(d + QB + wave * 256), 4, (r0 + lane) * 4, 0, 0, 0);
         }
         if (++g_next == G) g_next = 0, --next;
-    };
-    auto put_stat = [&](int i) {
-        if (threadIdx.x < 2 * BQ)
-            sL[i & 1][threadIdx.x / BQ][threadIdx.x & (BQ - 1)] = threadIdx.x < BQ ? stat * kLog2e : stat;
     };
 
     f32x16 dk[NB], dv[NB];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) dk[nb] = zero16(), dv[nb] = zero16();
-    if (i0 < i1) stage(i0, sQ0, sD0);
     int cur = tile_hi - i0 / G, g_cur = i0 % G;
-    auto compute = [&](int i, const char* q, const char* d) {
-        const int buf = i & 1, q0 = cur * BQ;
+    auto compute = [&](int, const char* q, const char* d) {
+        const int q0 = cur * BQ + 32 * qw;
         if (++g_cur == G) g_cur = 0, --cur;
-        if (a.causal && q0 + BQ - 1 < k_lo) return;  // all its queries come before the wave's keys
+        if (a.causal && q0 + 31 < k_lo) return;  // all the wave's queries come before its keys
+        const f32x4* stat = reinterpret_cast<const f32x4*>(d + QB + 128 * qw) + h;
+        q += qw * 64 * D;
+        d += qw * 64 * D;
         f32x16 s = zero16(), dp;
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {  // dP - delta straight from the accumulator
-            const f32x4 dl = *reinterpret_cast<const f32x4*>(&sL[buf][1][2 * e + 4 * h]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) dp[e + x] = -dl[x];
-        }
-        const char* v = sV + wave * 64 * D;
+        for (int e = 0; e < 16; ++e) dp[e] = -stat[SB / 16 + e / 4 * 2][e % 4];  // dP - delta straight from the accumulator
+        const char* v = sV + kw * 64 * D;
 #pragma unroll
         for (int e = 0; e < KS; ++e) {
             s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), kf[e], s);
@@ -551,13 +615,9 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dkv(AttnArgs a) {
                 if (8 * (e / 4) + e % 4 < first) s[e] = -INFINITY;
         }
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const f32x4 ls = *reinterpret_cast<const f32x4*>(&sL[buf][0][2 * e + 4 * h]);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                s[e + x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e + x], c, -ls[x]));
-                dp[e + x] *= s[e + x];
-            }
+        for (int e = 0; e < 16; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -stat[e / 4 * 2][e % 4]));
+            dp[e] *= s[e];
         }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -570,70 +630,85 @@ __global__ __launch_bounds__(64 * W, 2) void k_attn_bwd_dkv(AttnArgs a) {
             }
         }
     };
-    double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute, put_stat);
+    double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute);
     wait_vmcnt<0>();  // without a tile to use it, V's copy is still under way
-    if (key >= t.len) return;
-    const size_t row = size_t(t.begin) + key;
+    // The sums of a key block: waves qw > 0 hand theirs to wave 0 through the staging buffers,
+    // dk first, then dv, added in the order of qw.
+    auto meet = [&](f32x16(&x)[NB]) {
+        __syncthreads();
+        if (qw > 0) put_share(share_slot<D>((qw - 1) * KW + kw, QB, sQ0, sQ1, sD0, sD1, lane), x);
+        __syncthreads();
+        if (qw == 0) {
+            for (int q = 1; q < QW; ++q)
+                add_share(x, share_slot<D>((q - 1) * KW + kw, QB, sQ0, sQ1, sD0, sD1, lane), 1.0f, 1.0f);
+        }
+    };
+    meet(dk);
+    meet(dv);
+    if (qw > 0) return;
     if (a.splits == 1) {
+        if (key >= t.len) return;
+        const size_t at = (size_t(t.begin) + key) * ldk + kvh * D + 4 * h;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const size_t at = row * ldk + kvh * D + 32 * nb + 2 * e + 4 * h;
-                *reinterpret_cast<u32x2*>(a.dk + at) =
-                    u32x2{pack_bf16x2(dk[nb][e] * a.scale, dk[nb][e + 1] * a.scale),
-                          pack_bf16x2(dk[nb][e + 2] * a.scale, dk[nb][e + 3] * a.scale)};
-                *reinterpret_cast<u32x2*>(a.dv + at) =
-                    u32x2{pack_bf16x2(dv[nb][e], dv[nb][e + 1]), pack_bf16x2(dv[nb][e + 2], dv[nb][e + 3])};
-            }
+        for (int n = 0; n < 4 * NB; ++n) {
+            const int nb = n / 4, e = n % 4 * 4;
+            *reinterpret_cast<u32x2*>(a.dk + at + 8 * n) =
+                u32x2{pack_bf16x2(dk[nb][e] * a.scale, dk[nb][e + 1] * a.scale),
+                      pack_bf16x2(dk[nb][e + 2] * a.scale, dk[nb][e + 3] * a.scale)};
+            *reinterpret_cast<u32x2*>(a.dv + at + 8 * n) =
+                u32x2{pack_bf16x2(dv[nb][e], dv[nb][e + 1]), pack_bf16x2(dv[nb][e + 2], dv[nb][e + 3])};
+        }
         return;
     }
-    const size_t all = size_t(a.T) * ldk;
-    float* pk = a.part + size_t(split) * all + row * ldk + kvh * D;
-    float* pv = pk + size_t(a.splits) * all;
+    // a share as the lanes hold it, whole kilobytes a store
+    f32x4* part = reinterpret_cast<f32x4*>(a.part) + share_of<D>(tile, kvh, split, a) + kw * 256 * NB + lane;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const int at = 32 * nb + 2 * e + 4 * h;
-            *reinterpret_cast<f32x4*>(pk + at) = f32x4{dk[nb][e], dk[nb][e + 1], dk[nb][e + 2], dk[nb][e + 3]};
-            *reinterpret_cast<f32x4*>(pv + at) = f32x4{dv[nb][e], dv[nb][e + 1], dv[nb][e + 2], dv[nb][e + 3]};
-        }
+    for (int n = 0; n < 4 * NB; ++n) {
+        const int nb = n / 4, e = n % 4 * 4;
+        part[64 * n] = f32x4{dk[nb][e], dk[nb][e + 1], dk[nb][e + 2], dk[nb][e + 3]};
+        part[64 * n + KW * 256 * NB] = f32x4{dv[nb][e], dv[nb][e + 1], dv[nb][e + 2], dv[nb][e + 3]};
+    }
 }
 
-// dk = RNbf(scale * sum of the shares), dv = RNbf(sum of the shares), in split order, over
-// the rows of the sequences; 4 elements a thread.
-__global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a, int ldk) {
-    const size_t all = size_t(a.T) * ldk;
-    int lo = 0, hi = a.T;
-    if (a.cu) {
-        lo = min(max(a.cu[0], 0), a.T);
-        hi = min(max(a.cu[a.n_seqs], lo), a.T);
-    }
-    const size_t i = (size_t(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (i < size_t(lo) * ldk || i >= size_t(hi) * ldk) return;
-    const float* p = a.part + (blockIdx.y ? size_t(a.splits) * all : 0) + i;
+// dk = RNbf(scale * sum of the shares), dv = RNbf(sum of the shares), in split order; four
+// of a lane's elements a thread, 2 KW NB workgroups a tile and kv head.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
+    constexpr int KW = kKeyWaves, NB = D / 32;
+    const int i = blockIdx.x % (2 * KW * NB), th = blockIdx.x / (2 * KW * NB);
+    const int is_dv = i / (KW * NB), kw = i / NB % KW, nb = i % NB;
+    const int tile = th / a.hkv, kvh = th % a.hkv, lane = threadIdx.x & 63, n = 4 * nb + (threadIdx.x >> 6);
+    Tile t;
+    if (!find_tile(a, 32 * KW, tile, t)) return;
+    const int key = t.row0 + 32 * kw + (lane & 31);
+    if (key >= t.len) return;
+    const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + share_of<D>(tile, kvh, 0, a) +
+                     (is_dv * KW + kw) * 256 * NB + 64 * n + lane;
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int z = 0; z < a.splits; ++z) s += *reinterpret_cast<const f32x4*>(p + size_t(z) * all);
-    const float f = blockIdx.y ? 1.0f : a.scale;
-    *reinterpret_cast<u32x2*>((blockIdx.y ? a.dv : a.dk) + i) =
+#pragma unroll 4
+    for (int z = 0; z < a.splits; ++z) s += p[size_t(z) * (2 * KW * 256 * NB)];
+    const float f = is_dv ? 1.0f : a.scale;
+    const size_t at = (size_t(t.begin) + key) * (a.hkv * D) + kvh * D + 8 * n + 4 * (lane >> 5);
+    *reinterpret_cast<u32x2*>((is_dv ? a.dv : a.dk) + at) =
         u32x2{pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f)};
 }
-
-constexpr int kWaves = 4;
 
 int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
     return cu ? T / bm + n_seqs : cdiv(T, bm);
 }
 
-// Shares of dk and dv. Two workgroups fit a CU: 512 keep the card busy when all are equally
-// long; under a causal mask the first keys have the most queries, and twice as many let the
-// short ones fill up behind the long ones (8192 tokens, 64/8 heads: 4.43 ms without shares,
-// 3.43 ms with 2; 2048 tokens, 40/8, not causal: 313 us with 512 workgroups, 334 with 1024).
+// Shares of dk and dv: one workgroup a CU where the keys alone give fewer (7B widths, 512
+// tokens: 45.9 us with 128 workgroups in all, 41.5 with 256). Under a causal mask the first
+// keys have the most queries, and two a CU let the short workgroups fill up behind the long
+// ones, as long as each still has 8 tiles or more of 64 queries to pay for its share (72B
+// widths, 4096 tokens: 1170 us with 256, 932 with 512; 512 tokens: 52.9 and 63.0; without a
+// mask, 2048 tokens of 40/8 heads: 311 and 323).
 int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int causal) {
-    const int64_t wgs = std::max(cdiv(T, 32 * kWaves), n_seqs) * hkv;
-    const int64_t most = std::min<int64_t>(16, G * cdiv(T, kTile));
-    return int(std::max<int64_t>(1, std::min<int64_t>(most, cdiv(causal ? 1024 : 512, wgs))));
+    const int64_t seqs = std::max<int64_t>(1, n_seqs);
+    const int64_t wgs = std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv;
+    const int64_t one = cdiv(256, wgs), two = cdiv(512, wgs);
+    const int64_t s = causal && G * T >= 128 * 8 * seqs * two ? two : one;
+    return int(std::max<int64_t>(1, std::min<int64_t>({s, 16, G * cdiv(T, 64)})));
 }
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
@@ -658,14 +733,15 @@ int check_attn(const char* fn, int64_t T, int64_t hq, int64_t hkv, int64_t D, co
 
 struct AttnBwdPlan {
     int splits;
-    size_t delta_bytes, part_bytes;
+    size_t stats_bytes, part_bytes;
 };
 
 AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs, int causal) {
     AttnBwdPlan p{};
+    const size_t tiles = size_t(T) / (32 * kKeyWaves) + std::max<int64_t>(1, n_seqs);
     p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv), causal);
-    p.delta_bytes = (size_t(T) * hq * 4 + 255) & ~size_t(255);
-    p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * T * hkv * D * 4 : 0;
+    p.stats_bytes = (size_t(T) * hq * 8 + 255) & ~size_t(255);
+    p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * tiles * 32 * kKeyWaves * hkv * D * 4 : 0;
     return p;
 }
 
@@ -675,30 +751,45 @@ int check_grid(const char* fn, int64_t wgs) {
     return NF4_OK;
 }
 
+// Whether tiles of 128 rows would not even give every CU its resident workgroups (2, 3 or 4
+// of head width 128, 64, 32) once; the kernels then take 64 rows a workgroup. Forward, us with
+// 128 and 64 rows: 512 tokens of 28/4 heads of 128 14.8, 12.2; 1024: 24.4, 21.0; 2048: 49.1,
+// 50.0; 2048 tokens of 40/8: 55.4, 64.3; 4096 tokens of 14/2 heads of 64: 57.4, 46.7.
+bool few_rows(const AttnArgs& a, int D) { return cdiv(a.T, 128) * a.hq < 256 * (D == 128 ? 2 : D == 64 ? 3 : 4); }
+
 template <int D>
 int run_fwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
-    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kWaves));
+    const bool few = few_rows(a, D);
+    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, few ? 64 : 128));
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
     if (int st = check_grid("nf4_attn_fwd", wgs); st != NF4_OK) return st;
-    hipLaunchKernelGGL((k_attn_fwd<D, kWaves>), dim3(unsigned(wgs)), dim3(64 * kWaves), 0, stream, a);
+    if (few)
+        hipLaunchKernelGGL((k_attn_fwd<D, 2, 2>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attn_fwd<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
     return check_launch("nf4_attn_fwd");
 }
 
 template <int D>
 int run_bwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
-    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kWaves));
+    const bool few = few_rows(a, D);
+    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, few ? 64 : 128));
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
-    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
-    if (int st = check_grid("nf4_attn_bwd", std::max(wgs, wgs_kv)); st != NF4_OK) return st;
-    hipLaunchKernelGGL((k_attn_bwd_dq<D, kWaves>), dim3(unsigned(wgs)), dim3(64 * kWaves), 0, stream, a);
-    hipLaunchKernelGGL((k_attn_bwd_dkv<D, kWaves>), dim3(unsigned(wgs_kv)), dim3(64 * kWaves), 0, stream, a);
-    if (a.splits > 1) {
-        const int ldk = a.hkv * D;
-        hipLaunchKernelGGL(k_attn_bwd_join, dim3(unsigned(cdiv(int64_t(a.T) * ldk, 1024)), 2), dim3(256), 0, stream, a,
-                           ldk);
-    }
+    if (int st = check_grid("nf4_attn_bwd", wgs); st != NF4_OK) return st;
+    const int kv_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kKeyWaves));
+    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(kv_tiles) * a.splits);
+    if (int st = check_grid("nf4_attn_bwd", wgs_kv); st != NF4_OK) return st;
+    if (few)
+        hipLaunchKernelGGL((k_attn_bwd_dq<D, 2, 2>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
+    a.tiles = kv_tiles;
+    hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
+    if (a.splits > 1)
+        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(kv_tiles * a.hkv * (kKeyWaves * D / 16))), dim3(256), 0,
+                           stream, a);
     return check_launch("nf4_attn_bwd");
 }
 
@@ -732,7 +823,7 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
         (head_dim != 32 && head_dim != 64 && head_dim != 128))
         return 0;
     const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 1);  // never fewer shares than without a mask
-    return p.delta_bytes + p.part_bytes;
+    return p.stats_bytes + p.part_bytes;
 }
 
 int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
@@ -747,15 +838,15 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
         !aligned16(dk) || !aligned16(dv) || !lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
         return fail(NF4_E_ARG, "%s: tensors must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
     const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, causal);
-    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.delta_bytes + p.part_bytes)
+    if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.stats_bytes + p.part_bytes)
         return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
-                    p.delta_bytes + p.part_bytes, ws_bytes);
+                    p.stats_bytes + p.part_bytes, ws_bytes);
     AttnArgs a{};
     a.q = q, a.k = k, a.v = v, a.o = o, a.dO = dO, a.lse_in = lse, a.dq = dq, a.dk = dk, a.dv = dv, a.cu = cu_seqlens;
     a.T = int(T), a.n_seqs = int(n_seqs), a.hq = int(hq), a.hkv = int(hkv), a.causal = causal, a.scale = scale;
     a.splits = p.splits;
-    a.delta = static_cast<float*>(ws);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.delta_bytes);
+    a.stats = static_cast<float*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.stats_bytes);
     hipStream_t s = static_cast<hipStream_t>(stream);
     return head_dim == 128 ? run_bwd<128>(a, s) : head_dim == 64 ? run_bwd<64>(a, s) : run_bwd<32>(a, s);
 }

@@ -224,24 +224,24 @@ def test_graph_replays_equal_eager(gpu_lib):
 
 
 def test_offsets_past_32_bits(gpu_lib):
-    """The last rows of tensors over 4 GiB (q, o, do, dq) equal a call on those rows alone."""
+    """The last rows of tensors over 4 GiB (q, o, do, dq) give the bits of the same sequences
+    at the front of the same tensors."""
     lib, d, hq, hkv, t, n = gpu_lib, 128, 64, 8, 270000, 300
-    small = {k: to_dev_bf16(v) for k, v in _case(n, hq, hkv, d).items()}
-    big = {k: torch.empty(t, v.shape[1], dtype=torch.bfloat16, device="cuda") for k, v in small.items()}
+    big = {}
+    for k, v in _case(n, hq, hkv, d).items():
+        v = to_dev_bf16(v)
+        big[k] = torch.empty(t, v.shape[1], dtype=torch.bfloat16, device="cuda")
+        big[k][:n], big[k][t - n:] = v, v
     assert big["q"].numel() * 2 > 1 << 32
-    for k in big:
-        big[k][t - n:] = small[k]
-    cu = torch.tensor([t - n, t - 100, t], dtype=torch.int32).cuda()
-    o, lse = lib.attn_fwd(big["q"], big["k"], big["v"], d, cu)
-    g = lib.attn_bwd(big["q"], big["k"], big["v"], o, lse, big["do"], d, cu)
-    cu = torch.tensor([0, n - 100, n], dtype=torch.int32).cuda()
-    o2, lse2 = lib.attn_fwd(small["q"], small["k"], small["v"], d, cu)
-    g2 = lib.attn_bwd(small["q"], small["k"], small["v"], o2, lse2, small["do"], d, cu)
+    res = []
+    for first in (0, t - n):
+        cu = torch.tensor([first, first + n - 100, first + n], dtype=torch.int32).cuda()
+        o, lse = lib.attn_fwd(big["q"], big["k"], big["v"], d, cu)
+        g = lib.attn_bwd(big["q"], big["k"], big["v"], o, lse, big["do"], d, cu)
+        res.append([x[first:first + n].clone() for x in (o, *g)] + [lse[:, first:first + n].clone()])
     torch.cuda.synchronize()
-    assert torch.equal(o[t - n:], o2) and torch.equal(lse[:, t - n:], lse2)
-    assert torch.equal(g[0][t - n:], g2[0])
-    for a, b in zip(g[1:], g2[1:]):              # other sizes may split the sums elsewhere
-        assert torch.allclose(a[t - n:].float(), b.float(), rtol=2.0 ** -7, atol=1e-4 * float(b.float().abs().max()))
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+    assert all(torch.isfinite(a.float()).all() and a.any() for a in res[0])
 
 
 def test_python_refusals(gpu_lib):
