@@ -1,9 +1,12 @@
 // Global gradient norm over many tensors, and clipping: with all the elements g of a list,
 //   n = sqrt(sum g^2),   out = g * min(1, max_norm / (n + 10^-6)).
 // Memory bound: g is read for the norm, then read and written for the scaling (not at all
-// where it is in place and nothing has to be scaled). Squares and their sums are fp64, at
-// the full rate of the vector ALUs beside these loads: no overflow or underflow for any
-// fp32 gradient, and sums over 10^9 elements stay exact far below the fp32 result's
+// where it is in place and nothing has to be scaled). The scaling goes from the last element
+// to the first, so that it finds in the last-level cache what the norm read last; in lists
+// larger than that cache the rest is read and the outputs are written past it: 842 MB of fp32
+// (1120 tensors) 497 -> 422 us, 6.0 TB/s of the three passes' bytes. Squares and their sums
+// are fp64, at the full rate of the vector ALUs beside these loads: no overflow or underflow
+// for any fp32 gradient, and sums over 10^9 elements stay exact far below the fp32 result's
 // rounding. No atomics: every workgroup leaves one fp64 share, and every workgroup of the
 // scaling launch sums the shares itself, in the same order, instead of a third launch.
 #include <algorithm>
@@ -20,8 +23,8 @@ namespace nf4 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxShares = 2048;
-constexpr size_t kChunkBytes = 65536;
+constexpr int kMaxShares = 1024;
+constexpr double kCacheBytes = 192e6;  // of the 256 MB last-level cache, what a pass leaves to the next
 
 // One piece of one tensor; pieces of a list cover its elements once. kWide pieces start
 // 16-byte aligned in both buffers.
@@ -56,28 +59,42 @@ __device__ __forceinline__ double sq16(u32x4 v, bool bf16) {
     return s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_grad_norm(const Chunk* __restrict__ chunks, int n,
+// Non-temporal for what the caches would not keep until it is wanted again; at compile time,
+// a choice at run time beside each access cost the gain.
+template <bool NT>
+__device__ __forceinline__ u32x4 load16(const u32x4* p) {
+    return NT ? __builtin_nontemporal_load(p) : *p;
+}
+
+template <bool NT>
+__device__ __forceinline__ double chunk_sum(const Chunk ch) {
+    const bool bf16 = ch.flags & kBf16;
+    const uint32_t per = bf16 ? 8 : 4;
+    const uint32_t wide = (ch.flags & kWide) ? ch.count / per : 0;
+    const u32x4* p = static_cast<const u32x4*>(ch.in);
+    double sum = 0.0;
+    uint32_t i = threadIdx.x;
+    for (; i + 3 * kThreads < wide; i += 4 * kThreads) {
+        u32x4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = load16<NT>(p + i + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) sum += sq16(v[u], bf16);
+    }
+    for (; i < wide; i += kThreads) sum += sq16(p[i], bf16);
+    for (uint32_t e = wide * per + threadIdx.x; e < ch.count; e += kThreads)
+        sum += sq(bf16 ? bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]) : static_cast<const float*>(ch.in)[e]);
+    return sum;
+}
+
+// Pieces below `stream` are read past the caches, so that these hold the others when the
+// scaling launch starts there.
+__global__ __launch_bounds__(kThreads) void k_grad_norm(const Chunk* __restrict__ chunks, int n, int stream,
                                                         double* __restrict__ shares) {
     __shared__ double red[4];
     double sum = 0.0;
-    for (int c = blockIdx.x; c < n; c += gridDim.x) {
-        const Chunk ch = chunks[c];
-        const bool bf16 = ch.flags & kBf16;
-        const uint32_t per = bf16 ? 8 : 4;
-        const uint32_t wide = (ch.flags & kWide) ? ch.count / per : 0;
-        const u32x4* p = static_cast<const u32x4*>(ch.in);
-        uint32_t i = threadIdx.x;
-        for (; i + 3 * kThreads < wide; i += 4 * kThreads) {
-            u32x4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = p[i + u * kThreads];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) sum += sq16(v[u], bf16);
-        }
-        for (; i < wide; i += kThreads) sum += sq16(p[i], bf16);
-        for (uint32_t e = wide * per + threadIdx.x; e < ch.count; e += kThreads)
-            sum += sq(bf16 ? bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]) : static_cast<const float*>(ch.in)[e]);
-    }
+    for (int c = blockIdx.x; c < n; c += gridDim.x)
+        sum += c < stream ? chunk_sum<true>(chunks[c]) : chunk_sum<false>(chunks[c]);
     sum = block_sum(sum, red);
     if (threadIdx.x == 0) shares[blockIdx.x] = sum;
 }
@@ -93,11 +110,41 @@ __device__ __forceinline__ u32x4 scale16(u32x4 v, float f, bool bf16) {
     return v;
 }
 
-// The norm from the shares (written by workgroup 0); then, when `scale`, the pieces. A norm
-// that is not finite scales by 1: the caller sees it in *norm.
+template <bool LOAD_NT, bool STORE_NT>
+__device__ __forceinline__ void chunk_scale(const Chunk ch, float f) {
+    const bool bf16 = ch.flags & kBf16;
+    const uint32_t per = bf16 ? 8 : 4;
+    const uint32_t wide = (ch.flags & kWide) ? ch.count / per : 0;
+    const u32x4* p = static_cast<const u32x4*>(ch.in);
+    u32x4* d = static_cast<u32x4*>(ch.out);
+    uint32_t i = threadIdx.x;
+    for (; i + 3 * kThreads < wide; i += 4 * kThreads) {
+        u32x4 v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = load16<LOAD_NT>(p + i + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const u32x4 w = scale16(v[u], f, bf16);
+            if constexpr (STORE_NT)
+                __builtin_nontemporal_store(w, d + i + u * kThreads);
+            else
+                d[i + u * kThreads] = w;
+        }
+    }
+    for (; i < wide; i += kThreads) d[i] = scale16(p[i], f, bf16);
+    for (uint32_t e = wide * per + threadIdx.x; e < ch.count; e += kThreads) {
+        if (bf16)
+            static_cast<uint16_t*>(ch.out)[e] = bf16_bits(bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]) * f);
+        else
+            static_cast<float*>(ch.out)[e] = static_cast<const float*>(ch.in)[e] * f;
+    }
+}
+
+// The norm from the shares (written by workgroup 0); then, when `scale`, the pieces, from the
+// last one on. A norm that is not finite scales by 1: the caller sees it in *norm.
 __global__ __launch_bounds__(kThreads) void k_grad_scale(const Chunk* __restrict__ chunks, int n,
                                                          const double* __restrict__ shares, int n_shares,
-                                                         float max_norm, int scale, int in_place,
+                                                         float max_norm, int scale, int in_place, int stream,
                                                          float* __restrict__ norm) {
     __shared__ double red[4];
     double sum = 0.0;
@@ -109,42 +156,26 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const Chunk* __restrict
     const bool clip = q < 1.0 && total < __builtin_inf();
     if (in_place && !clip) return;
     const float f = clip ? float(q) : 1.0f;
-    for (int c = blockIdx.x; c < n; c += gridDim.x) {
-        const Chunk ch = chunks[c];
-        const bool bf16 = ch.flags & kBf16;
-        const uint32_t per = bf16 ? 8 : 4;
-        const uint32_t wide = (ch.flags & kWide) ? ch.count / per : 0;
-        const u32x4* p = static_cast<const u32x4*>(ch.in);
-        u32x4* d = static_cast<u32x4*>(ch.out);
-        uint32_t i = threadIdx.x;
-        for (; i + 3 * kThreads < wide; i += 4 * kThreads) {
-            u32x4 v[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) v[u] = p[i + u * kThreads];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) d[i + u * kThreads] = scale16(v[u], f, bf16);
-        }
-        for (; i < wide; i += kThreads) d[i] = scale16(p[i], f, bf16);
-        for (uint32_t e = wide * per + threadIdx.x; e < ch.count; e += kThreads) {
-            if (bf16)
-                static_cast<uint16_t*>(ch.out)[e] = bf16_bits(bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]) * f);
-            else
-                static_cast<float*>(ch.out)[e] = static_cast<const float*>(ch.in)[e] * f;
-        }
+    int c = n - 1 - int(blockIdx.x);
+    if (stream == 0) {
+        for (; c >= 0; c -= gridDim.x) chunk_scale<false, false>(chunks[c], f);
+        return;
     }
+    for (; c >= stream; c -= gridDim.x) chunk_scale<false, true>(chunks[c], f);
+    for (; c >= 0; c -= gridDim.x) chunk_scale<true, true>(chunks[c], f);
 }
 
 size_t elem_bytes(int dtype) { return dtype == NF4_DTYPE_BF16 ? 2 : 4; }
 
 // The pieces of one tensor: a short head up to the first 16-byte boundary that both buffers
-// share, then kChunkBytes at a time; without such a boundary narrow pieces throughout.
+// share, then piece_bytes at a time; without such a boundary narrow pieces throughout.
 template <typename F>
-void pieces(const nf4_grad_tensor& t, F&& emit) {
+void pieces(const nf4_grad_tensor& t, size_t piece_bytes, F&& emit) {
     const size_t es = elem_bytes(t.dtype);
     const uint32_t type = t.dtype == NF4_DTYPE_BF16 ? kBf16 : 0;
     const uintptr_t a = reinterpret_cast<uintptr_t>(t.grad), b = reinterpret_cast<uintptr_t>(t.out);
     const bool wide = (a - b) % 16 == 0;
-    const int64_t step = int64_t(kChunkBytes / es);
+    const int64_t step = int64_t(piece_bytes / es);
     int64_t at = 0;
     auto put = [&](int64_t count, uint32_t flags) {
         emit(Chunk{static_cast<const char*>(t.grad) + at * es, static_cast<char*>(t.out) + at * es, uint32_t(count),
@@ -153,6 +184,18 @@ void pieces(const nf4_grad_tensor& t, F&& emit) {
     };
     if (wide && a % 16 != 0 && t.count > 0) put(std::min<int64_t>(t.count, int64_t((16 - a % 16) / es)), type);
     while (at < t.count) put(std::min(step, t.count - at), type | (wide ? kWide : 0));
+}
+
+size_t all_bytes(const nf4_grad_tensor* tensors, int n) {
+    size_t all = 0;
+    for (int i = 0; i < n; ++i) all += size_t(tensors[i].count) * elem_bytes(tensors[i].dtype);
+    return all;
+}
+
+// 64 KB, or less where that would give fewer than about 1024 pieces: the 14 tensors of one 7B
+// layer in bf16 (2.9 MB) take 12.4 us in 64 KB pieces, 7.6 us in 4 KB ones.
+size_t piece_of(size_t all) {
+    return std::min<size_t>(65536, std::max<size_t>(4096, (all / 1024 + 4095) & ~size_t(4095)));
 }
 
 int check_tensors(const char* fn, const nf4_grad_tensor* tensors, int n) {
@@ -180,6 +223,7 @@ struct nf4_grad_list {
     const nf4::Chunk* table;
     int n;         // pieces
     int in_place;  // every tensor's out is its grad
+    int stream;    // first pieces that the caches cannot hold from one launch to the next
 };
 
 using namespace nf4;
@@ -188,9 +232,10 @@ extern "C" {
 
 size_t nf4_grad_list_table(const nf4_grad_tensor* tensors, int n) {
     if (check_tensors("nf4_grad_list_table", tensors, n) != NF4_OK) return 0;
+    const size_t piece = piece_of(all_bytes(tensors, n));
     size_t pieces_all = 1;
     for (int i = 0; i < n; ++i)
-        pieces_all += size_t(tensors[i].count) * elem_bytes(tensors[i].dtype) / kChunkBytes + 2;
+        pieces_all += size_t(tensors[i].count) * elem_bytes(tensors[i].dtype) / piece + 2;
     return pieces_all * sizeof(Chunk);
 }
 
@@ -214,6 +259,7 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
         std::vector<Range> ranges;
         std::vector<Chunk> chunks;
         int in_place = 1;
+        const size_t all = all_bytes(tensors, n), piece = piece_of(all);
         for (int i = 0; i < n; ++i) {
             const nf4_grad_tensor& t = tensors[i];
             if (t.count == 0) continue;
@@ -224,7 +270,7 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
                 ranges.push_back({g, g + bytes, false});
                 in_place = 0;
             }
-            pieces(t, [&](const Chunk& c) { chunks.push_back(c); });
+            pieces(t, piece, [&](const Chunk& c) { chunks.push_back(c); });
         }
         std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
         uintptr_t written = 0, read = 0;
@@ -241,7 +287,8 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
             if (e == hipSuccess) e = hipStreamSynchronize(s);  // the source is this call's own
             if (e != hipSuccess) return fail(NF4_E_HIP, "%s: %s", fn, hipGetErrorString(e));
         }
-        *out = new nf4_grad_list{static_cast<const Chunk*>(table), int(chunks.size()), in_place};
+        *out = new nf4_grad_list{static_cast<const Chunk*>(table), int(chunks.size()), in_place,
+                                 double(all) > kCacheBytes ? int(double(chunks.size()) * (1.0 - kCacheBytes / double(all))) : 0};
     } catch (const std::bad_alloc&) {
         return fail(NF4_E_OOM, "%s: out of host memory", fn);
     }
@@ -268,9 +315,10 @@ static int grad_run(const char* fn, const nf4_grad_list* list, float max_norm, i
     double* shares = static_cast<double*>(ws);
     const int wgs = std::min(list->n, kMaxShares);
     if (wgs)
-        hipLaunchKernelGGL(k_grad_norm, dim3(unsigned(wgs)), dim3(kThreads), 0, s, list->table, list->n, shares);
+        hipLaunchKernelGGL(k_grad_norm, dim3(unsigned(wgs)), dim3(kThreads), 0, s, list->table, list->n,
+                           list->stream, shares);
     hipLaunchKernelGGL(k_grad_scale, dim3(unsigned(scale && wgs ? wgs : 1)), dim3(kThreads), 0, s, list->table, list->n,
-                       shares, wgs, max_norm, scale, list->in_place, norm);
+                       shares, wgs, max_norm, scale, list->in_place, list->stream, norm);
     return check_launch(fn);
 }
 

@@ -515,13 +515,18 @@ def _device(t, *more) -> int:
     return dev
 
 
+# torch's current stream as the raw handle, without the Stream object around it (0.1 us against 1.1)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _enqueue(dev: int, stream, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current, on its current stream by default."""
     if dev != torch.cuda.current_device():
         with torch.cuda.device(dev):
             return _enqueue(dev, stream, fn, *args)
     if stream is None:
-        raw_stream = torch.cuda.current_stream(dev).cuda_stream
+        raw_stream = _current_raw_stream(dev)
     else:
         raw_stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     _check(fn(*args, raw_stream))
