@@ -698,17 +698,22 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
 }
 
 // Shares of dk and dv: one workgroup a CU where the keys alone give fewer (7B widths, 512
-// tokens: 45.9 us with 128 workgroups in all, 41.5 with 256). Under a causal mask the first
-// keys have the most queries, and two a CU let the short workgroups fill up behind the long
-// ones, as long as each still has 8 tiles or more of 64 queries to pay for its share (72B
-// widths, 4096 tokens: 1170 us with 256, 932 with 512; 512 tokens: 52.9 and 63.0; without a
-// mask, 2048 tokens of 40/8 heads: 311 and 323).
+// tokens: 45.9 us with 128 workgroups in all, 41.5 with 256), of two tiles of 64 queries or
+// more each (256 tokens: 33.3 us with one tile a share, 29.3 with two), and none for a
+// handful of tiles, which cost less than the launch that joins shares. Under a causal mask the
+// first keys have the most queries, and two workgroups a CU let the short ones fill up behind
+// the long ones, as long as each still has 8 tiles or more (72B widths, 4096 tokens: 1170 us
+// with 256, 932 with 512; 512 tokens: 52.9 and 63.0; without a mask, 2048 tokens of 40/8
+// heads: 311 and 323).
 int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int causal) {
     const int64_t seqs = std::max<int64_t>(1, n_seqs);
     const int64_t wgs = std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv;
     const int64_t one = cdiv(256, wgs), two = cdiv(512, wgs);
-    const int64_t s = causal && G * T >= 128 * 8 * seqs * two ? two : one;
-    return int(std::max<int64_t>(1, std::min<int64_t>({s, 16, G * cdiv(T, 64)})));
+    const int64_t len = cdiv(T, seqs * 64);                        // tiles of an average sequence
+    const int64_t tiles = G * (causal ? cdiv(len + 1, 2) : len);  // an average workgroup's
+    if (tiles < 8) return 1;
+    const int64_t s = causal && tiles >= 8 * two ? two : one;
+    return int(std::max<int64_t>(1, std::min<int64_t>({s, 16, tiles / 2})));
 }
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
@@ -822,8 +827,8 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
     if (T <= 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024 || n_seqs < 0 ||
         (head_dim != 32 && head_dim != 64 && head_dim != 128))
         return 0;
-    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 1);  // never fewer shares than without a mask
-    return p.stats_bytes + p.part_bytes;
+    const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 1);  // enough with and without a mask
+    return p.stats_bytes + std::max(p.part_bytes, plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 0).part_bytes);
 }
 
 int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
