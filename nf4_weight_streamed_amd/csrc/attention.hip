@@ -524,7 +524,7 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
     return ((size_t(tile) * a.hkv + kvh) * a.splits + split) * (2 * kKeyWaves * 8 * D);
 }
 
-// One workgroup: 8 waves, KW blocks of 32 keys of one kv head x QW = 8 / KW. K fragments stay
+// One workgroup: 8 waves, KW blocks of 32 keys of one kv head x QW. K fragments stay
 // in registers, V in LDS (both in registers would leave room for one wave a SIMD only); the
 // queries of the G heads pass through LDS in tiles of 32 QW (Q, dO, lse, delta), 32 to each of
 // the QW waves of a key block, whose sums meet at the end. Per 32 queries S = Q K^T,
@@ -533,7 +533,7 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
 template <int D>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
-    constexpr int KW = kKeyWaves, QW = 8 / KW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = 32 * QW;
+    constexpr int KW = kKeyWaves, QW = 2, W = KW * QW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = 32 * QW;
     __shared__ __align__(1024) char sV[BM * 2 * D];
     // a tile's Q, and its dO with the rows' lse * log2 e and delta behind it
     constexpr int QB = BQ * 2 * D, SB = BQ < 64 ? 256 : BQ * 4, DB = QB + 2 * SB;
@@ -567,10 +567,10 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
         const uint32_t o = uint32_t(32 * kw + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
 #pragma unroll
         for (int s = 0; s < KS; ++s) kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
-        TileCopy<D, BM, 8>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
+        TileCopy<D, BM, W>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
     }
     const LdsMap<D> map(lane);
-    const TileCopy<D, BQ, 8> copy(wave, lane, ldq);
+    const TileCopy<D, BQ, W> copy(wave, lane, ldq);
     int next = tile_hi - i0 / G, g_next = i0 % G;  // of the tile to be staged
     auto stage = [&](int, char* q, char* d) {
         const int q0 = next * BQ, head = kvh * G + g_next, rows = t.len - q0;
@@ -632,16 +632,13 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
     };
     double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute);
     wait_vmcnt<0>();  // without a tile to use it, V's copy is still under way
-    // The sums of a key block: waves qw > 0 hand theirs to wave 0 through the staging buffers,
-    // dk first, then dv, added in the order of qw.
+    // The sums of a key block: its second wave hands them to the first through the staging
+    // buffers, dk first, then dv.
     auto meet = [&](f32x16(&x)[NB]) {
         __syncthreads();
-        if (qw > 0) put_share(share_slot<D>((qw - 1) * KW + kw, QB, sQ0, sQ1, sD0, sD1, lane), x);
+        if (qw > 0) put_share(share_slot<D>(kw, QB, sQ0, sQ1, sD0, sD1, lane), x);
         __syncthreads();
-        if (qw == 0) {
-            for (int q = 1; q < QW; ++q)
-                add_share(x, share_slot<D>((q - 1) * KW + kw, QB, sQ0, sQ1, sD0, sD1, lane), 1.0f, 1.0f);
-        }
+        if (qw == 0) add_share(x, share_slot<D>(kw, QB, sQ0, sQ1, sD0, sD1, lane), 1.0f, 1.0f);
     };
     meet(dk);
     meet(dv);
@@ -697,23 +694,32 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
     return cu ? T / bm + n_seqs : cdiv(T, bm);
 }
 
-// Shares of dk and dv: one workgroup a CU where the keys alone give fewer (7B widths, 512
-// tokens: 45.9 us with 128 workgroups in all, 41.5 with 256), of two tiles of 64 queries or
-// more each (256 tokens: 33.3 us with one tile a share, 29.3 with two), and none for a
-// handful of tiles, which cost less than the launch that joins shares. Under a causal mask the
-// first keys have the most queries, and two workgroups a CU let the short ones fill up behind
-// the long ones, as long as each still has 8 tiles or more (72B widths, 4096 tokens: 1170 us
-// with 256, 932 with 512; 512 tokens: 52.9 and 63.0; without a mask, 2048 tokens of 40/8
-// heads: 311 and 323).
-int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int causal) {
+// Shares of dk and dv: the power of two up to 16 that is expected to take the least time, more
+// of them only for a gain of 3 %. A CU holds one workgroup of the dk/dv kernel, so s shares of
+// each run in rounds of 256. A tile of 64 queries takes about 1.9 us (head width 128), starting
+// and ending a workgroup 5 us, and the shares are written and read again, in a launch of 4 us
+// more, at about 4.5 TB/s, or twice that while all of them fit the caches. Under a causal
+// mask, and among sequences of different lengths, the longest workgroup has about twice the
+// average's tiles; the long ones start first, which leaves a sixth of a workgroup at the end.
+// Measured (us, whole backward): 8192 tokens of 64/8 heads 3545 with one share, 3618 with 2;
+// 4096: 1170 with 1, 932 with 2; 512 of 28/4: 43.1 with 8, 39.5 with 15; 1408 of 8/8, no mask:
+// 70.5, 64.9 and 73.0 with 1, 2 and 4; of 16/16 heads of 64: 55.1 and 68.7 with 1 and 2.
+int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int D, int causal) {
     const int64_t seqs = std::max<int64_t>(1, n_seqs);
-    const int64_t wgs = std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv;
-    const int64_t one = cdiv(256, wgs), two = cdiv(512, wgs);
-    const int64_t len = cdiv(T, seqs * 64);                        // tiles of an average sequence
-    const int64_t tiles = G * (causal ? cdiv(len + 1, 2) : len);  // an average workgroup's
-    if (tiles < 8) return 1;
-    const int64_t s = causal && tiles >= 8 * two ? two : one;
-    return int(std::max<int64_t>(1, std::min<int64_t>({s, 16, tiles / 2})));
+    const double wgs = double(std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv);
+    const int64_t len = cdiv(T, seqs * 64);                              // tiles of an average sequence
+    const double tiles = double(G) * (causal ? (len + 1) * 0.5 : len);  // an average workgroup's
+    const double tile_us = 1.9 * D / 128, ends_us = 3 + 2.0 * D / 128, share_bytes = wgs * (2 * 32 * kKeyWaves * D * 4);
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 16 && (s == 1 || tiles >= 1.9 * s); s *= 2) {
+        const double one = tiles / s * tile_us, rounds = wgs * s / 256, bytes = s * share_bytes;
+        double us = std::ceil(rounds) * (one + ends_us);
+        if (causal || seqs > 1) us = std::max(2 * one + ends_us, rounds * (one + ends_us) + one / 6);
+        if (s > 1) us += 4 + 2 * bytes / (bytes < 64e6 ? 9e6 : 4.5e6);
+        if (s == 1 || us < 0.97 * least) best = s, least = us;
+    }
+    return best;
 }
 
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) % 16) == 0; }
@@ -744,7 +750,7 @@ struct AttnBwdPlan {
 AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs, int causal) {
     AttnBwdPlan p{};
     const size_t tiles = size_t(T) / (32 * kKeyWaves) + std::max<int64_t>(1, n_seqs);
-    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv), causal);
+    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv), int(D), causal);
     p.stats_bytes = (size_t(T) * hq * 8 + 255) & ~size_t(255);
     p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * tiles * 32 * kKeyWaves * hkv * D * 4 : 0;
     return p;
