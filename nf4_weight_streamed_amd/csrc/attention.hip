@@ -42,7 +42,7 @@ struct AttnArgs {
     uint16_t *out, *dq, *dk, *dv;
     float *lse, *stats, *part;  // stats [2][hq][T]: lse * log2 e, delta; part: fp32 shares of dk and dv
     const int32_t* cu;
-    int T, n_seqs, hq, hkv, causal, tiles, splits;
+    int T, n_seqs, hq, hkv, causal, tiles, q_tiles, splits;
     float scale;
 };
 
@@ -401,16 +401,15 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 // As the forward, with dO beside Q in registers: per 64-key tile S^T = K Q^T,
 // dP^T = V dO^T, dS^T in place, dq^T += K^T dS^T. delta is formed here first (the dk/dv
 // kernel behind this one reads it). R, C and B as in the forward.
-template <int D, int R, int C>
-__global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
+template <int D, int R, int C, bool STATS>
+__device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* sK0, char* sV0, char* sK1, char* sV1) {
     constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
-    __shared__ __align__(1024) char sK0[kTile * 2 * D], sV0[kTile * 2 * D], sK1[kTile * 2 * D], sV1[kTile * 2 * D];
     const int G = a.hq / a.hkv;
     int kvh, item;
-    if (!pick_item(blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
+    if (!pick_item(block, a.hkv, a.q_tiles * G, kvh, item)) return;
     const int head = kvh * G + item % G;
     Tile t;
-    if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;
+    if (!find_tile(a, BM, a.q_tiles - 1 - item / G, t)) return;
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
     const int wr = wave % R, wc = C == 1 ? 0 : wave / R, b0 = B * wc;
     const int ldq = a.hq * D, ldk = a.hkv * D;
@@ -447,7 +446,7 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
     if (q_row < t.len) {
         const size_t at = size_t(head) * a.T + t.begin + q_row;
         lse2 = a.lse_in[at] * kLog2e;
-        if (h == 0 && wc == 0) {
+        if (STATS && h == 0 && wc == 0) {
             a.stats[at] = lse2;
             a.stats[size_t(a.hq) * a.T + at] = delta;
         }
@@ -497,12 +496,12 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
     double_buffered(0, n, sK0, sV0, sK1, sV1, stage, compute);
     if constexpr (C > 1) {  // the waves of a row hand their shares to its first
         __syncthreads();
-        if (wc > 0) put_share(share_slot<D>((wc - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), acc);
+        if (wc > 0) put_share(share_slot<D>((wc - 1) * R + wr, kTile * 2 * D, sK0, sV0, sK1, sV1, lane), acc);
         __syncthreads();
         if (wc > 0) return;
 #pragma unroll
         for (int i = 1; i < C; ++i)
-            add_share(acc, share_slot<D>((i - 1) * R + wr, sizeof sK0, sK0, sV0, sK1, sV1, lane), 1.0f, 1.0f);
+            add_share(acc, share_slot<D>((i - 1) * R + wr, kTile * 2 * D, sK0, sV0, sK1, sV1, lane), 1.0f, 1.0f);
     }
     if (q_row < t.len) {
         uint16_t* out = a.dq + (size_t(t.begin) + q_row) * ldq + head * D;
@@ -514,6 +513,12 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
                     u32x2{pack_bf16x2(acc[nb][e] * a.scale, acc[nb][e + 1] * a.scale),
                           pack_bf16x2(acc[nb][e + 2] * a.scale, acc[nb][e + 3] * a.scale)};
     }
+}
+
+template <int D, int R, int C>
+__global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
+    __shared__ __align__(1024) char sK0[128 * D], sV0[128 * D], sK1[128 * D], sV1[128 * D];
+    bwd_dq<D, R, C, true>(a, blockIdx.x, sK0, sV0, sK1, sV1);
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
@@ -531,16 +536,22 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
 // dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
+// LDS of a dk/dv workgroup: V; two pairs of a tile's Q, and its dO with the rows' lse * log2 e
+// and delta behind it.
 template <int D>
-__global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
-    constexpr int KW = kKeyWaves, QW = 2, W = KW * QW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = 32 * QW;
-    __shared__ __align__(1024) char sV[BM * 2 * D];
-    // a tile's Q, and its dO with the rows' lse * log2 e and delta behind it
-    constexpr int QB = BQ * 2 * D, SB = BQ < 64 ? 256 : BQ * 4, DB = QB + 2 * SB;
-    __shared__ __align__(1024) char sQ0[QB], sD0[DB], sQ1[QB], sD1[DB];
+struct DkvLds {
+    static constexpr int QW = 2, BQ = 32 * QW, QB = BQ * 2 * D, SB = 256, DB = QB + 2 * SB, VB = 64 * kKeyWaves * D;
+};
+
+template <int D>
+__device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sV, char* sQ0, char* sD0, char* sQ1,
+                                        char* sD1) {
+    using L = DkvLds<D>;
+    constexpr int KW = kKeyWaves, QW = L::QW, W = KW * QW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = L::BQ;
+    constexpr int QB = L::QB, SB = L::SB;
     const int G = a.hq / a.hkv;
     int kvh, item;
-    if (!pick_item(blockIdx.x, a.hkv, a.tiles * a.splits, kvh, item)) return;
+    if (!pick_item(block, a.hkv, a.tiles * a.splits, kvh, item)) return;
     const int split = item % a.splits;
     Tile t;
     const int tile = item / a.splits;
@@ -667,6 +678,48 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
     }
 }
 
+template <int D>
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
+    using L = DkvLds<D>;
+    __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
+    bwd_dkv<D>(a, blockIdx.x, sV, sQ0, sD0, sQ1, sD1);
+}
+
+// Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
+// idle: the first q_wgs workgroups take 128 rows of dq each, with two waves a row. lse * log2 e
+// and delta come from k_attn_bwd_stats, since neither kind can wait for the other.
+template <int D>
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q_wgs) {
+    using L = DkvLds<D>;
+    __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
+    if (blockIdx.x < q_wgs)
+        bwd_dq<D, 4, 2, false>(a, blockIdx.x, sQ0, sD0, sQ1, sD1);
+    else
+        bwd_dkv<D>(a, blockIdx.x - q_wgs, sV, sQ0, sD0, sQ1, sD1);
+}
+
+// stats[0] = lse * log2 e, stats[1] = delta = do . o for every row and head: D / 8 lanes each.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_bwd_stats(AttnArgs a) {
+    constexpr int LN = D / 8;
+    const int64_t n = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LN, all = int64_t(a.T) * a.hq;
+    if (n >= all) return;  // whole groups of LN lanes
+    const int head = int(n % a.hq), x = threadIdx.x % LN;
+    const int64_t row = n / a.hq;
+    const bf16x8 d = as_bf16x8(*reinterpret_cast<const u32x4*>(a.dO + n * D + 8 * x));
+    const bf16x8 o = as_bf16x8(*reinterpret_cast<const u32x4*>(a.o + n * D + 8 * x));
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(float(d[e]), float(o[e]), s);
+#pragma unroll
+    for (int m = 1; m < LN; m *= 2) s += __shfl_xor(s, m, 64);
+    if (x == 0) {
+        const size_t at = size_t(head) * a.T + row;
+        a.stats[at] = a.lse_in[at] * kLog2e;
+        a.stats[size_t(a.hq) * a.T + at] = s;
+    }
+}
+
 // dk = RNbf(scale * sum of the shares), dv = RNbf(sum of the shares), in split order; four
 // of a lane's elements a thread, 2 KW NB workgroups a tile and kv head.
 template <int D>
@@ -694,30 +747,50 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
     return cu ? T / bm + n_seqs : cdiv(T, bm);
 }
 
-// Shares of dk and dv: the power of two up to 16 that is expected to take the least time, more
-// of them only for a gain of 3 %. A CU holds one workgroup of the dk/dv kernel, so s shares of
-// each run in rounds of 256. A tile of 64 queries takes about 1.9 us (head width 128), starting
-// and ending a workgroup 5 us, and the shares are written and read again, in a launch of 4 us
-// more, at about 4.5 TB/s, or twice that while all of them fit the caches. Under a causal
-// mask, and among sequences of different lengths, the longest workgroup has about twice the
-// average's tiles; the long ones start first, which leaves a sixth of a workgroup at the end.
-// Measured (us, whole backward): 8192 tokens of 64/8 heads 3545 with one share, 3618 with 2;
-// 4096: 1170 with 1, 932 with 2; 512 of 28/4: 43.1 with 8, 39.5 with 15; 1408 of 8/8, no mask:
-// 70.5, 64.9 and 73.0 with 1, 2 and 4; of 16/16 heads of 64: 55.1 and 68.7 with 1 and 2.
-int pick_splits(int64_t T, int64_t n_seqs, int hkv, int G, int D, int causal) {
+// Whether tiles of 128 rows would not even give every CU its resident workgroups (2, 3 or 4
+// of head width 128, 64, 32) once; the forward then takes 64 rows a workgroup. Us with 128 and
+// 64 rows: 512 tokens of 28/4 heads of 128 14.8, 12.2; 1024: 24.4, 21.0; 2048: 49.1, 50.0;
+// 2048 tokens of 40/8: 55.4, 64.3; 4096 tokens of 14/2 heads of 64: 57.4, 46.7.
+bool few_rows(int64_t T, int64_t hq, int64_t D) { return cdiv(T, 128) * hq < 256 * (D == 128 ? 2 : D == 64 ? 3 : 4); }
+
+// Whether the backward takes both kinds of workgroups in one launch: up to one and a half
+// workgroups of dq a CU. Us in two launches and in one: 512 tokens of 28/4 heads 39.8, 32.5;
+// 1024: 68.7, 60.8; 2048: 150.7, 164.7; 1408 tokens of 32/32 heads of 64: 92.1, 85.6; 4096 of
+// 14/2: 142.9, 148.1.
+bool one_launch(int64_t T, int64_t hq) { return cdiv(T, 128) * hq <= 384; }
+
+// Shares of dk and dv: the power of two up to 16 that is expected to take the least time. A CU
+// holds one workgroup of 8 waves, so the workgroups of a launch (with those of dq, where they
+// share it) run in rounds of 256. A tile of 64 queries takes about 1.9 us (head width 128),
+// one of 64 keys in dq half that, starting and ending a workgroup 5 us, or 8 when it stores a
+// share; the shares are written and read again, in a launch of 4 us more, at about 6 TB/s, or
+// 9 while the caches hold them all. Under a causal mask, and among sequences of different
+// lengths, the longest workgroup has about twice the average's tiles. Measured (us, whole
+// backward): 8192 tokens of 64/8 heads 3545 with one share, 3618 with 2; 4096: 1170 with 1, 932
+// with 2; 512 of 28/4: 40.6, 32.3 and 38.0 with 4, 8 and 16; 1408 of 8/8, no mask: 51.6 and
+// 65.0 with 1 and 2; 1408 of 4/4 heads of 64: 31.7, 29.0 and 32.7 with 1, 2 and 4.
+int pick_splits(int64_t T, int64_t n_seqs, int hq, int hkv, int D, int causal) {
     const int64_t seqs = std::max<int64_t>(1, n_seqs);
     const double wgs = double(std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv);
-    const int64_t len = cdiv(T, seqs * 64);                              // tiles of an average sequence
-    const double tiles = double(G) * (causal ? (len + 1) * 0.5 : len);  // an average workgroup's
-    const double tile_us = 1.9 * D / 128, ends_us = 3 + 2.0 * D / 128, share_bytes = wgs * (2 * 32 * kKeyWaves * D * 4);
+    const double dq_wgs = one_launch(T, hq) ? double(std::max(cdiv(T, 128), seqs) * hq) : 0.0;
+    const int64_t len = cdiv(T, seqs * 64);                    // tiles of an average sequence
+    const double avg = causal ? (len + 1) * 0.5 : double(len);  // that an average row or key meets
+    const double tiles = double(hq / hkv) * avg, tile_us = 1.9 * D / 128;
+    const double dq_us = 0.5 * tile_us * avg + 5, share_bytes = wgs * (2 * 32 * kKeyWaves * D * 4);
     int best = 1;
     double least = 0.0;
     for (int s = 1; s <= 16 && (s == 1 || tiles >= 1.9 * s); s *= 2) {
-        const double one = tiles / s * tile_us, rounds = wgs * s / 256, bytes = s * share_bytes;
-        double us = std::ceil(rounds) * (one + ends_us);
-        if (causal || seqs > 1) us = std::max(2 * one + ends_us, rounds * (one + ends_us) + one / 6);
-        if (s > 1) us += 4 + 2 * bytes / (bytes < 64e6 ? 9e6 : 4.5e6);
-        if (s == 1 || us < 0.97 * least) best = s, least = us;
+        const double ends_us = s == 1 ? 3 + 2.0 * D / 128 : 4 + 4.0 * D / 128;
+        const double run = tiles / s * tile_us, one = run + ends_us, bytes = s * share_bytes;
+        const double all = wgs * s + dq_wgs, rounds = std::ceil(all / 256);
+        double us;
+        if (causal || seqs > 1)  // many rounds even out, a few go by the average
+            us = std::max(one + run, rounds < 5 ? rounds * (wgs * s * one + dq_wgs * dq_us) / all
+                                                : (wgs * s * one + dq_wgs * dq_us) / 256 + run / 6);
+        else
+            us = rounds * std::max(one, dq_wgs > 0 ? dq_us : 0.0);
+        if (s > 1) us += 4 + 2 * bytes / (bytes < 128e6 ? 9e6 : 6e6);
+        if (s == 1 || us < 0.99 * least) best = s, least = us;
     }
     return best;
 }
@@ -750,7 +823,7 @@ struct AttnBwdPlan {
 AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs, int causal) {
     AttnBwdPlan p{};
     const size_t tiles = size_t(T) / (32 * kKeyWaves) + std::max<int64_t>(1, n_seqs);
-    p.splits = pick_splits(T, n_seqs, int(hkv), int(hq / hkv), int(D), causal);
+    p.splits = pick_splits(T, n_seqs, int(hq), int(hkv), int(D), causal);
     p.stats_bytes = (size_t(T) * hq * 8 + 255) & ~size_t(255);
     p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * tiles * 32 * kKeyWaves * hkv * D * 4 : 0;
     return p;
@@ -762,16 +835,10 @@ int check_grid(const char* fn, int64_t wgs) {
     return NF4_OK;
 }
 
-// Whether tiles of 128 rows would not even give every CU its resident workgroups (2, 3 or 4
-// of head width 128, 64, 32) once; the kernels then take 64 rows a workgroup. Forward, us with
-// 128 and 64 rows: 512 tokens of 28/4 heads of 128 14.8, 12.2; 1024: 24.4, 21.0; 2048: 49.1,
-// 50.0; 2048 tokens of 40/8: 55.4, 64.3; 4096 tokens of 14/2 heads of 64: 57.4, 46.7.
-bool few_rows(const AttnArgs& a, int D) { return cdiv(a.T, 128) * a.hq < 256 * (D == 128 ? 2 : D == 64 ? 3 : 4); }
-
 template <int D>
 int run_fwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
-    const bool few = few_rows(a, D);
+    const bool few = few_rows(a.T, a.hq, D);
     a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, few ? 64 : 128));
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
     if (int st = check_grid("nf4_attn_fwd", wgs); st != NF4_OK) return st;
@@ -785,21 +852,20 @@ int run_fwd(const AttnArgs& in, hipStream_t stream) {
 template <int D>
 int run_bwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
-    const bool few = few_rows(a, D);
-    a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, few ? 64 : 128));
-    const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
-    if (int st = check_grid("nf4_attn_bwd", wgs); st != NF4_OK) return st;
-    const int kv_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 32 * kKeyWaves));
-    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(kv_tiles) * a.splits);
-    if (int st = check_grid("nf4_attn_bwd", wgs_kv); st != NF4_OK) return st;
-    if (few)
-        hipLaunchKernelGGL((k_attn_bwd_dq<D, 2, 2>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
-    else
+    a.tiles = a.q_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 128));
+    const int64_t wgs = attn_grid(a.hkv, int64_t(a.q_tiles) * (a.hq / a.hkv));
+    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
+    if (int st = check_grid("nf4_attn_bwd", wgs + wgs_kv); st != NF4_OK) return st;
+    if (one_launch(a.T, a.hq)) {
+        hipLaunchKernelGGL(k_attn_bwd_stats<D>, dim3(unsigned(cdiv(int64_t(a.T) * a.hq * (D / 8), 256))), dim3(256), 0,
+                           stream, a);
+        hipLaunchKernelGGL(k_attn_bwd_both<D>, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
+    } else {
         hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
-    a.tiles = kv_tiles;
-    hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
+    }
     if (a.splits > 1)
-        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(kv_tiles * a.hkv * (kKeyWaves * D / 16))), dim3(256), 0,
+        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(a.tiles * a.hkv * (kKeyWaves * D / 16))), dim3(256), 0,
                            stream, a);
     return check_launch("nf4_attn_bwd");
 }

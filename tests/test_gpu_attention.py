@@ -13,6 +13,13 @@ from helpers import bits_of, f32_of, half_ulp_bf16, to_dev_bf16
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(scope="module", autouse=True)
+def stream_pair_first(gpu_lib):
+    """The library's compute/copy pair, made for the life of the process, before this file
+    makes streams and graphs: made later, the two may fall on one hardware queue."""
+    gpu_lib.pool_streams()
+
+
 def _bits(a):
     return torch.from_numpy(np.asarray(a, np.float32)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
 

@@ -8,6 +8,13 @@ import torch
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(scope="module", autouse=True)
+def stream_pair_first(gpu_lib):
+    """The library's compute/copy pair, made for the life of the process, before this file
+    makes streams and graphs: made later, the two may fall on one hardware queue."""
+    gpu_lib.pool_streams()
+
+
 def _tensors(sizes, seed=0, std=1.0):
     """fp32 and bf16 in turn, each cut from a larger buffer at an odd element offset."""
     g = torch.Generator(device="cuda")
