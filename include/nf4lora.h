@@ -328,8 +328,9 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
  *     n = sqrt( sum over all elements g of all tensors of g^2 )     (sums in fp64)
  *     out = RN( g * min(1, max_norm / (n + 1e-6)) )                 (RN to the tensor's type)
  * A list is made once over the gradient buffers of a training program and used every
- * step; the buffers must outlive it, and so must the table, device memory of the caller
- * that holds the list's description (nf4_grad_list_table() bytes, 256-byte aligned).
+ * step; the buffers and the table, device memory of the caller that holds the list's
+ * description (nf4_grad_list_table() bytes, 256-byte aligned), must outlive its calls, those
+ * of captured graphs among them.
  * nf4_grad_list_create copies the description there on `stream` and waits for the copy.
  *   tensors  HOST array of n descriptions (read during the call only); dtype bf16 or fp32,
  *            mixed freely; pointers aligned to their elements; count 0 allowed (pointers

@@ -532,6 +532,19 @@ def _enqueue(dev: int, stream, fn, *args) -> None:
     _check(fn(*args, raw_stream))
 
 
+def _as_stream(stream):
+    return stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+
+
+def _empty(shape, dtype, device, stream):
+    """torch.empty for a call on `stream`: memory of that stream's, since what the current
+    stream still has pending may use a block it has freed."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(_as_stream(stream)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def rope_inv_freq(head_dim: int, theta: float = 1e6, device="cuda") -> torch.Tensor:
     """theta^(-2i/head_dim), i < head_dim/2, fp64: the frequencies of plain rotary positions."""
     return float(theta) ** (-torch.arange(0, head_dim, 2, dtype=torch.float64, device=device) / head_dim)
@@ -546,8 +559,12 @@ def rope(q, k, head_dim: int, pos, inv_freq, sections=None, inverse: bool = Fals
         pos = pos.unsqueeze(0)
     sections = (head_dim // 2,) if sections is None else tuple(sections)
     hq, hkv = _head_count(q, "q", head_dim), 0 if k is None else _head_count(k, "k", head_dim)
-    q_out = torch.empty_like(q) if q_out is None else q_out
-    k_out = None if k is None else torch.empty_like(k) if k_out is None else k_out
+    if q_out is None:
+        q_out = _empty(q.shape, torch.bfloat16, q.device, stream)
+    if k is None:
+        k_out = None
+    elif k_out is None:
+        k_out = _empty(k.shape, torch.bfloat16, k.device, stream)
     _need(q, "q", torch.bfloat16, (t, hq * head_dim))
     _need(q_out, "q_out", torch.bfloat16, (t, hq * head_dim))
     if k is not None:
@@ -563,22 +580,25 @@ def rope(q, k, head_dim: int, pos, inv_freq, sections=None, inverse: bool = Fals
 
 
 def _head_count(x, name: str, head_dim: int) -> int:
-    if x.dim() != 2 or head_dim < 1 or x.shape[1] % head_dim:
-        raise ValueError(f"{name} must be [T, heads * {head_dim}], got {tuple(x.shape)}")
-    return x.shape[1] // head_dim
+    shape = x.shape
+    if len(shape) != 2 or head_dim < 1 or shape[1] % head_dim:
+        raise ValueError(f"{name} must be [T, heads * {head_dim}], got {tuple(shape)}")
+    return shape[1] // head_dim
 
 
 def _attn_args(q, k, v, head_dim, cu_seqlens, scale):
-    t = q.shape[0]
+    """(T, hq, hkv, n_seqs, scale), q's shape and k's, after checking the inputs."""
     hq, hkv = _head_count(q, "q", head_dim), _head_count(k, "k", head_dim)
-    _need(q, "q", torch.bfloat16, (t, hq * head_dim))
-    _need(k, "k", torch.bfloat16, (t, hkv * head_dim))
-    _need(v, "v", torch.bfloat16, (t, hkv * head_dim))
+    t = q.shape[0]
+    q_shape, k_shape = (t, hq * head_dim), (t, hkv * head_dim)
+    _need(q, "q", torch.bfloat16, q_shape)
+    _need(k, "k", torch.bfloat16, k_shape)
+    _need(v, "v", torch.bfloat16, k_shape)
     n_seqs = 0
     if cu_seqlens is not None:
         n_seqs = cu_seqlens.numel() - 1
         _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seqs + 1,))
-    return t, hq, hkv, n_seqs, head_dim ** -0.5 if scale is None else float(scale)
+    return (t, hq, hkv, n_seqs, head_dim ** -0.5 if scale is None else float(scale)), q_shape, k_shape
 
 
 def attn_bwd_workspace_bytes(T: int, hq: int, hkv: int, head_dim: int, n_seqs: int = 0) -> int:
@@ -589,10 +609,10 @@ def attn_fwd(q, k, v, head_dim: int, cu_seqlens=None, causal: bool = True, scale
     """Softmax attention of q [T, hq * head_dim] over k, v [T, hkv * head_dim] (bf16), within the
     sequences cu_seqlens (int32 [n + 1]; None: one sequence). Returns (o like q, lse fp32 [hq, T]);
     rows outside every sequence are not written."""
-    t, hq, hkv, n_seqs, scale = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((hq, t), dtype=torch.float32, device=q.device) if lse is None else lse
-    _need(o, "o", torch.bfloat16, (t, hq * head_dim))
+    (t, hq, hkv, n_seqs, scale), q_shape, _ = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
+    o = _empty(q_shape, torch.bfloat16, q.device, stream) if o is None else o
+    lse = _empty((hq, t), torch.float32, q.device, stream) if lse is None else lse
+    _need(o, "o", torch.bfloat16, q_shape)
     _need(lse, "lse", torch.float32, (hq, t))
     _enqueue(_device(q, k, v, o, lse, cu_seqlens), stream, _lib.nf4_attn_fwd, q.data_ptr(), k.data_ptr(), v.data_ptr(), t,
              hq, hkv, head_dim, None if cu_seqlens is None else cu_seqlens.data_ptr(), n_seqs, int(bool(causal)), scale,
@@ -603,11 +623,10 @@ def attn_fwd(q, k, v, head_dim: int, cu_seqlens=None, causal: bool = True, scale
 def attn_bwd(q, k, v, o, lse, do, head_dim: int, cu_seqlens=None, causal: bool = True, scale=None, dq=None, dk=None,
              dv=None, ws=None, stream=None):
     """Backward of attn_fwd from its o and lse: returns (dq, dk, dv)."""
-    t, hq, hkv, n_seqs, scale = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    q_shape, k_shape = (t, hq * head_dim), (t, hkv * head_dim)
+    (t, hq, hkv, n_seqs, scale), q_shape, k_shape = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
+    dq = _empty(q_shape, torch.bfloat16, q.device, stream) if dq is None else dq
+    dk = _empty(k_shape, torch.bfloat16, q.device, stream) if dk is None else dk
+    dv = _empty(k_shape, torch.bfloat16, q.device, stream) if dv is None else dv
     _need(o, "o", torch.bfloat16, q_shape)
     _need(do, "do", torch.bfloat16, q_shape)
     _need(lse, "lse", torch.float32, (hq, t))
@@ -615,7 +634,7 @@ def attn_bwd(q, k, v, o, lse, do, head_dim: int, cu_seqlens=None, causal: bool =
     _need(dk, "dk", torch.bfloat16, k_shape)
     _need(dv, "dv", torch.bfloat16, k_shape)
     if ws is None:
-        ws = workspace(attn_bwd_workspace_bytes(t, hq, hkv, head_dim, n_seqs), q.device)
+        ws = _empty(max(attn_bwd_workspace_bytes(t, hq, hkv, head_dim, n_seqs), 256), torch.uint8, q.device, stream)
     _enqueue(_device(q, k, v, o, lse, do, dq, dk, dv, ws, cu_seqlens), stream, _lib.nf4_attn_bwd, q.data_ptr(),
              k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), do.data_ptr(), t, hq, hkv, head_dim,
              None if cu_seqlens is None else cu_seqlens.data_ptr(), n_seqs, int(bool(causal)), scale, dq.data_ptr(),
@@ -626,7 +645,8 @@ def attn_bwd(q, k, v, o, lse, do, head_dim: int, cu_seqlens=None, causal: bool =
 class GradList:
     """A training program's gradient tensors (bf16 or fp32, mixed freely) as one list for the
     global norm and clipping (nf4_grad_list_*): made once over the buffers, used every step.
-    outs: where the scaled gradients go (default: in place). The tensors are kept alive."""
+    outs: where the scaled gradients go (default: in place). The tensors are kept alive with
+    this object, which has to outlive every graph that captured a call of it."""
 
     def __init__(self, grads, outs=None, stream=None):
         self._h = None
@@ -652,7 +672,8 @@ class GradList:
         if not nbytes:
             raise Nf4Error(NF4_E_ARG, last_error())
         h = C.c_void_p()
-        self._table = workspace(nbytes, self.device)
+        self._table = _empty(nbytes, torch.uint8, self.device, stream)
+        self._home = _current_raw_stream(dev) if stream is None else _as_stream(stream).cuda_stream
         _enqueue(dev, stream, lambda s: _lib.nf4_grad_list_create(arr, len(self.grads), _ptr(self._table),
                                                                   self._table.numel(), s, C.byref(h)))
         self._h = h
@@ -661,10 +682,14 @@ class GradList:
     def _run(self, call, norm, ws, stream, *args):
         if self._h is None:
             raise Nf4Error(NF4_E_STATE, "the gradient list is closed")
-        norm = torch.empty(1, dtype=torch.float32, device=self.device) if norm is None else norm
+        norm = _empty(1, torch.float32, self.device, stream) if norm is None else norm
         _need(norm, "norm", torch.float32, (1,))
-        ws = workspace(self._ws_bytes, self.device) if ws is None else ws
-        _enqueue(_device(self._table, norm, ws), stream, call, self._h, *args, norm.data_ptr(), ws.data_ptr(),
+        ws = _empty(self._ws_bytes, torch.uint8, self.device, stream) if ws is None else ws
+        dev = _device(self._table, norm, ws)
+        if stream is not None or _current_raw_stream(dev) != self._home:
+            # the table may be freed (with this object) while that stream still reads it
+            self._table.record_stream(torch.cuda.current_stream(dev) if stream is None else _as_stream(stream))
+        _enqueue(dev, stream, call, self._h, *args, norm.data_ptr(), ws.data_ptr(),
                  ws.numel() * ws.element_size())
         return norm
 

@@ -160,3 +160,43 @@ def test_python_refusals(gpu_lib):
     gl.close()
     with pytest.raises(lib.Nf4Error, match="closed"):
         gl.norm()
+
+
+def test_list_freed_while_another_stream_still_reads_its_table(gpu_lib):
+    """A list used on a side stream and dropped at once: its table's memory is not handed out
+    again before that stream is done (the stream is held up by a bounded spin)."""
+    lib = gpu_lib
+    grads = [torch.ones(1000, device="cuda") for _ in range(200)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    gl = lib.GradList(grads)
+    nbytes = gl._table.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    at = gl._table.data_ptr()
+    n = gl.clip(1.0, stream=side)
+    del gl
+    again = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    assert all(t.data_ptr() != at for t in again)   # checked before anything could be written there
+    torch.cuda.synchronize()
+    assert n.item() == pytest.approx(math.sqrt(200_000), rel=1e-6)
+
+
+def test_outputs_of_a_side_stream_call_are_that_streams_memory(gpu_lib):
+    """Results allocated for a call on a side stream are not blocks that the current stream
+    has freed but still writes (behind a bounded spin)."""
+    lib = gpu_lib
+    g = torch.ones(5000, device="cuda")
+    gl = lib.GradList([g])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    freed = torch.empty(1, device="cuda")
+    torch.cuda._sleep(20_000_000)
+    freed.fill_(7.0)                                # pending on the current stream
+    at = freed.data_ptr()
+    del freed
+    n = gl.norm(stream=side)
+    assert n.data_ptr() != at
+    torch.cuda.synchronize()
+    assert n.item() == pytest.approx(math.sqrt(5000), rel=1e-6)
