@@ -267,7 +267,7 @@ int nf4_repeat_kv_bwd(const uint16_t* da, int64_t T, int64_t q, int64_t kv, int6
  *              theta^(-2i/head_dim); scaled variants pass their own)
  *   sections   HOST int array [n_axes], each >= 1, sum = head_dim/2; n_axes in 1..4
  *   inverse    0, or 1 to rotate by -phi: the backward (dq, dk from the rotated ones)
- *   q_out, k_out  device bf16; each may be its input itself (not a shifted overlap)
+ *   q_out, k_out  device bf16; each may be its input itself (any other overlap is refused)
  * head_dim a multiple of 16 up to 256; hq, hkv <= 1024; T <= 2^23; T == 0 is a no-op.
  * q, k and the outputs 16-byte, inv_freq 8-byte aligned.
  */
@@ -293,7 +293,8 @@ int nf4_rope(const uint16_t* q, const uint16_t* k, int64_t T, int64_t hq, int64_
  * The probabilities are rounded to bf16 for their product with v. A value of k or v that is
  * not finite makes rows of its own sequence not finite (also rows that a causal mask hides
  * it from), never rows of another. head_dim 32, 64 or 128; hkv | hq <= 1024; T <= 2^23;
- * n_seqs <= 2^20; T == 0 is a no-op. q, k, v, o 16-byte aligned; o must not overlap q, k, v.
+ * n_seqs <= 2^20; T == 0 is a no-op. q, k, v, o 16-byte aligned; an o or lse that overlaps
+ * another argument is refused (NF4_E_ARG).
  */
 int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t T, int64_t hq, int64_t hkv,
                  int64_t head_dim, const int32_t* cu_seqlens, int64_t n_seqs, int causal, float scale, uint16_t* o,
@@ -311,11 +312,13 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
  *   o, lse      as nf4_attn_fwd wrote them
  *   dO          device bf16 [T][hq*head_dim]
  *   dq, dk, dv  device bf16 like q, k, v (overwritten; rows outside every sequence are
- *               left as they were); they must not overlap the inputs
+ *               left as they were); an overlap with another argument is refused
+ *               (NF4_E_ARG), one of ws too
  *   ws          device workspace of at least nf4_attn_bwd_workspace() bytes, 256-byte
  *               aligned; its contents on entry are ignored. Calls that may run at the same
  *               time (two streams, two graphs) need one each.
- * P and dS are rounded to bf16 for their products. Other arguments, limits and errors as
+ * P and dS are rounded to bf16 for their products; dq and dk of a sequence of one row are
+ * exactly zero. Other arguments, limits and errors as
  * nf4_attn_fwd.
  */
 int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,

@@ -87,6 +87,10 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int bm, int g, Tile
     return false;
 }
 
+// The factor of dq and dk. A softmax over one key is 1 whatever its score, so nothing reaches q
+// and k of a sequence of one token; what rounding leaves of dP - delta there is not passed on.
+__device__ __forceinline__ float grad_scale(const AttnArgs& a, const Tile& t) { return t.len > 1 ? a.scale : 0.0f; }
+
 // Workgroup id -> (kv head, item of that head). Items of one kv head share its K and V (or
 // its queries' dO), so they are kept on as few XCDs as the head count allows: the XCD of a
 // workgroup is its id mod 8, and each L2 then holds the operands of hkv / 8 heads at a time.
@@ -505,13 +509,14 @@ __device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* 
     }
     if (q_row < t.len) {
         uint16_t* out = a.dq + (size_t(t.begin) + q_row) * ldq + head * D;
+        const float f = grad_scale(a, t);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 16; e += 4)
                 *reinterpret_cast<u32x2*>(out + 32 * nb + 2 * e + 4 * h) =
-                    u32x2{pack_bf16x2(acc[nb][e] * a.scale, acc[nb][e + 1] * a.scale),
-                          pack_bf16x2(acc[nb][e + 2] * a.scale, acc[nb][e + 3] * a.scale)};
+                    u32x2{pack_bf16x2(acc[nb][e] * f, acc[nb][e + 1] * f),
+                          pack_bf16x2(acc[nb][e + 2] * f, acc[nb][e + 3] * f)};
     }
 }
 
@@ -657,12 +662,12 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
     if (a.splits == 1) {
         if (key >= t.len) return;
         const size_t at = (size_t(t.begin) + key) * ldk + kvh * D + 4 * h;
+        const float f = grad_scale(a, t);
 #pragma unroll
         for (int n = 0; n < 4 * NB; ++n) {
             const int nb = n / 4, e = n % 4 * 4;
             *reinterpret_cast<u32x2*>(a.dk + at + 8 * n) =
-                u32x2{pack_bf16x2(dk[nb][e] * a.scale, dk[nb][e + 1] * a.scale),
-                      pack_bf16x2(dk[nb][e + 2] * a.scale, dk[nb][e + 3] * a.scale)};
+                u32x2{pack_bf16x2(dk[nb][e] * f, dk[nb][e + 1] * f), pack_bf16x2(dk[nb][e + 2] * f, dk[nb][e + 3] * f)};
             *reinterpret_cast<u32x2*>(a.dv + at + 8 * n) =
                 u32x2{pack_bf16x2(dv[nb][e], dv[nb][e + 1]), pack_bf16x2(dv[nb][e + 2], dv[nb][e + 3])};
         }
@@ -737,7 +742,7 @@ __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
     for (int z = 0; z < a.splits; ++z) s += p[size_t(z) * (2 * KW * 256 * NB)];
-    const float f = is_dv ? 1.0f : a.scale;
+    const float f = is_dv ? 1.0f : grad_scale(a, t);
     const size_t at = (size_t(t.begin) + key) * (a.hkv * D) + kvh * D + 8 * n + 4 * (lane >> 5);
     *reinterpret_cast<u32x2*>((is_dv ? a.dv : a.dk) + at) =
         u32x2{pack_bf16x2(s.x * f, s.y * f), pack_bf16x2(s.z * f, s.w * f)};
@@ -815,6 +820,14 @@ int check_attn(const char* fn, int64_t T, int64_t hq, int64_t hkv, int64_t D, co
     return NF4_OK;
 }
 
+// The first n_out ranges are written: none of them may meet another range of the list.
+int check_apart(const char* fn, const ByteRange* r, int n_out, int n) {
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (r[i].meets(r[j])) return fail(NF4_E_ARG, "%s: an output overlaps another argument", fn);
+    return NF4_OK;
+}
+
 struct AttnBwdPlan {
     int splits;
     size_t stats_bytes, part_bytes;
@@ -855,7 +868,8 @@ int run_bwd(const AttnArgs& in, hipStream_t stream) {
     a.tiles = a.q_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 128));
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.q_tiles) * (a.hq / a.hkv));
     const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
-    if (int st = check_grid("nf4_attn_bwd", wgs + wgs_kv); st != NF4_OK) return st;
+    const int64_t wgs_join = a.splits > 1 ? int64_t(a.tiles) * a.hkv * (kKeyWaves * D / 16) : 0;
+    if (int st = check_grid("nf4_attn_bwd", std::max(wgs + wgs_kv, wgs_join)); st != NF4_OK) return st;
     if (one_launch(a.T, a.hq)) {
         hipLaunchKernelGGL(k_attn_bwd_stats<D>, dim3(unsigned(cdiv(int64_t(a.T) * a.hq * (D / 8), 256))), dim3(256), 0,
                            stream, a);
@@ -865,8 +879,7 @@ int run_bwd(const AttnArgs& in, hipStream_t stream) {
         hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
     }
     if (a.splits > 1)
-        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(a.tiles * a.hkv * (kKeyWaves * D / 16))), dim3(256), 0,
-                           stream, a);
+        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(wgs_join)), dim3(256), 0, stream, a);
     return check_launch("nf4_attn_bwd");
 }
 
@@ -888,6 +901,10 @@ int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !lse ||
         reinterpret_cast<uintptr_t>(lse) % 4 != 0)
         return fail(NF4_E_ARG, "%s: q, k, v and o must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
+    const size_t q_bytes = size_t(T) * hq * head_dim * 2, k_bytes = size_t(T) * hkv * head_dim * 2;
+    const size_t lse_bytes = size_t(T) * hq * 4, cu_bytes = cu_seqlens ? (size_t(n_seqs) + 1) * 4 : 0;
+    const ByteRange r[] = {{o, q_bytes}, {lse, lse_bytes}, {q, q_bytes}, {k, k_bytes}, {v, k_bytes}, {cu_seqlens, cu_bytes}};
+    if (st = check_apart(fn, r, 2, 6); st != NF4_OK) return st;
     AttnArgs a{};
     a.q = q, a.k = k, a.v = v, a.out = o, a.lse = lse, a.cu = cu_seqlens;
     a.T = int(T), a.n_seqs = int(n_seqs), a.hq = int(hq), a.hkv = int(hkv), a.causal = causal, a.scale = scale;
@@ -918,6 +935,11 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.stats_bytes + p.part_bytes)
         return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
                     p.stats_bytes + p.part_bytes, ws_bytes);
+    const size_t q_bytes = size_t(T) * hq * head_dim * 2, k_bytes = size_t(T) * hkv * head_dim * 2;
+    const size_t lse_bytes = size_t(T) * hq * 4, cu_bytes = cu_seqlens ? (size_t(n_seqs) + 1) * 4 : 0;
+    const ByteRange r[] = {{dq, q_bytes}, {dk, k_bytes}, {dv, k_bytes}, {ws, p.stats_bytes + p.part_bytes}, {q, q_bytes},
+                           {k, k_bytes}, {v, k_bytes}, {o, q_bytes}, {dO, q_bytes}, {lse, lse_bytes}, {cu_seqlens, cu_bytes}};
+    if (st = check_apart(fn, r, 4, 11); st != NF4_OK) return st;
     AttnArgs a{};
     a.q = q, a.k = k, a.v = v, a.o = o, a.dO = dO, a.lse_in = lse, a.dq = dq, a.dk = dk, a.dv = dv, a.cu = cu_seqlens;
     a.T = int(T), a.n_seqs = int(n_seqs), a.hq = int(hq), a.hkv = int(hkv), a.causal = causal, a.scale = scale;

@@ -153,6 +153,16 @@ void prof_gemm_end(hipStream_t stream);
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Whether two ranges share a byte (an empty range shares none).
+struct ByteRange {
+    const void* p;
+    size_t bytes;
+    bool meets(const ByteRange& o) const {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(o.p);
+        return a < b + o.bytes && b < a + bytes && bytes && o.bytes;
+    }
+};
+
 // Compute units of one MI355X (gfx950): the round size of the GEMM grids (the
 // dispatcher gives linear workgroup ids L, L + 256, L + 512 the same CU).
 constexpr int64_t kChipCUs = 256;

@@ -106,6 +106,12 @@ extern "C" int nf4_rope(const uint16_t* q, const uint16_t* k, int64_t T, int64_t
         return fail(NF4_E_ARG, "%s: q, k and the outputs must be non-NULL and 16-byte aligned", fn);
     if (!pos || reinterpret_cast<uintptr_t>(pos) % 4 != 0 || !inv_freq || reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0)
         return fail(NF4_E_ARG, "%s: pos must be 4-byte and inv_freq 8-byte aligned and non-NULL", fn);
+    const size_t q_bytes = size_t(T) * hq * head_dim * 2, k_bytes = size_t(T) * hkv * head_dim * 2;
+    const ByteRange rq{q, q_bytes}, rk{k, k_bytes}, wq{q_out, q_bytes}, wk{k_out, k_bytes};
+    const ByteRange rp{pos, size_t(T) * n_axes * 4}, rf{inv_freq, size_t(head_dim) * 4};
+    if (wq.meets(wk) || wq.meets(rk) || wk.meets(rq) || wq.meets(rp) || wq.meets(rf) || wk.meets(rp) || wk.meets(rf) ||
+        (q != q_out && wq.meets(rq)) || (k != k_out && wk.meets(rk)))
+        return fail(NF4_E_ARG, "%s: an output overlaps another argument (only its own input, exactly, is allowed)", fn);
     a.q = q, a.k = k, a.q_out = q_out, a.k_out = k_out, a.pos = pos, a.inv_freq = inv_freq, a.T = T;
     a.hq = int(hq), a.hkv = int(hkv), a.D = int(head_dim), a.sign = inverse ? -1.0f : 1.0f;
     a.tokens = kThreads / (a.D / 2);

@@ -58,6 +58,39 @@ def test_attention_output_and_workspace_validation(L):
     assert L.attn_bwd_workspace_bytes(512, 5, 2, 64) == 0
 
 
+def test_attention_overlaps_are_refused(L):
+    """Ranges of T=4, hq=4, hkv=2, D=64: q, o and their gradients 2048 bytes, k and v 1024, lse 64."""
+    at = lambda i: C.c_void_p(0x100000 + 0x10000 * i)
+    lib = L.raw()
+
+    def fwd(o=at(3), lse=at(4), cu=at(5)):
+        return lib.nf4_attn_fwd(at(0), at(1), at(2), 4, 4, 2, 64, cu, 1, 1, 0.125, o, lse, None)
+
+    for kw in ({"o": at(0)}, {"o": at(1)}, {"o": C.c_void_p(at(2).value + 1008)}, {"lse": at(3)}, {"lse": at(0)},
+               {"lse": C.c_void_p(at(5).value + 4)}):
+        _err(L, fwd(**kw), L.NF4_E_ARG, "overlaps")
+
+    def bwd(dq=at(6), dk=at(7), dv=at(8), ws=at(9)):
+        return lib.nf4_attn_bwd(at(0), at(1), at(2), at(3), at(4), at(5), 4, 4, 2, 64, at(11), 1, 1, 0.125, dq, dk, dv, ws,
+                                0x10000, None)
+
+    for kw in ({"dq": at(0)}, {"dq": at(5)}, {"dk": at(8)}, {"dk": at(1)}, {"dv": at(2)}, {"dv": at(4)}, {"ws": at(6)},
+               {"dk": C.c_void_p(at(6).value + 2032)}, {"ws": at(3)}, {"dv": at(11)}):
+        _err(L, bwd(**kw), L.NF4_E_ARG, "overlaps")
+
+
+def test_rope_overlaps_are_refused(L):
+    at = lambda i: C.c_void_p(0x100000 + 0x10000 * i)
+    sections = (C.c_int * 1)(32)
+
+    def rope(q_out=at(0), k_out=at(1)):
+        return L.raw().nf4_rope(at(0), at(1), 4, 4, 2, 64, at(2), at(3), sections, 1, 0, q_out, k_out, None)
+
+    for kw in ({"q_out": at(1)}, {"q_out": C.c_void_p(at(0).value + 16)}, {"k_out": C.c_void_p(at(1).value - 16)},
+               {"k_out": at(0)}, {"q_out": at(4), "k_out": at(4)}, {"q_out": at(2)}, {"k_out": at(3)}):
+        _err(L, rope(**kw), L.NF4_E_ARG, "overlaps")
+
+
 def _rope(L, q=FAKE, k=FAKE, T=4, hq=4, hkv=2, D=64, pos=FAKE, inv=FAKE, sections=(32,), n=None, inverse=0, out=FAKE):
     arr = None if sections is None else (C.c_int * max(1, len(sections)))(*sections)
     return L.raw().nf4_rope(q, k, T, hq, hkv, D, pos, inv, arr, len(sections or ()) if n is None else n, inverse, out,

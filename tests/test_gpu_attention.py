@@ -90,6 +90,24 @@ def test_packed_sequences(gpu_lib, lens):
         _check(gpu_lib, _case(t, 4, 2, d), d, lens, causal)
 
 
+@pytest.mark.parametrize("hq,hkv,t", [(2, 2, 5), (8, 1, 300), (32, 1, 40), (64, 64, 1400)])
+def test_sequences_of_one_token_pass_nothing_to_q_and_k(gpu_lib, hq, hkv, t):
+    """A softmax over one key is 1 whatever its score: dq and dk are exactly zero, dv is the
+    sum of do over the kv head's queries, and o is v."""
+    for d, causal in ((64, True), (128, False)):
+        c = {n: to_dev_bf16(x) for n, x in _case(t, hq, hkv, d).items()}
+        cu = _cu([1] * t)
+        o, lse = gpu_lib.attn_fwd(c["q"], c["k"], c["v"], d, cu, causal)
+        dq, dk, dv = gpu_lib.attn_bwd(c["q"], c["k"], c["v"], o, lse, c["do"], d, cu, causal)
+        torch.cuda.synchronize()
+        assert torch.equal(o.view(t, hkv, -1, d), c["v"].view(t, hkv, 1, d).expand(-1, -1, hq // hkv, -1))
+        assert not dq.any() and not dk.any()
+        exact = c["do"].double().view(t, hkv, -1, d).sum(2).view(t, -1)
+        # P is 2^(S - lse) with both in fp32, about 2^-18 off at |S| < 64; rounded to bf16 it is 1
+        parts = c["do"].double().abs().view(t, hkv, -1, d).sum(2).view(t, -1)
+        assert bool(((dv.double() - exact).abs() <= exact.abs() * 2.0 ** -8 + parts * 2.0 ** -18).all())
+
+
 def test_longer_sequences_and_split_gradients(gpu_lib):
     """Key tiles by the dozen, and dk, dv from several shares (few kv heads) or one (many)."""
     _check(gpu_lib, _case(1100, 2, 1, 128), 128)
