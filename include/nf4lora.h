@@ -317,7 +317,8 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
  *   ws          device workspace of at least nf4_attn_bwd_workspace() bytes, 256-byte
  *               aligned; its contents on entry are ignored. Calls that may run at the same
  *               time (two streams, two graphs) need one each.
- * P and dS are rounded to bf16 for their products; dq and dk of a sequence of one row are
+ * P and dS are rounded to bf16 for their products (dS to the sum of two bf16 values in calls
+ * of at most 64 rows, and for the dq of heads 32 wide); dq and dk of a sequence of one row are
  * exactly zero. Other arguments, limits and errors as
  * nf4_attn_fwd.
  */

@@ -8,7 +8,9 @@
 // (dk, dv also summed over the G query heads of a kv head). Scores are never stored: the
 // backward recomputes P from lse. Everything is fp32 except the operands of the second
 // products, which are P and dS rounded to bf16 for the bf16 MFMA: a relative error of at
-// most 2^-8 per term, of the size of the rounding of the bf16 results.
+// most 2^-8 per term, which leaves the results about 1.4 times as far from exact as their own
+// rounding does. Where few terms carry a sum that is not enough (1.5 to 1.6 times): dS is then
+// the sum of two bf16 values, each multiplied (FINE below).
 //
 // MFMA layout used throughout (32x32x16): an accumulator lane l holds column l % 32 and
 // rows 8 (e / 4) + 4 (l / 32) + e % 4; an operand lane holds one row (or column) and 8
@@ -162,6 +164,18 @@ __device__ __forceinline__ bf16x8 lds_frag_tr(const char* p0, const char* p1) {
 __device__ __forceinline__ bf16x8 pack8(const f32x16& v, int g) {
     return as_bf16x8(u32x4{pack_bf16x2(v[8 * g], v[8 * g + 1]), pack_bf16x2(v[8 * g + 2], v[8 * g + 3]),
                            pack_bf16x2(v[8 * g + 4], v[8 * g + 5]), pack_bf16x2(v[8 * g + 6], v[8 * g + 7])});
+}
+
+// What pack8 rounded off, rounded itself: both together hold v to 2^-16 of its size.
+__device__ __forceinline__ bf16x8 pack8_rest(const f32x16& v, int g) {
+    u32x4 r;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = v[8 * g + 2 * e], b = v[8 * g + 2 * e + 1];
+        const uint32_t x = pack_bf16x2(a, b);
+        r[e] = pack_bf16x2(a - __uint_as_float(x << 16), b - __uint_as_float(x & 0xFFFF0000u));
+    }
+    return as_bf16x8(r);
 }
 
 __device__ __forceinline__ f32x16 zero16() {
@@ -404,8 +418,12 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 
 // As the forward, with dO beside Q in registers: per 64-key tile S^T = K Q^T,
 // dP^T = V dO^T, dS^T in place, dq^T += K^T dS^T. delta is formed here first (the dk/dv
-// kernel behind this one reads it). R, C and B as in the forward.
-template <int D, int R, int C, bool STATS>
+// kernel behind this one reads it). R, C and B as in the forward. FINE: for heads 32 wide, whose
+// scores spread further with the length of q than those of wider heads and leave a row to its
+// largest few, and for calls of at most 64 tokens. Measured (us, one bf16 value for dS and two):
+// 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 28/4 heads of 128 18.1, 19.7, of
+// 64/8 15.4, 16.6.
+template <int D, int R, int C, bool STATS, bool FINE>
 __device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* sK0, char* sV0, char* sK1, char* sV1) {
     constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
     const int G = a.hq / a.hkv;
@@ -492,8 +510,11 @@ __device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* 
                 const bf16x8 ds = pack8(s, g);
                 const char* kg = k + (2 * b + g) * 32 * D;
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-                    acc[nb] = mfma32x32x16(lds_frag_tr(kg + map.tr[nb][0], kg + map.tr[nb][1]), ds, acc[nb]);
+                for (int nb = 0; nb < NB; ++nb) {
+                    const bf16x8 kt = lds_frag_tr(kg + map.tr[nb][0], kg + map.tr[nb][1]);
+                    acc[nb] = mfma32x32x16(kt, ds, acc[nb]);
+                    if constexpr (FINE) acc[nb] = mfma32x32x16(kt, pack8_rest(s, g), acc[nb]);
+                }
             }
         }
     };
@@ -523,7 +544,7 @@ __device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* 
 template <int D, int R, int C>
 __global__ __launch_bounds__(64 * R * C, 2) void k_attn_bwd_dq(AttnArgs a) {
     __shared__ __align__(1024) char sK0[128 * D], sV0[128 * D], sK1[128 * D], sV1[128 * D];
-    bwd_dq<D, R, C, true>(a, blockIdx.x, sK0, sV0, sK1, sV1);
+    bwd_dq<D, R, C, true, D == 32>(a, blockIdx.x, sK0, sV0, sK1, sV1);
 }
 
 // ------------------------------------------------------------------ backward: dk, dv
@@ -548,7 +569,7 @@ struct DkvLds {
     static constexpr int QW = 2, BQ = 32 * QW, QB = BQ * 2 * D, SB = 256, DB = QB + 2 * SB, VB = 64 * kKeyWaves * D;
 };
 
-template <int D>
+template <int D, bool FINE>
 __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sV, char* sQ0, char* sD0, char* sQ1,
                                         char* sD1) {
     using L = DkvLds<D>;
@@ -642,7 +663,9 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
                 dv[nb] = mfma32x32x16(lds_frag_tr(dg + map.tr[nb][0], dg + map.tr[nb][1]), p, dv[nb]);
-                dk[nb] = mfma32x32x16(lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]), ds, dk[nb]);
+                const bf16x8 qt = lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]);
+                dk[nb] = mfma32x32x16(qt, ds, dk[nb]);
+                if constexpr (FINE) dk[nb] = mfma32x32x16(qt, pack8_rest(dp, g), dk[nb]);
             }
         }
     };
@@ -687,20 +710,21 @@ template <int D>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
     using L = DkvLds<D>;
     __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
-    bwd_dkv<D>(a, blockIdx.x, sV, sQ0, sD0, sQ1, sD1);
+    bwd_dkv<D, false>(a, blockIdx.x, sV, sQ0, sD0, sQ1, sD1);
 }
 
 // Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
 // idle: the first q_wgs workgroups take 128 rows of dq each, with two waves a row. lse * log2 e
-// and delta come from k_attn_bwd_stats, since neither kind can wait for the other.
-template <int D>
+// and delta come from k_attn_bwd_stats, since neither kind can wait for the other. FINE: calls
+// of at most 64 tokens.
+template <int D, bool FINE>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q_wgs) {
     using L = DkvLds<D>;
     __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
     if (blockIdx.x < q_wgs)
-        bwd_dq<D, 4, 2, false>(a, blockIdx.x, sQ0, sD0, sQ1, sD1);
+        bwd_dq<D, 4, 2, false, FINE || D == 32>(a, blockIdx.x, sQ0, sD0, sQ1, sD1);
     else
-        bwd_dkv<D>(a, blockIdx.x - q_wgs, sV, sQ0, sD0, sQ1, sD1);
+        bwd_dkv<D, FINE>(a, blockIdx.x - q_wgs, sV, sQ0, sD0, sQ1, sD1);
 }
 
 // stats[0] = lse * log2 e, stats[1] = delta = do . o for every row and head: D / 8 lanes each.
@@ -758,11 +782,14 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
 // 2048 tokens of 40/8: 55.4, 64.3; 4096 tokens of 14/2 heads of 64: 57.4, 46.7.
 bool few_rows(int64_t T, int64_t hq, int64_t D) { return cdiv(T, 128) * hq < 256 * (D == 128 ? 2 : D == 64 ? 3 : 4); }
 
+// Calls whose dk has dS as two bf16 values (dq: those, and all heads 32 wide).
+bool fine_ds(int64_t T) { return T <= 64; }
+
 // Whether the backward takes both kinds of workgroups in one launch: up to one and a half
 // workgroups of dq a CU. Us in two launches and in one: 512 tokens of 28/4 heads 39.8, 32.5;
 // 1024: 68.7, 60.8; 2048: 150.7, 164.7; 1408 tokens of 32/32 heads of 64: 92.1, 85.6; 4096 of
 // 14/2: 142.9, 148.1.
-bool one_launch(int64_t T, int64_t hq) { return cdiv(T, 128) * hq <= 384; }
+bool one_launch(int64_t T, int64_t hq) { return fine_ds(T) || cdiv(T, 128) * hq <= 384; }
 
 // Shares of dk and dv: the power of two up to 16 that is expected to take the least time. A CU
 // holds one workgroup of 8 waves, so the workgroups of a launch (with those of dq, where they
@@ -873,7 +900,8 @@ int run_bwd(const AttnArgs& in, hipStream_t stream) {
     if (one_launch(a.T, a.hq)) {
         hipLaunchKernelGGL(k_attn_bwd_stats<D>, dim3(unsigned(cdiv(int64_t(a.T) * a.hq * (D / 8), 256))), dim3(256), 0,
                            stream, a);
-        hipLaunchKernelGGL(k_attn_bwd_both<D>, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
+        const auto both = fine_ds(a.T) ? k_attn_bwd_both<D, true> : k_attn_bwd_both<D, false>;
+        hipLaunchKernelGGL(both, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
     } else {
         hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
         hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);

@@ -78,7 +78,7 @@ def attention_bwd(q, k, v, o, lse, do, head_dim, lens=None, causal=True, scale=N
     return dq, dk, dv
 
 
-def attention_bounds(q, k, v, o, lse, do, head_dim, lens=None, causal=True, scale=None):
+def attention_bounds(q, k, v, o, lse, do, head_dim, lens=None, causal=True, scale=None, ds_unit=2.0 ** -8):
     """How far an fp32 evaluation that rounds P and dS to bf16 for their products may be from
     the exact outputs (before an output's own rounding): {"o", "lse", "dq", "dk", "dv"}.
 
@@ -88,7 +88,8 @@ def attention_bounds(q, k, v, o, lse, do, head_dim, lens=None, causal=True, scal
     (lse: its own rounding and its product with log2 e), which is P's relative error. Rounding P to bf16 adds at most 2^-8 of P. Sums over n rows
     add n u of the sum of magnitudes. lse: its sum's relative error (e + n u) as an absolute
     one, plus 2^-22 of its own size. dP and delta are D-term sums: off by
-    u (D + 1) (|do||v| + |do||o|); dS by P times that, plus |dS| (e + 2u), plus 2^-8 of |dS|.
+    u (D + 1) (|do||v| + |do||o|); dS by P times that, plus |dS| (e + 2u), plus ds_unit of |dS|
+    (2^-8 for one bf16 value, 2^-16 for the sum of two).
     Underflow: a P or dS below 2^-126, the least normal value of fp32 and bf16 alike, may
     come out as zero: each is off by at most 2^-126 more (P's times |dP - delta| in dS).
     """
@@ -116,7 +117,7 @@ def attention_bounds(q, k, v, o, lse, do, head_dim, lens=None, causal=True, scal
             err_dp = u * (d + 1) * (ga @ va.T + np.sum(ga * oa, axis=1, keepdims=True))
             rest = np.abs(do[b:e_, c] @ v[b:e_, ck].T - np.sum(do[b:e_, c] * o[b:e_, c], axis=1, keepdims=True))
             ds = p * rest
-            err = p * err_dp * (1 + 2.0 ** -8) + ds * (2.0 ** -8 + e + 2 * u) + tiny * (1 + rest)
+            err = p * err_dp * (1 + ds_unit) + ds * (ds_unit + e + 2 * u) + tiny * (1 + rest)
             # sums over n rows (and rep heads) in fp32, and the final scaling
             out["dq"][b:e_, c] = scale * ((err + (n + 64) * u * ds) @ ka)
             out["dk"][b:e_, ck] += scale * ((err + (rep * n + 64) * u * ds).T @ qa)
