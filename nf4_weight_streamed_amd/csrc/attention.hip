@@ -280,6 +280,11 @@ __device__ __forceinline__ void add_share(f32x16 (&x)[NB], const f32x4* p, float
 // query in a lane, so the softmax statistics are one register each. The running maximum is
 // raised, and o and the sum rescaled, only when some row's tile maximum exceeds it by more than
 // 8 (in log2 units): p then stays below 2^8.
+// Bound by the matrix and vector units in turn, at long lengths by the card's power: 8192 tokens
+// of 64/8 heads of 128, causal, 1030 us, 1.07 PFLOP/s of what the mask leaves (on zeros, which
+// draw less power, 758 us), without an LDS bank conflict and with 96 % of the L2 reads hits;
+// 4096 in seven sequences of 40/8 heads 70 us, 610 TFLOP/s (ragged tiles); 512 tokens of 28/4
+// heads 11 us: the longest row's 8 tiles one after the other.
 template <int D, int R, int C>
 __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
     constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
@@ -423,6 +428,8 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 // largest few, and for calls of at most 64 tokens. Measured (us, one bf16 value for dS and two):
 // 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 28/4 heads of 128 18.1, 19.7, of
 // 64/8 15.4, 16.6.
+// Bound as the forward: 8192 tokens of 64/8 heads of 128 1364 us, 1.21 PFLOP/s with its share
+// (S, dP and dq: 6 D operations a pair).
 template <int D, int R, int C, bool STATS, bool FINE>
 __device__ __forceinline__ void bwd_dq(const AttnArgs& a, uint32_t block, char* sK0, char* sV0, char* sK1, char* sV1) {
     constexpr int BM = 32 * R, B = 2 / C, kTile = 64, KS = D / 16, NB = D / 32;
@@ -562,6 +569,13 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
 // dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
+// Bound by LDS reads beside the products (each wave reads Q and dO twice, by rows and
+// transposed, and V: two products an operand, against a row's four in the forward) and by power:
+// 8192 tokens of 64/8 heads of 128 2100 us, 1.05 PFLOP/s (S, dP, dv and dk: 8 D operations a
+// pair). Measured and left out: V in registers too, which leaves one wave a SIMD (with the walk
+// below the whole backward 4027 -> 3497 us without it); the products ordered by hand (slower), a
+// higher wave priority around them (no change); the second wave of a key block half a tile
+// behind the first, whose state spills (five times slower at width 128, 15 % at 64).
 // LDS of a dk/dv workgroup: V; two pairs of a tile's Q, and its dO with the rows' lse * log2 e
 // and delta behind it.
 template <int D>
@@ -716,7 +730,9 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
 // Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
 // idle: the first q_wgs workgroups take 128 rows of dq each, with two waves a row. lse * log2 e
 // and delta come from k_attn_bwd_stats, since neither kind can wait for the other. FINE: calls
-// of at most 64 tokens.
+// of at most 64 tokens. 512 tokens of 28/4 heads of 128: 25 us, of which the row statistics
+// before and the join behind take 4 us each; 2048 tokens of 16/16 heads of 64 in three
+// sequences without a mask 57 us in all, 410 TFLOP/s.
 template <int D, bool FINE>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q_wgs) {
     using L = DkvLds<D>;
@@ -728,6 +744,8 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q
 }
 
 // stats[0] = lse * log2 e, stats[1] = delta = do . o for every row and head: D / 8 lanes each.
+// Memory bound; at the sizes that take it (7.3 MB at 512 tokens of 28/4 heads) a launch's own
+// 4 us.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_bwd_stats(AttnArgs a) {
     constexpr int LN = D / 8;
@@ -750,7 +768,8 @@ __global__ __launch_bounds__(256) void k_attn_bwd_stats(AttnArgs a) {
 }
 
 // dk = RNbf(scale * sum of the shares), dv = RNbf(sum of the shares), in split order; four
-// of a lane's elements a thread, 2 KW NB workgroups a tile and kv head.
+// of a lane's elements a thread, 2 KW NB workgroups a tile and kv head. 8 shares of 512 tokens
+// and 4 heads of 128 (16.8 MB) take 4 us.
 template <int D>
 __global__ __launch_bounds__(256) void k_attn_bwd_join(AttnArgs a) {
     constexpr int KW = kKeyWaves, NB = D / 32;
