@@ -562,29 +562,31 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
     return ((size_t(tile) * a.hkv + kvh) * a.splits + split) * (2 * kKeyWaves * 8 * D);
 }
 
-// One workgroup: 8 waves, KW blocks of 32 keys of one kv head x QW. K fragments stay
-// in registers, V in LDS (both in registers would leave room for one wave a SIMD only); the
+// One workgroup: 8 waves, KW blocks of 32 keys of one kv head x QW. K and V stay in LDS; the
 // queries of the G heads pass through LDS in tiles of 32 QW (Q, dO, lse, delta), 32 to each of
 // the QW waves of a key block, whose sums meet at the end. Per 32 queries S = Q K^T,
 // dP = dO V^T (a key in a lane), dv^T += dO^T P, dk^T += Q^T dS.
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
-// Bound by LDS reads beside the products (each wave reads Q and dO twice, by rows and
-// transposed, and V: two products an operand, against a row's four in the forward) and by power:
-// 8192 tokens of 64/8 heads of 128 2100 us, 1.05 PFLOP/s (S, dP, dv and dk: 8 D operations a
-// pair). Measured and left out: V in registers too, which leaves one wave a SIMD (with the walk
-// below the whole backward 4027 -> 3497 us without it); the products ordered by hand (slower), a
-// higher wave priority around them (no change); the second wave of a key block half a tile
-// behind the first, whose state spills (five times slower at width 128, 15 % at 64).
-// LDS of a dk/dv workgroup: V; two pairs of a tile's Q, and its dO with the rows' lse * log2 e
+// Bound by LDS reads beside the products (every operand of S and dP is read anew, Q and dO once
+// more transposed) and at long lengths by power: 8192 tokens of 64/8 heads of 128 2050 us,
+// 1.07 PFLOP/s (S, dP, dv and dk: 8 D operations a pair). K and V in registers leave room for
+// one wave a SIMD only (the whole backward 4027 us at those sizes, against 3497 with V in LDS);
+// K alone there leaves none for fragments read ahead (1024 tokens of 28/4 heads of 128 61.2 ->
+// 57.5 us with K in LDS too, 512 of 64/8 51.0 -> 48.5). Measured and left out: the products
+// ordered by hand (slower); a higher wave priority around them, or for one of the two waves of a
+// SIMD (no change); the second wave of a key block half a tile behind the first, whose third
+// pair of buffers and state do not fit beside K (with K in registers five times slower at width
+// 128, 15 % at 64).
+// LDS of a dk/dv workgroup: K; V; two pairs of a tile's Q, and its dO with the rows' lse * log2 e
 // and delta behind it.
 template <int D>
 struct DkvLds {
-    static constexpr int QW = 2, BQ = 32 * QW, QB = BQ * 2 * D, SB = 256, DB = QB + 2 * SB, VB = 64 * kKeyWaves * D;
+    static constexpr int QW = 2, BQ = 32 * QW, QB = BQ * 2 * D, SB = 256, DB = QB + 2 * SB, KB = 64 * kKeyWaves * D;
 };
 
 template <int D, bool FINE>
-__device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sV, char* sQ0, char* sD0, char* sQ1,
+__device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sK, char* sV, char* sQ0, char* sD0, char* sQ1,
                                         char* sD1) {
     using L = DkvLds<D>;
     constexpr int KW = kKeyWaves, QW = L::QW, W = KW * QW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = L::BQ;
@@ -610,15 +612,12 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
     const int total = G * (tile_hi + 1 - tile_lo);
     const int i0 = int(int64_t(split) * total / a.splits), i1 = int(int64_t(split + 1) * total / a.splits);
 
-    bf16x8 kf[KS];
     {
         const size_t at = (size_t(t.begin) + t.row0) * ldk + kvh * D;
         const int rows = min(t.len - t.row0, BM);
-        const auto rk = make_rsrc(a.k + at, uint32_t(rows - 1) * uint32_t(ldk) * 2u + 2u * D);
-        const uint32_t o = uint32_t(32 * kw + (lane & 31)) * uint32_t(ldk) * 2u + 16u * h;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) kf[s] = as_bf16x8(buf_load16(rk, o + 32u * s));
-        TileCopy<D, BM, W>(wave, lane, ldk).issue(a.v + at, rows, ldk, sV, wave);
+        const TileCopy<D, BM, W> keys(wave, lane, ldk);
+        keys.issue(a.k + at, rows, ldk, sK, wave);
+        keys.issue(a.v + at, rows, ldk, sV, wave);
     }
     const LdsMap<D> map(lane);
     const TileCopy<D, BQ, W> copy(wave, lane, ldq);
@@ -653,10 +652,10 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
         f32x16 s = zero16(), dp;
 #pragma unroll
         for (int e = 0; e < 16; ++e) dp[e] = -stat[SB / 16 + e / 4 * 2][e % 4];  // dP - delta straight from the accumulator
-        const char* v = sV + kw * 64 * D;
+        const char *v = sV + kw * 64 * D, *k = sK + kw * 64 * D;
 #pragma unroll
         for (int e = 0; e < KS; ++e) {
-            s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), kf[e], s);
+            s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), lds_frag(k + map.row_chunk[e]), s);
             dp = mfma32x32x16(lds_frag(d + map.row_chunk[e]), lds_frag(v + map.row_chunk[e]), dp);
         }
         if (a.causal && q0 < k_lo + 31) {
@@ -684,7 +683,7 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
         }
     };
     double_buffered(i0, i1, sQ0, sD0, sQ1, sD1, stage, compute);
-    wait_vmcnt<0>();  // without a tile to use it, V's copy is still under way
+    wait_vmcnt<0>();  // without a tile to use them, the copies of K and V are still under way
     // The sums of a key block: its second wave hands them to the first through the staging
     // buffers, dk first, then dv.
     auto meet = [&](f32x16(&x)[NB]) {
@@ -723,8 +722,8 @@ __device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char*
 template <int D>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
     using L = DkvLds<D>;
-    __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
-    bwd_dkv<D, false>(a, blockIdx.x, sV, sQ0, sD0, sQ1, sD1);
+    __shared__ __align__(1024) char sK[L::KB], sV[L::KB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
+    bwd_dkv<D, false>(a, blockIdx.x, sK, sV, sQ0, sD0, sQ1, sD1);
 }
 
 // Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
@@ -736,11 +735,11 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
 template <int D, bool FINE>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q_wgs) {
     using L = DkvLds<D>;
-    __shared__ __align__(1024) char sV[L::VB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
+    __shared__ __align__(1024) char sK[L::KB], sV[L::KB], sQ0[L::QB], sD0[L::DB], sQ1[L::QB], sD1[L::DB];
     if (blockIdx.x < q_wgs)
         bwd_dq<D, 4, 2, false, FINE || D == 32>(a, blockIdx.x, sQ0, sD0, sQ1, sD1);
     else
-        bwd_dkv<D, FINE>(a, blockIdx.x - q_wgs, sV, sQ0, sD0, sQ1, sD1);
+        bwd_dkv<D, FINE>(a, blockIdx.x - q_wgs, sK, sV, sQ0, sD0, sQ1, sD1);
 }
 
 // stats[0] = lse * log2 e, stats[1] = delta = do . o for every row and head: D / 8 lanes each.
