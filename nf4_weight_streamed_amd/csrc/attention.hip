@@ -569,8 +569,8 @@ __device__ __forceinline__ size_t share_of(int tile, int kvh, int split, const A
 // With splits > 1 the (head, query tile) list is cut into contiguous ranges, one a
 // workgroup, whose fp32 shares k_attn_bwd_join adds in order.
 // Bound by LDS reads beside the products (every operand of S and dP is read anew, Q and dO once
-// more transposed) and at long lengths by power: 8192 tokens of 64/8 heads of 128 2050 us,
-// 1.07 PFLOP/s (S, dP, dv and dk: 8 D operations a pair). K and V in registers leave room for
+// more transposed) and at long lengths by power: 8192 tokens of 64/8 heads of 128 2070 us,
+// 1.06 PFLOP/s (S, dP, dv and dk: 8 D operations a pair). K and V in registers leave room for
 // one wave a SIMD only (the whole backward 4027 us at those sizes, against 3497 with V in LDS);
 // K alone there leaves none for fragments read ahead (1024 tokens of 28/4 heads of 128 61.2 ->
 // 57.5 us with K in LDS too, 512 of 64/8 51.0 -> 48.5). Measured and left out: the products
