@@ -426,8 +426,7 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 // kernel behind this one reads it). R, C and B as in the forward. FINE: for heads 32 wide, whose
 // scores spread further with the length of q than those of wider heads and leave a row to its
 // largest few, and for calls of at most 64 tokens. Measured (us, one bf16 value for dS and two):
-// 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 28/4 heads of 128 18.1, 19.7, of
-// 64/8 15.4, 16.6.
+// 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 28/4 heads of 128 18.1, 18.9.
 // Bound as the forward: 8192 tokens of 64/8 heads of 128 1364 us, 1.21 PFLOP/s with its share
 // (S, dP and dq: 6 D operations a pair).
 template <int D, int R, int C, bool STATS, bool FINE>
@@ -729,7 +728,7 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
 // Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
 // idle: the first q_wgs workgroups take 128 rows of dq each, with two waves a row. lse * log2 e
 // and delta come from k_attn_bwd_stats, since neither kind can wait for the other. FINE: calls
-// of at most 64 tokens. 512 tokens of 28/4 heads of 128: 25 us, of which the row statistics
+// of at most 64 tokens that k_attn_bwd_few does not take. 512 tokens of 28/4 heads of 128: 25 us, of which the row statistics
 // before and the join behind take 4 us each; 2048 tokens of 16/16 heads of 64 in three
 // sequences without a mask 57 us in all, 410 TFLOP/s.
 template <int D, bool FINE>
@@ -740,6 +739,137 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q
         bwd_dq<D, 4, 2, false, FINE || D == 32>(a, blockIdx.x, sQ0, sD0, sQ1, sD1);
     else
         bwd_dkv<D, FINE>(a, blockIdx.x - q_wgs, sK, sV, sQ0, sD0, sQ1, sD1);
+}
+
+// dk and dv of a call of few tokens: 32 keys of one kv head a workgroup, and each of its 8 waves
+// 32 queries of a head at a time, with a part of LDS and row statistics of its own, so that the
+// G heads of a kv head are taken side by side; the waves' sums meet at the end, in wave order.
+// As bwd_dkv with FINE otherwise. Bound by latency, of one load, one tile and two sums through
+// LDS: 2 tokens of 28/4 heads of 128 9.8 us with the launch.
+template <int D>
+struct FewLds {
+    static constexpr int W = 8, BB = 64 * D, SUM = 128 * D;  // bytes of 32 rows; of a wave's sums of dk or dv
+    static constexpr int ALL = W * 2 * BB;                   // every wave's Q and dO; then every wave's sums
+};
+
+template <int D>
+__device__ __forceinline__ void bwd_dkv_few(const AttnArgs& a, uint32_t block, char* sK, char* sV, char* sB, float* sStat) {
+    using L = FewLds<D>;
+    constexpr int W = L::W, KS = D / 16, NB = D / 32;
+    static_assert(L::ALL == W * L::SUM, "the sums take the place of Q and dO");
+    const int G = a.hq / a.hkv;
+    int kvh, tile;
+    if (!pick_item(block, a.hkv, a.tiles, kvh, tile)) return;
+    Tile t;
+    if (!find_tile(a, 32, tile, t)) return;
+    const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
+    const int ldq = a.hq * D, ldk = a.hkv * D;
+    const float c = a.scale * kLog2e;
+    {
+        const size_t at = (size_t(t.begin) + t.row0) * ldk + kvh * D;
+        const TileCopy<D, 32, W> keys(wave, lane, ldk);
+        keys.issue(a.k + at, t.len - t.row0, ldk, sK, wave);
+        keys.issue(a.v + at, t.len - t.row0, ldk, sV, wave);
+    }
+    const LdsMap<D> map(lane);
+    const TileCopy<D, 32, 1> copy(0, lane, ldq);
+    char *q = sB + wave * 2 * L::BB, *d = q + L::BB;
+    float* stat = sStat + wave * 64;
+
+    f32x16 dk[NB], dv[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) dk[nb] = zero16(), dv[nb] = zero16();
+    const int first_q = a.causal ? t.row0 / 32 : 0, nq = (t.len - 1) / 32 + 1 - first_q;  // a head's blocks that see a key
+    const int total = G * nq;
+    for (int i0 = 0; i0 < total; i0 += W) {
+        const int i = i0 + wave, q0 = (first_q + i % nq) * 32;
+        if (i0 > 0) __syncthreads();  // the last round's reads are done
+        if (i < total) {
+            const int head = kvh * G + i / nq, rows = t.len - q0, row = lane & 31;
+            const size_t at = (size_t(t.begin) + q0) * ldq + head * D;
+            copy.issue(a.q + at, rows, ldq, q, 0);
+            copy.issue(a.dO + at, rows, ldq, d, 0);
+            const uint32_t bytes = uint32_t(min(rows, 32) - 1) * uint32_t(ldq) * 2u + 2u * D;
+            const auto rd = make_rsrc(a.dO + at, bytes), ro = make_rsrc(a.o + at, bytes);
+            const uint32_t o = uint32_t(row) * uint32_t(ldq) * 2u + 16u * h;
+            float delta = 0.0f;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                const bf16x8 df = as_bf16x8(buf_load16(rd, o + 32u * s)), of = as_bf16x8(buf_load16(ro, o + 32u * s));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) delta = __builtin_fmaf(float(df[e]), float(of[e]), delta);
+            }
+            delta = sum_halves(delta);
+            if (h == 0) {
+                stat[row] = row < rows ? a.lse_in[size_t(head) * a.T + t.begin + q0 + row] * kLog2e : 0.0f;
+                stat[32 + row] = delta;
+            }
+        }
+        wait_vmcnt<0>();
+        __syncthreads();
+        if (i >= total) continue;
+        const f32x4* st = reinterpret_cast<const f32x4*>(stat) + h;
+        f32x16 s = zero16(), dp;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) dp[e] = -st[8 + e / 4 * 2][e % 4];
+#pragma unroll
+        for (int e = 0; e < KS; ++e) {
+            s = mfma32x32x16(lds_frag(q + map.row_chunk[e]), lds_frag(sK + map.row_chunk[e]), s);
+            dp = mfma32x32x16(lds_frag(d + map.row_chunk[e]), lds_frag(sV + map.row_chunk[e]), dp);
+        }
+        if (a.causal && q0 < t.row0 + 31) {
+            const int first = t.row0 + (lane & 31) - q0 - 4 * h;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (8 * (e / 4) + e % 4 < first) s[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            s[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c, -st[e / 4 * 2][e % 4]));
+            dp[e] *= s[e];
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const bf16x8 p = pack8(s, g), ds = pack8(dp, g), rest = pack8_rest(dp, g);
+            const char *dg = d + g * 32 * D, *qg = q + g * 32 * D;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+                dv[nb] = mfma32x32x16(lds_frag_tr(dg + map.tr[nb][0], dg + map.tr[nb][1]), p, dv[nb]);
+                const bf16x8 qt = lds_frag_tr(qg + map.tr[nb][0], qg + map.tr[nb][1]);
+                dk[nb] = mfma32x32x16(qt, ds, dk[nb]);
+                dk[nb] = mfma32x32x16(qt, rest, dk[nb]);
+            }
+        }
+    }
+    const int n_sums = min(total, W);
+    auto meet = [&](const f32x16(&x)[NB], uint16_t* out, float f) {
+        __syncthreads();
+        if (wave < n_sums) put_share(reinterpret_cast<f32x4*>(sB + wave * L::SUM) + lane, x);
+        __syncthreads();
+        for (int n = wave; n < 4 * NB; n += W) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(sB) + 64 * n + lane;
+            f32x4 sum = p[0];
+            for (int w = 1; w < n_sums; ++w) sum += p[w * (L::SUM / 16)];
+            const int key = t.row0 + (lane & 31);
+            if (key < t.len)
+                *reinterpret_cast<u32x2*>(out + (size_t(t.begin) + key) * ldk + kvh * D + 8 * n + 4 * h) =
+                    u32x2{pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f)};
+        }
+    };
+    meet(dk, a.dk, grad_scale(a, t));
+    meet(dv, a.dv, 1.0f);
+}
+
+// The whole backward of a call of few tokens in one launch.
+template <int D>
+__global__ __launch_bounds__(512, 2) void k_attn_bwd_few(AttnArgs a, uint32_t q_wgs) {
+    using L = FewLds<D>;
+    __shared__ __align__(1024) char sB[L::ALL], sK[L::BB], sV[L::BB];
+    __shared__ __align__(16) float sStat[L::W * 64];
+    if (blockIdx.x < q_wgs)
+        bwd_dq<D, 4, 2, false, true>(a, blockIdx.x, sB, sB + 128 * D, sB + 256 * D, sB + 384 * D);
+    else
+        bwd_dkv_few<D>(a, blockIdx.x - q_wgs, sK, sV, sB, sStat);
 }
 
 // stats[0] = lse * log2 e, stats[1] = delta = do . o for every row and head: D / 8 lanes each.
@@ -802,6 +932,15 @@ bool few_rows(int64_t T, int64_t hq, int64_t D) { return cdiv(T, 128) * hq < 256
 
 // Calls whose dk has dS as two bf16 values (dq: those, and all heads 32 wide).
 bool fine_ds(int64_t T) { return T <= 64; }
+
+// Those of them whose dk and dv take a kv head's queries side by side (bwd_dkv_few) instead of
+// one after the other: where a sequence's blocks of 32 queries of all G heads keep 8 waves busy
+// once. Us one after the other and side by side: 32 tokens of 28/4 heads of 128 18.8, 11.9, of 64/8
+// 15.3, 12.7; three times 20 tokens of 64/8 24.3, 13.1; 40 of 4/1 heads of 32 10.1, 5.9; with
+// two rounds of blocks 64 tokens of 64/8 15.6, 19.4.
+bool few_tokens(int64_t T, int64_t n_seqs, int64_t hq, int64_t hkv) {
+    return fine_ds(T) && hq / hkv * cdiv(T, std::max<int64_t>(1, n_seqs) * 32) <= 8;
+}
 
 // Whether the backward takes both kinds of workgroups in one launch: up to one and a half
 // workgroups of dq a CU. Us in two launches and in one: 512 tokens of 28/4 heads 39.8, 32.5;
@@ -881,7 +1020,7 @@ struct AttnBwdPlan {
 AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t n_seqs, int causal) {
     AttnBwdPlan p{};
     const size_t tiles = size_t(T) / (32 * kKeyWaves) + std::max<int64_t>(1, n_seqs);
-    p.splits = pick_splits(T, n_seqs, int(hq), int(hkv), int(D), causal);
+    p.splits = few_tokens(T, n_seqs, hq, hkv) ? 1 : pick_splits(T, n_seqs, int(hq), int(hkv), int(D), causal);
     p.stats_bytes = (size_t(T) * hq * 8 + 255) & ~size_t(255);
     p.part_bytes = p.splits > 1 ? size_t(2) * p.splits * tiles * 32 * kKeyWaves * hkv * D * 4 : 0;
     return p;
@@ -910,12 +1049,16 @@ int run_fwd(const AttnArgs& in, hipStream_t stream) {
 template <int D>
 int run_bwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
-    a.tiles = a.q_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 128));
+    const bool few = few_tokens(a.T, a.n_seqs, a.hq, a.hkv);
+    a.q_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 128));
+    a.tiles = few ? int(tiles_of(a.T, a.cu, a.n_seqs, 32)) : a.q_tiles;
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.q_tiles) * (a.hq / a.hkv));
     const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
     const int64_t wgs_join = a.splits > 1 ? int64_t(a.tiles) * a.hkv * (kKeyWaves * D / 16) : 0;
     if (int st = check_grid("nf4_attn_bwd", std::max(wgs + wgs_kv, wgs_join)); st != NF4_OK) return st;
-    if (one_launch(a.T, a.hq)) {
+    if (few) {
+        hipLaunchKernelGGL(k_attn_bwd_few<D>, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
+    } else if (one_launch(a.T, a.hq)) {
         hipLaunchKernelGGL(k_attn_bwd_stats<D>, dim3(unsigned(cdiv(int64_t(a.T) * a.hq * (D / 8), 256))), dim3(256), 0,
                            stream, a);
         const auto both = fine_ds(a.T) ? k_attn_bwd_both<D, true> : k_attn_bwd_both<D, false>;
