@@ -426,7 +426,7 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 // kernel behind this one reads it). R, C and B as in the forward. FINE: for heads 32 wide, whose
 // scores spread further with the length of q than those of wider heads and leave a row to its
 // largest few, and for calls of at most 64 tokens. Measured (us, one bf16 value for dS and two):
-// 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 28/4 heads of 128 18.1, 18.9.
+// 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 64/8 heads of 128 15.4, 15.6.
 // Bound as the forward: 8192 tokens of 64/8 heads of 128 1364 us, 1.21 PFLOP/s with its share
 // (S, dP and dq: 6 D operations a pair).
 template <int D, int R, int C, bool STATS, bool FINE>
@@ -935,7 +935,7 @@ bool fine_ds(int64_t T) { return T <= 64; }
 
 // Those of them whose dk and dv take a kv head's queries side by side (bwd_dkv_few) instead of
 // one after the other: where a sequence's blocks of 32 queries of all G heads keep 8 waves busy
-// once. Us one after the other and side by side: 32 tokens of 28/4 heads of 128 18.8, 11.9, of 64/8
+// once. Us one after the other and side by side: 32 tokens of 28/4 heads of 128 15.3, 11.9, of 64/8
 // 15.3, 12.7; three times 20 tokens of 64/8 24.3, 13.1; 40 of 4/1 heads of 32 10.1, 5.9; with
 // two rounds of blocks 64 tokens of 64/8 15.6, 19.4.
 bool few_tokens(int64_t T, int64_t n_seqs, int64_t hq, int64_t hkv) {
@@ -957,7 +957,9 @@ bool one_launch(int64_t T, int64_t hq) { return fine_ds(T) || cdiv(T, 128) * hq 
 // lengths, the longest workgroup has about twice the average's tiles. Measured (us, whole
 // backward): 8192 tokens of 64/8 heads 3545 with one share, 3618 with 2; 4096: 1170 with 1, 932
 // with 2; 512 of 28/4: 40.6, 32.3 and 38.0 with 4, 8 and 16; 1408 of 8/8, no mask: 51.6 and
-// 65.0 with 1 and 2; 1408 of 4/4 heads of 64: 31.7, 29.0 and 32.7 with 1, 2 and 4.
+// 65.0 with 1 and 2; 1408 of 4/4 heads of 64: 31.7, 29.0 and 32.7 with 1, 2 and 4; no
+// share has fewer than 1.7 tiles: 64 of 28/4 19.0 and 15.3 with 1 and 4 (1.75 tiles), 100 of 64/8
+// 18.7 and 20.9 with 4 and 8.
 int pick_splits(int64_t T, int64_t n_seqs, int hq, int hkv, int D, int causal) {
     const int64_t seqs = std::max<int64_t>(1, n_seqs);
     const double wgs = double(std::max(cdiv(T, 32 * kKeyWaves), seqs) * hkv);
@@ -968,7 +970,7 @@ int pick_splits(int64_t T, int64_t n_seqs, int hq, int hkv, int D, int causal) {
     const double dq_us = 0.5 * tile_us * avg + 5, share_bytes = wgs * (2 * 32 * kKeyWaves * D * 4);
     int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 16 && (s == 1 || tiles >= 1.9 * s); s *= 2) {
+    for (int s = 1; s <= 16 && (s == 1 || tiles >= 1.7 * s); s *= 2) {
         const double ends_us = s == 1 ? 3 + 2.0 * D / 128 : 4 + 4.0 * D / 128;
         const double run = tiles / s * tile_us, one = run + ends_us, bytes = s * share_bytes;
         const double all = wgs * s + dq_wgs, rounds = std::ceil(all / 256);
