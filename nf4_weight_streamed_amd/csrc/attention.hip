@@ -274,8 +274,8 @@ __device__ __forceinline__ void add_share(f32x16 (&x)[NB], const f32x4* p, float
 // ------------------------------------------------------------------ forward
 
 // One workgroup: R rows of waves x C waves, 32 queries of one head a row; K and V in tiles of
-// 64 keys, double buffered in LDS. R = 4, C = 1: a row is one wave, which takes both 32-key
-// blocks of a tile. R = 2, C = 2: its two waves take one block each and meet at the end: twice
+// 64 keys, double buffered in LDS. C = 1: a row is one wave, which takes both 32-key blocks of a
+// tile. C = 2: its two waves take one block each and meet at the end. R = 2, C = 2 makes twice
 // the workgroups, each half as long, for calls too small to fill the card. S^T = K Q^T puts a
 // query in a lane, so the softmax statistics are one register each. The running maximum is
 // raised, and o and the sum rescaled, only when some row's tile maximum exceeds it by more than
@@ -1034,6 +1034,12 @@ int check_grid(const char* fn, int64_t wgs) {
     return NF4_OK;
 }
 
+// Waves of a row in calls that fill the card (forward and dq): two for heads 64 wide, whose tiles
+// are too short for one wave to hide their loads, one for the others. Us with one and two: 64 wide, 8192 tokens of 16/16 heads 190, 176 and backward 535, 523; 4096, backward, 173, 154; 8192
+// of 14/2 backward 460, 470; 128 wide, 8192 of 64/8 990, 1150 and backward 3314, 3454; 32 wide equal.
+template <int D>
+constexpr int kRowWaves = D == 64 ? 2 : 1;
+
 template <int D>
 int run_fwd(const AttnArgs& in, hipStream_t stream) {
     AttnArgs a = in;
@@ -1044,7 +1050,7 @@ int run_fwd(const AttnArgs& in, hipStream_t stream) {
     if (few)
         hipLaunchKernelGGL((k_attn_fwd<D, 2, 2>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((k_attn_fwd<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attn_fwd<D, 4, kRowWaves<D>>), dim3(unsigned(wgs)), dim3(256 * kRowWaves<D>), 0, stream, a);
     return check_launch("nf4_attn_fwd");
 }
 
@@ -1066,7 +1072,7 @@ int run_bwd(const AttnArgs& in, hipStream_t stream) {
         const auto both = fine_ds(a.T) ? k_attn_bwd_both<D, true> : k_attn_bwd_both<D, false>;
         hipLaunchKernelGGL(both, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
     } else {
-        hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, 1>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, kRowWaves<D>>), dim3(unsigned(wgs)), dim3(256 * kRowWaves<D>), 0, stream, a);
         hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
     }
     if (a.splits > 1)
