@@ -1039,9 +1039,9 @@ AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t
     return p;
 }
 
-// Workgroups of a launch, refused where they would pass the 31-bit grid.
-int check_grid(const char* fn, int64_t wgs) {
-    if (wgs > 0x7FFFFFFF) return fail(NF4_E_SHAPE, "%s: too many tiles (%lld workgroups)", fn, (long long)wgs);
+// Workgroups of a launch, refused where its threads would pass the 32 bits of a grid.
+int check_grid(const char* fn, int64_t wgs, int threads) {
+    if (wgs * threads > 0xFFFFFFFFll) return fail(NF4_E_SHAPE, "%s: too many tiles (%lld workgroups)", fn, (long long)wgs);
     return NF4_OK;
 }
 
@@ -1057,7 +1057,7 @@ int run_fwd(const AttnArgs& in, hipStream_t stream) {
     const bool few = few_rows(a.T, a.hq, D);
     a.tiles = int(tiles_of(a.T, a.cu, a.n_seqs, few ? 64 : 128));
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.tiles) * (a.hq / a.hkv));
-    if (int st = check_grid("nf4_attn_fwd", wgs); st != NF4_OK) return st;
+    if (int st = check_grid("nf4_attn_fwd", wgs, 256 * kRowWaves<D>); st != NF4_OK) return st;
     if (few)
         hipLaunchKernelGGL((k_attn_fwd<D, 2, 2>), dim3(unsigned(wgs)), dim3(256), 0, stream, a);
     else
@@ -1074,7 +1074,7 @@ int run_bwd(const AttnArgs& in, hipStream_t stream) {
     const int64_t wgs = attn_grid(a.hkv, int64_t(a.q_tiles) * (a.hq / a.hkv));
     const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
     const int64_t wgs_join = a.splits > 1 ? int64_t(a.tiles) * a.hkv * (kKeyWaves * D / 16) : 0;
-    if (int st = check_grid("nf4_attn_bwd", std::max(wgs + wgs_kv, wgs_join)); st != NF4_OK) return st;
+    if (int st = check_grid("nf4_attn_bwd", std::max(wgs + wgs_kv, wgs_join), 512); st != NF4_OK) return st;
     if (few) {
         hipLaunchKernelGGL(k_attn_bwd_few<D>, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
     } else if (one_launch(a.T, a.hq)) {

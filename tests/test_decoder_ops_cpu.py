@@ -79,6 +79,17 @@ def test_attention_overlaps_are_refused(L):
         _err(L, bwd(**kw), L.NF4_E_ARG, "overlaps")
 
 
+def test_more_workgroups_than_a_grid_holds_are_refused(L):
+    """2^23 rows of 1024 heads: 2^26 workgroups of 256 threads and more (tensors of terabytes)."""
+    lib, T, big = L.raw(), 1 << 23, 1 << 44
+    at = [C.c_void_p(big * (i + 1)) for i in range(10)]
+    rc = lib.nf4_attn_fwd(at[0], at[1], at[2], T, 1024, 1024, 64, None, 0, 1, 0.125, at[3], at[4], None)
+    _err(L, rc, L.NF4_E_SHAPE, "workgroups")
+    rc = lib.nf4_attn_bwd(at[0], at[1], at[2], at[3], at[4], at[5], T, 1024, 1024, 64, None, 0, 1, 0.125, at[6], at[7], at[8],
+                          at[9], 1 << 43, None)
+    _err(L, rc, L.NF4_E_SHAPE, "workgroups")
+
+
 def test_rope_overlaps_are_refused(L):
     at = lambda i: C.c_void_p(0x100000 + 0x10000 * i)
     sections = (C.c_int * 1)(32)
