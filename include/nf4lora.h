@@ -336,7 +336,8 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
  * step; the buffers and the table, device memory of the caller that holds the list's
  * description (nf4_grad_list_table() bytes, 256-byte aligned), must outlive its calls, those
  * of captured graphs among them.
- * nf4_grad_list_create copies the description there on `stream` and waits for the copy.
+ * nf4_grad_list_create copies the description there on `stream` and waits for the copy
+ * (NF4_E_STATE while the stream is being captured).
  *   tensors  HOST array of n descriptions (read during the call only); dtype bf16 or fp32,
  *            mixed freely; pointers aligned to their elements; count 0 allowed (pointers
  *            then ignored); out == grad scales in place

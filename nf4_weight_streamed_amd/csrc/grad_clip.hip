@@ -284,6 +284,11 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
             return fail(NF4_E_SHAPE, "%s: %zu pieces do not fit the table", fn, chunks.size());
         if (!chunks.empty()) {
             hipStream_t s = static_cast<hipStream_t>(stream);
+            hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
+            if (hipStreamIsCapturing(s, &capture) != hipSuccess || capture != hipStreamCaptureStatusNone) {
+                (void)hipGetLastError();
+                return fail(NF4_E_STATE, "%s: a list is made before a capture, not within one", fn);
+            }
             hipError_t e = hipMemcpyAsync(table, chunks.data(), chunks.size() * sizeof(Chunk), hipMemcpyHostToDevice, s);
             if (e == hipSuccess) e = hipStreamSynchronize(s);  // the source is this call's own
             if (e != hipSuccess) return fail(NF4_E_HIP, "%s: %s", fn, hipGetErrorString(e));

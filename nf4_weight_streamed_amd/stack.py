@@ -563,7 +563,7 @@ class NF4Stack:
     def clip_grads(self, max_norm: float) -> torch.Tensor:
         """Scale every adapter gradient of the last backward in place by
         min(1, max_norm / (norm + 1e-6)); returns their global norm before that (fp32 [1],
-        on the device)."""
+        on the device). The first call makes the list of them, before any capture."""
         with self._on_compute():
             if self._grad_list is None:
                 self._grad_list = lib.GradList([t for layer in self.grads for name in PROJS for t in layer[name]])

@@ -162,6 +162,24 @@ def test_python_refusals(gpu_lib):
         gl.norm()
 
 
+def test_a_list_is_not_made_within_a_capture(gpu_lib):
+    """Making one waits for a copy: refused, and the capture around it stays whole."""
+    lib = gpu_lib
+    a, x = torch.full((64,), 2.0, device="cuda"), torch.zeros(1, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        x.add_(1)
+        with pytest.raises(lib.Nf4Error, match="before a capture"):
+            lib.GradList([a])
+        x.add_(1)
+    for n in (1, 2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert x.item() == 2.0 * n
+    assert lib.GradList([a]).norm().item() == 16.0
+
+
 def test_list_freed_while_another_stream_still_reads_its_table(gpu_lib):
     """A list used on a side stream and dropped at once: its table's memory is not handed out
     again before that stream is done (the stream is held up by a bounded spin)."""
