@@ -596,8 +596,8 @@ struct DkvLds {
 };
 
 template <int D, bool FINE>
-__device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sK, char* sV, char* sQ0, char* sD0, char* sQ1,
-                                        char* sD1) {
+__device__ __forceinline__ void bwd_dkv(const AttnArgs& a, uint32_t block, char* sK, char* sV, char* sQ0, char* sD0,
+                                        char* sQ1, char* sD1) {
     using L = DkvLds<D>;
     constexpr int KW = kKeyWaves, QW = L::QW, W = KW * QW, BM = 32 * KW, KS = D / 16, NB = D / 32, BQ = L::BQ;
     constexpr int QB = L::QB, SB = L::SB;
@@ -739,9 +739,9 @@ __global__ __launch_bounds__(512, 2) void k_attn_bwd_dkv(AttnArgs a) {
 // Both in one launch, for calls whose dq and dk/dv workgroups would each leave the card partly
 // idle: the first q_wgs workgroups take 128 rows of dq each, with two waves a row. lse * log2 e
 // and delta come from k_attn_bwd_stats, since neither kind can wait for the other. FINE: calls
-// of at most 64 tokens that k_attn_bwd_few does not take. 512 tokens of 28/4 heads of 128: 25 us, of which the row statistics
-// before and the join behind take 4 us each; 2048 tokens of 16/16 heads of 64 in three
-// sequences without a mask 57 us in all, 410 TFLOP/s.
+// of at most 64 tokens that k_attn_bwd_few does not take. 512 tokens of 28/4 heads of 128: 24 us,
+// with the row statistics before and the join behind of 4 us each; 2048 tokens of 16/16 heads of
+// 64 in three sequences without a mask 58 us, 400 TFLOP/s.
 template <int D, bool FINE>
 __global__ __launch_bounds__(512, 2) void k_attn_bwd_both(AttnArgs a, uint32_t q_wgs) {
     using L = DkvLds<D>;
@@ -1046,8 +1046,10 @@ int check_grid(const char* fn, int64_t wgs, int threads) {
 }
 
 // Waves of a row in calls that fill the card (forward and dq): two for heads 64 wide, whose tiles
-// are too short for one wave to hide their loads, one for the others. Us with one and two: 64 wide, 8192 tokens of 16/16 heads 190, 176 and backward 535, 523; 4096, backward, 173, 154; 8192
-// of 14/2 backward 460, 470; 128 wide, 8192 of 64/8 990, 1150 and backward 3314, 3454; 32 wide equal.
+// are too short for one wave to hide their loads, one for the others. Us with one and two: 64
+// wide, 8192 tokens of 16/16 heads 190, 176 and backward 535, 523; 4096, backward, 173, 154; 8192
+// of 14/2 backward 460, 470; 128 wide, 8192 of 64/8 990, 1150 and backward 3314, 3454; 32 wide
+// equal.
 template <int D>
 constexpr int kRowWaves = D == 64 ? 2 : 1;
 
@@ -1146,7 +1148,8 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
     const size_t q_bytes = size_t(T) * hq * head_dim * 2, k_bytes = size_t(T) * hkv * head_dim * 2;
     const size_t lse_bytes = size_t(T) * hq * 4, cu_bytes = cu_seqlens ? (size_t(n_seqs) + 1) * 4 : 0;
     const ByteRange r[] = {{dq, q_bytes}, {dk, k_bytes}, {dv, k_bytes}, {ws, p.stats_bytes + p.part_bytes}, {q, q_bytes},
-                           {k, k_bytes}, {v, k_bytes}, {o, q_bytes}, {dO, q_bytes}, {lse, lse_bytes}, {cu_seqlens, cu_bytes}};
+                           {k, k_bytes}, {v, k_bytes}, {o, q_bytes}, {dO, q_bytes}, {lse, lse_bytes},
+                           {cu_seqlens, cu_bytes}};
     if (st = check_apart(fn, r, 4, 11); st != NF4_OK) return st;
     AttnArgs a{};
     a.q = q, a.k = k, a.v = v, a.o = o, a.dO = dO, a.lse_in = lse, a.dq = dq, a.dk = dk, a.dv = dv, a.cu = cu_seqlens;
