@@ -9,6 +9,7 @@ There is no fallback: if the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -601,6 +602,7 @@ def _attn_args(q, k, v, head_dim, cu_seqlens, scale):
     return (t, hq, hkv, n_seqs, head_dim ** -0.5 if scale is None else float(scale)), q_shape, k_shape
 
 
+@functools.lru_cache(maxsize=256)  # of the sizes alone; 0.7 us a call of attn_bwd
 def attn_bwd_workspace_bytes(T: int, hq: int, hkv: int, head_dim: int, n_seqs: int = 0) -> int:
     return int(_lib.nf4_attn_bwd_workspace(T, hq, hkv, head_dim, n_seqs))
 
