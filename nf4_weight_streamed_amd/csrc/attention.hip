@@ -367,9 +367,10 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
             for (int e = 0; e < 16; ++e) mt = fmaxf(mt, s[b][e]);
         mt = max_halves(mt) * c;
         if (__any(mt > m + 8.0f)) {
-            m = fmaxf(m, mt);
-            const float to = m > -INFINITY ? m : 0.0f;
-            const float f = exp2f(base - to);
+            const float top = fmaxf(m, mt), to = top > -INFINITY ? top : 0.0f;
+            // before the first key o and l are 0, and 2^(0 - to) may be infinite
+            const float f = m > -INFINITY ? exp2f(base - to) : 0.0f;
+            m = top;
             base = to;
             l *= f;
 #pragma unroll

@@ -319,3 +319,34 @@ def test_python_refusals(gpu_lib):
     o, lse = lib.attn_fwd(q[:0], k[:0], k[:0], 64)   # no rows: a no-op
     assert o.shape == (0, 128) and lse.shape == (2, 0)
     lib.attn_bwd(q[:0], k[:0], k[:0], o, lse, o, 64)
+
+
+def _away(t, hq, hkv, d, k_scores):
+    """q and k whose score at key j is about k_scores[j] for every row, heads, elements and rows varying."""
+    c = _case(t, hq, hkv, d)
+    # E|N| = 0.8: a dot product of D magnitudes is 0.64 D, scaled 0.64 sqrt(D)
+    c["q"] = _bits(np.abs(O.bf16_bits_to_f64(c["q"])) / 1.5)
+    c["k"] = _bits(np.abs(O.bf16_bits_to_f64(c["k"])) * (np.asarray(k_scores) / (0.64 * d ** 0.5))[:, None])
+    return c
+
+
+# (query heads, kv heads) whose 130 rows take the forward's small and its full workgroups, and the
+# backward's one launch and its two
+FILLS = {32: (512, 256), 64: (384, 192), 128: (256, 128)}
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_scores_far_below_zero(gpu_lib, d, full):
+    """Rows whose first keys' scores, or all of them, lie far below zero (e^S is zero in fp32): rising
+    and falling along the keys, at the first keys only, and in sequences of one token."""
+    t = 130
+    hq, hkv = FILLS[d] if full else (2, 1)
+    ramp = np.linspace(-1000.0, -100.0, t)
+    for k_scores in (ramp, ramp[::-1]):
+        for causal in (True, False):
+            _check(gpu_lib, _away(t, hq, hkv, d, k_scores), d, causal=causal)
+    for first in (32, 64):
+        _check(gpu_lib, _away(t, hq, hkv, d, np.where(np.arange(t) < first, -400.0, 2.0)), d)
+    _check(gpu_lib, _away(t, hq, hkv, d, ramp), d, [1, 1, 0, 31, 1, 65, 1, 30])
+    _check(gpu_lib, _away(t, hq, hkv, d, np.full(t, -250.0)), d, [1] * t)
