@@ -350,3 +350,13 @@ def test_scores_far_below_zero(gpu_lib, d, full):
         _check(gpu_lib, _away(t, hq, hkv, d, np.where(np.arange(t) < first, -400.0, 2.0)), d)
     _check(gpu_lib, _away(t, hq, hkv, d, ramp), d, [1, 1, 0, 31, 1, 65, 1, 30])
     _check(gpu_lib, _away(t, hq, hkv, d, np.full(t, -250.0)), d, [1] * t)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d,hq,hkv", [(64, 256, 128), (128, 256, 64), (32, 352, 352)])
+def test_calls_that_fill_the_card(gpu_lib, d, hq, hkv, causal):
+    """Three row tiles of enough heads for the forward's full workgroups and the backward's dq and dk/dv in
+    launches of their own, one sequence and several."""
+    _check(gpu_lib, _case(260, hq, hkv, d), d, causal=causal)
+    if causal:
+        _check(gpu_lib, _case(260, hq, hkv, d), d, [3, 0, 130, 127])
