@@ -100,19 +100,22 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const Chunk* __restrict_
     if (threadIdx.x == 0) shares[blockIdx.x] = sum;
 }
 
-__device__ __forceinline__ u32x4 scale16(u32x4 v, float f, bool bf16) {
+// The factor stays fp64: as fp32 it would lose bits below 2^-126, which bounds far below the norm reach.
+__device__ __forceinline__ float scaled(float v, double f) { return float(double(v) * f); }
+
+__device__ __forceinline__ u32x4 scale16(u32x4 v, double f, bool bf16) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (bf16)
-            v[e] = pack_bf16x2(__uint_as_float(v[e] << 16) * f, __uint_as_float(v[e] & 0xFFFF0000u) * f);
+            v[e] = pack_bf16x2(scaled(__uint_as_float(v[e] << 16), f), scaled(__uint_as_float(v[e] & 0xFFFF0000u), f));
         else
-            v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            v[e] = __float_as_uint(scaled(__uint_as_float(v[e]), f));
     }
     return v;
 }
 
 template <bool LOAD_NT, bool STORE_NT>
-__device__ __forceinline__ void chunk_scale(const Chunk ch, float f) {
+__device__ __forceinline__ void chunk_scale(const Chunk ch, double f) {
     const bool bf16 = ch.flags & kBf16;
     const uint32_t per = bf16 ? 8 : 4;
     const uint32_t wide = (ch.flags & kWide) ? ch.count / per : 0;
@@ -135,9 +138,9 @@ __device__ __forceinline__ void chunk_scale(const Chunk ch, float f) {
     for (; i < wide; i += kThreads) d[i] = scale16(p[i], f, bf16);
     for (uint32_t e = wide * per + threadIdx.x; e < ch.count; e += kThreads) {
         if (bf16)
-            static_cast<uint16_t*>(ch.out)[e] = bf16_bits(bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]) * f);
+            static_cast<uint16_t*>(ch.out)[e] = bf16_bits(scaled(bf16_to_f32(static_cast<const uint16_t*>(ch.in)[e]), f));
         else
-            static_cast<float*>(ch.out)[e] = static_cast<const float*>(ch.in)[e] * f;
+            static_cast<float*>(ch.out)[e] = scaled(static_cast<const float*>(ch.in)[e], f);
     }
 }
 
@@ -156,7 +159,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const Chunk* __restrict
     const double q = double(max_norm) / (total + 1e-6);
     const bool clip = q < 1.0 && total < __builtin_inf();
     if (in_place && !clip) return;
-    const float f = clip ? float(q) : 1.0f;
+    const double f = clip ? q : 1.0;
     int c = n - 1 - int(blockIdx.x);
     if (stream == 0) {
         for (; c >= 0; c -= gridDim.x) chunk_scale<false, false>(chunks[c], f);

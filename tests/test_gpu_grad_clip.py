@@ -218,3 +218,22 @@ def test_outputs_of_a_side_stream_call_are_that_streams_memory(gpu_lib):
     assert n.data_ptr() != at
     torch.cuda.synchronize()
     assert n.item() == pytest.approx(math.sqrt(5000), rel=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("size,max_norm", [(1e38, 1e-3), (3e38, 1e-5), (1e30, 1e-12), (1e-30, 1e-38)])
+def test_factors_below_fp32s_normal_range(gpu_lib, dtype, size, max_norm):
+    """max_norm / norm down to 10^-45, where fp32 holds a few bits or none: the scaled values are right
+    to their own rounding all the same (values that would round below the normal range left out)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    t = ((torch.rand(5000, generator=g, device="cuda") * 2 - 1) * size).to(dtype)
+    want = _norm64([t])
+    exact = t.double() * (max_norm / (want + 1e-6))
+    gpu_lib.GradList([t]).clip(max_norm)
+    torch.cuda.synchronize()
+    normal = exact.abs() >= 2.0 ** -126
+    assert normal.any() or max_norm == 1e-38
+    # one rounding to the type, for bf16 behind one to fp32; the fp64 factor and product below 2^-48
+    lim = exact.abs() * (_ulp(dtype) + 2.0 ** -24 + 2.0 ** -48) + torch.where(normal, 0.0, 2.0 ** -126)
+    assert torch.all((t.double() - exact).abs() <= lim)
