@@ -161,12 +161,17 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const Chunk* __restrict
     if (in_place && !clip) return;
     const double f = clip ? q : 1.0;
     int c = n - 1 - int(blockIdx.x);
-    if (stream == 0) {
-        for (; c >= 0; c -= gridDim.x) chunk_scale<false, false>(chunks[c], f);
-        return;
+    auto leave = [&](const Chunk& ch) { return !clip && ch.in == ch.out; };  // in place, among others that are not
+    for (; c >= stream; c -= gridDim.x) {
+        const Chunk ch = chunks[c];
+        if (leave(ch)) continue;
+        if (stream == 0)
+            chunk_scale<false, false>(ch, f);
+        else
+            chunk_scale<false, true>(ch, f);
     }
-    for (; c >= stream; c -= gridDim.x) chunk_scale<false, true>(chunks[c], f);
-    for (; c >= 0; c -= gridDim.x) chunk_scale<true, true>(chunks[c], f);
+    for (; c >= 0; c -= gridDim.x)
+        if (const Chunk ch = chunks[c]; !leave(ch)) chunk_scale<true, true>(ch, f);
 }
 
 size_t elem_bytes(int dtype) { return dtype == NF4_DTYPE_BF16 ? 2 : 4; }

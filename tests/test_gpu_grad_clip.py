@@ -237,3 +237,18 @@ def test_factors_below_fp32s_normal_range(gpu_lib, dtype, size, max_norm):
     # one rounding to the type, for bf16 behind one to fp32; the fp64 factor and product below 2^-48
     lim = exact.abs() * (_ulp(dtype) + 2.0 ** -24 + 2.0 ** -48) + torch.where(normal, 0.0, 2.0 ** -126)
     assert torch.all((t.double() - exact).abs() <= lim)
+
+
+def test_unscaled_tensors_in_place_are_left_alone_beside_others(gpu_lib):
+    """In a list of tensors in place and not, the former keep every bit when nothing is to be scaled: below
+    the bound, and with a norm that is not finite, signalling NaN among the gradients."""
+    for bad in (False, True):
+        a, b = torch.randn(5000, device="cuda"), torch.randn(3001, device="cuda")
+        if bad:
+            a.view(torch.int32)[7] = 0x7F800001
+            a.view(torch.int32)[4999] = 0x7FA00000
+        bits, out = a.view(torch.int32).clone(), torch.zeros_like(b)
+        n = gpu_lib.GradList([a, b], [a, out]).clip(1e6)
+        torch.cuda.synchronize()
+        assert math.isnan(n.item()) == bad
+        assert torch.equal(a.view(torch.int32), bits) and torch.equal(out, b)
