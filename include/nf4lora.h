@@ -342,7 +342,7 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
  *            mixed freely; pointers aligned to their elements; count 0 allowed (pointers
  *            then ignored); out == grad scales in place
  * NF4_E_ARG when a tensor's out overlaps any other range of the list (the same tensor
- * twice, a shifted overlap with its own grad). n <= 2^20, count <= 2^36.
+ * twice, a shifted overlap with its own grad), or the table a tensor. n <= 2^20, count <= 2^36.
  */
 typedef struct {
     const void* grad; /* device */
@@ -359,7 +359,8 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
 /* Frees the handle (host memory only); calls already enqueued keep using the table. */
 int nf4_grad_list_destroy(nf4_grad_list* list);
 
-/* Bytes of device workspace of the two calls below (256-byte aligned; one per call that may run at the same time). */
+/* Bytes of device workspace of the two calls below (256-byte aligned; one per call that may run at the same time).
+ * A norm or workspace that overlaps the other, the list's table or one of its tensors is refused (NF4_E_ARG). */
 size_t nf4_grad_workspace(void);
 
 /* *norm (device fp32) = n; the outs are not touched. An empty list gives 0. */

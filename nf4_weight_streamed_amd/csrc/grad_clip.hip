@@ -12,7 +12,9 @@
 // launch.
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "../../include/nf4lora.h"
@@ -174,6 +176,12 @@ __global__ __launch_bounds__(kThreads) void k_grad_scale(const Chunk* __restrict
         if (const Chunk ch = chunks[c]; !leave(ch)) chunk_scale<true, true>(ch, f);
 }
 
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+};
+bool by_address(const Range& a, const Range& b) { return a.lo < b.lo; }
+
 size_t elem_bytes(int dtype) { return dtype == NF4_DTYPE_BF16 ? 2 : 4; }
 
 // The pieces of one tensor: a short head up to the first 16-byte boundary that both buffers
@@ -233,6 +241,13 @@ struct nf4_grad_list {
     int n;         // pieces
     int in_place;  // every tensor's out is its grad
     int stream;    // first pieces that the caches cannot hold from one launch to the next
+    std::vector<nf4::Range> memory;  // of the tensors and the table, in order of address, joined where they meet
+
+    bool meets(const void* p, size_t bytes) const {
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        const auto after = std::upper_bound(memory.begin(), memory.end(), nf4::Range{lo, lo, false}, nf4::by_address);
+        return (after != memory.end() && after->lo < lo + bytes) || (after != memory.begin() && std::prev(after)->hi > lo);
+    }
 };
 
 using namespace nf4;
@@ -261,10 +276,6 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
                     need, table_bytes);
     try {
         // a written range must not meet another tensor's range: the pieces run concurrently
-        struct Range {
-            uintptr_t lo, hi;
-            bool written;
-        };
         std::vector<Range> ranges;
         std::vector<Chunk> chunks;
         int in_place = 1;
@@ -281,7 +292,7 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
             }
             pieces(t, piece, [&](const Chunk& c) { chunks.push_back(c); });
         }
-        std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        std::sort(ranges.begin(), ranges.end(), by_address);
         uintptr_t written = 0, read = 0;
         for (const Range& r : ranges) {
             if (r.lo < written || (r.written && r.lo < read))
@@ -290,6 +301,19 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
         }
         if (chunks.size() * sizeof(Chunk) > table_bytes)
             return fail(NF4_E_SHAPE, "%s: %zu pieces do not fit the table", fn, chunks.size());
+        const uintptr_t at = reinterpret_cast<uintptr_t>(table);
+        const Range own{at, at + chunks.size() * sizeof(Chunk), false};
+        for (const Range& r : ranges)
+            if (r.lo < own.hi && own.lo < r.hi) return fail(NF4_E_ARG, "%s: the table overlaps a tensor", fn);
+        ranges.push_back(own);
+        std::sort(ranges.begin(), ranges.end(), by_address);
+        std::vector<Range> memory;
+        for (const Range& r : ranges) {
+            if (memory.empty() || r.lo > memory.back().hi)
+                memory.push_back(r);
+            else
+                memory.back().hi = std::max(memory.back().hi, r.hi);
+        }
         if (!chunks.empty()) {
             hipStream_t s = static_cast<hipStream_t>(stream);
             hipStreamCaptureStatus capture = hipStreamCaptureStatusNone;
@@ -302,7 +326,8 @@ int nf4_grad_list_create(const nf4_grad_tensor* tensors, int n, void* table, siz
             if (e != hipSuccess) return fail(NF4_E_HIP, "%s: %s", fn, hipGetErrorString(e));
         }
         *out = new nf4_grad_list{static_cast<const Chunk*>(table), int(chunks.size()), in_place,
-                                 double(all) > kCacheBytes ? int(double(chunks.size()) * (1.0 - kCacheBytes / double(all))) : 0};
+                                 double(all) > kCacheBytes ? int(double(chunks.size()) * (1.0 - kCacheBytes / double(all))) : 0,
+                                 std::move(memory)};
     } catch (const std::bad_alloc&) {
         return fail(NF4_E_OOM, "%s: out of host memory", fn);
     }
@@ -325,6 +350,9 @@ static int grad_run(const char* fn, const nf4_grad_list* list, float max_norm, i
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < nf4_grad_workspace())
         return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
                     nf4_grad_workspace(), ws_bytes);
+    const ByteRange norm_at{norm, sizeof(float)}, ws_at{ws, nf4_grad_workspace()};
+    if (norm_at.meets(ws_at) || list->meets(norm, norm_at.bytes) || list->meets(ws, ws_at.bytes))
+        return fail(NF4_E_ARG, "%s: norm or the workspace overlaps another argument, a tensor of the list or its table", fn);
     hipStream_t s = static_cast<hipStream_t>(stream);
     double* shares = static_cast<double*>(ws);
     const int wgs = std::min(list->n, kMaxShares);

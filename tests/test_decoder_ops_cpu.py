@@ -167,3 +167,19 @@ def test_empty_grad_list_and_call_validation(L):
     _err(L, raw.nf4_grad_norm(h, FAKE, C.c_void_p(0x10010), ws, None), L.NF4_E_ARG, "256-byte")
     assert raw.nf4_grad_list_destroy(h) == 0
     _err(L, raw.nf4_grad_list_destroy(None), L.NF4_E_ARG, "NULL list")
+
+
+def test_grad_norm_within_its_workspace_is_refused(L):
+    rc, h = _list(L, [(None, None, 0, L.NF4_DTYPE_F32)])
+    raw, ws = L.raw(), L.raw().nf4_grad_workspace()
+    for call in (raw.nf4_grad_norm, lambda h, *a: raw.nf4_grad_clip(h, 1.0, *a)):
+        for at in (0, 8, ws - 4):
+            _err(L, call(h, C.c_void_p(FAKE.value + at), FAKE, ws, None), L.NF4_E_ARG, "overlaps")
+    assert raw.nf4_grad_list_destroy(h) == 0
+
+
+def test_grad_table_over_a_tensor_is_refused(L):
+    at = 0x20000
+    for grad, out in ((at, at), (at + 0x8000, at), (at, at + 0x8000)):
+        rc, _ = _list(L, [(grad, out, 64, L.NF4_DTYPE_F32)], table=C.c_void_p(at))
+        _err(L, rc, L.NF4_E_ARG, "table overlaps")

@@ -252,3 +252,29 @@ def test_unscaled_tensors_in_place_are_left_alone_beside_others(gpu_lib):
         torch.cuda.synchronize()
         assert math.isnan(n.item()) == bad
         assert torch.equal(a.view(torch.int32), bits) and torch.equal(out, b)
+
+
+def test_norms_and_workspaces_over_the_lists_memory_are_refused(gpu_lib):
+    """The tensors, wherever they lie in the order of addresses, their outputs and the table."""
+    lib = gpu_lib
+    flat = torch.ones(40_000, device="cuda")
+    grads = [flat[4 * i:4 * i + 2] for i in range(1000)] + [flat[8000:8001], flat[20_000:30_000]]
+    outs = grads[:1001] + [torch.zeros(10_000, device="cuda")]
+    gl = lib.GradList(grads, outs)
+    free_norm, free_ws = torch.empty(1, device="cuda"), lib.workspace(gl._ws_bytes)
+    refused = [flat[0:1], flat[1:2], flat[2000:2001], flat[3997:3998], flat[8000:8001], flat[20_000:20_001],
+               flat[29_999:30_000], outs[1001][:1], outs[1001][9999:], gl._table[:4].view(torch.float32),
+               free_ws[:4].view(torch.float32)]
+    for norm in refused:
+        with pytest.raises(lib.Nf4Error, match="overlaps"):
+            gl.norm(norm=norm, ws=free_ws)
+        with pytest.raises(lib.Nf4Error, match="overlaps"):
+            gl.clip(1.0, norm=norm, ws=free_ws)
+    n = gl._ws_bytes // 4
+    for first in (0, 8000 - n + 64, 19_968, 29_952):           # 256-byte aligned, over tensors before, behind or within
+        with pytest.raises(lib.Nf4Error, match="overlaps"):
+            gl.norm(norm=free_norm, ws=flat[first:first + n])
+    want = math.sqrt(2000 + 1 + 10_000)
+    for norm in (flat[2:3], flat[3998:3999], flat[8001:8002], flat[19_999:20_000], flat[30_000:30_001]):  # between them
+        assert gl.norm(norm=norm, ws=flat[32_000:32_000 + n]).item() == pytest.approx(want, rel=1e-6)
+    assert torch.all(flat[:2] == 1) and torch.all(flat[20_000:29_999] == 1)
