@@ -320,8 +320,8 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
  *               time (two streams, two graphs) need one each.
  * P and dS are rounded to bf16 for their products (dS to the sum of two bf16 values in calls
  * of at most 64 rows, and for the dq of heads 32 wide); dq and dk of a sequence of one row are
- * exactly zero. Other arguments, limits and errors as
- * nf4_attn_fwd.
+ * exactly zero. Other arguments, limits and errors as nf4_attn_fwd, but for the launch:
+ * sizes up to (T/64 + n_seqs) * (hq + hkv) = 2^22 fit.
  */
 int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
                  const uint16_t* dO, int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, const int32_t* cu_seqlens,

@@ -1040,7 +1040,7 @@ AttnBwdPlan plan_bwd_attn(int64_t T, int64_t hq, int64_t hkv, int64_t D, int64_t
     return p;
 }
 
-// Workgroups of a launch, refused where its threads would pass the 32 bits of a grid.
+// Whether a launch's threads pass the 32 bits of a grid: refused.
 int check_grid(const char* fn, int64_t wgs, int threads) {
     if (wgs * threads > 0xFFFFFFFFll) return fail(NF4_E_SHAPE, "%s: too many tiles (%lld workgroups)", fn, (long long)wgs);
     return NF4_OK;
@@ -1068,29 +1068,46 @@ int run_fwd(const AttnArgs& in, hipStream_t stream) {
     return check_launch("nf4_attn_fwd");
 }
 
+struct BwdGrids {
+    bool few, one;         // dq with dk and dv in one launch, of k_attn_bwd_few or _both
+    int q_tiles, kv_tiles;
+    int64_t q, kv, join;   // workgroups
+};
+
+BwdGrids bwd_grids(int64_t T, int64_t hq, int64_t hkv, int64_t D, const void* cu, int64_t n_seqs, int splits) {
+    BwdGrids g{};
+    g.few = few_tokens(T, n_seqs, hq, hkv), g.one = g.few || one_launch(T, hq);
+    g.q_tiles = int(tiles_of(T, cu, n_seqs, 128));
+    g.kv_tiles = g.few ? int(tiles_of(T, cu, n_seqs, 32)) : g.q_tiles;
+    g.q = attn_grid(int(hkv), int64_t(g.q_tiles) * (hq / hkv));
+    g.kv = attn_grid(int(hkv), int64_t(g.kv_tiles) * splits);
+    g.join = splits > 1 ? int64_t(g.kv_tiles) * hkv * (kKeyWaves * D / 16) : 0;
+    return g;
+}
+
+int check_bwd_grids(const char* fn, const BwdGrids& g, int64_t D) {
+    int st = g.one ? check_grid(fn, g.q + g.kv, 512) : check_grid(fn, g.q, D == 64 ? 256 * kRowWaves<64> : 256);
+    if (st == NF4_OK && !g.one) st = check_grid(fn, g.kv, 512);
+    return st == NF4_OK ? check_grid(fn, g.join, 256) : st;
+}
+
 template <int D>
-int run_bwd(const AttnArgs& in, hipStream_t stream) {
+int run_bwd(const AttnArgs& in, const BwdGrids& g, hipStream_t stream) {
     AttnArgs a = in;
-    const bool few = few_tokens(a.T, a.n_seqs, a.hq, a.hkv);
-    a.q_tiles = int(tiles_of(a.T, a.cu, a.n_seqs, 128));
-    a.tiles = few ? int(tiles_of(a.T, a.cu, a.n_seqs, 32)) : a.q_tiles;
-    const int64_t wgs = attn_grid(a.hkv, int64_t(a.q_tiles) * (a.hq / a.hkv));
-    const int64_t wgs_kv = attn_grid(a.hkv, int64_t(a.tiles) * a.splits);
-    const int64_t wgs_join = a.splits > 1 ? int64_t(a.tiles) * a.hkv * (kKeyWaves * D / 16) : 0;
-    if (int st = check_grid("nf4_attn_bwd", std::max(wgs + wgs_kv, wgs_join), 512); st != NF4_OK) return st;
-    if (few) {
-        hipLaunchKernelGGL(k_attn_bwd_few<D>, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
-    } else if (one_launch(a.T, a.hq)) {
+    a.q_tiles = g.q_tiles, a.tiles = g.kv_tiles;
+    if (g.few) {
+        hipLaunchKernelGGL(k_attn_bwd_few<D>, dim3(unsigned(g.q + g.kv)), dim3(512), 0, stream, a, unsigned(g.q));
+    } else if (g.one) {
         hipLaunchKernelGGL(k_attn_bwd_stats<D>, dim3(unsigned(cdiv(int64_t(a.T) * a.hq * (D / 8), 256))), dim3(256), 0,
                            stream, a);
         const auto both = fine_ds(a.T) ? k_attn_bwd_both<D, true> : k_attn_bwd_both<D, false>;
-        hipLaunchKernelGGL(both, dim3(unsigned(wgs + wgs_kv)), dim3(512), 0, stream, a, unsigned(wgs));
+        hipLaunchKernelGGL(both, dim3(unsigned(g.q + g.kv)), dim3(512), 0, stream, a, unsigned(g.q));
     } else {
-        hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, kRowWaves<D>>), dim3(unsigned(wgs)), dim3(256 * kRowWaves<D>), 0, stream, a);
-        hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(wgs_kv)), dim3(512), 0, stream, a);
+        hipLaunchKernelGGL((k_attn_bwd_dq<D, 4, kRowWaves<D>>), dim3(unsigned(g.q)), dim3(256 * kRowWaves<D>), 0, stream, a);
+        hipLaunchKernelGGL(k_attn_bwd_dkv<D>, dim3(unsigned(g.kv)), dim3(512), 0, stream, a);
     }
     if (a.splits > 1)
-        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(wgs_join)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(k_attn_bwd_join<D>, dim3(unsigned(g.join)), dim3(256), 0, stream, a);
     return check_launch("nf4_attn_bwd");
 }
 
@@ -1143,6 +1160,8 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
         !aligned16(dk) || !aligned16(dv) || !lse || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
         return fail(NF4_E_ARG, "%s: tensors must be non-NULL and 16-byte aligned, lse 4-byte aligned", fn);
     const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, causal);
+    const BwdGrids grids = bwd_grids(T, hq, hkv, head_dim, cu_seqlens, n_seqs, p.splits);
+    if (st = check_bwd_grids(fn, grids, head_dim); st != NF4_OK) return st;
     if (!ws || reinterpret_cast<uintptr_t>(ws) % 256 != 0 || ws_bytes < p.stats_bytes + p.part_bytes)
         return fail(NF4_E_ARG, "%s: workspace must be 256-byte aligned and at least %zu bytes (got %zu)", fn,
                     p.stats_bytes + p.part_bytes, ws_bytes);
@@ -1159,7 +1178,7 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
     a.stats = static_cast<float*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.stats_bytes);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    return head_dim == 128 ? run_bwd<128>(a, s) : head_dim == 64 ? run_bwd<64>(a, s) : run_bwd<32>(a, s);
+    return head_dim == 128 ? run_bwd<128>(a, grids, s) : head_dim == 64 ? run_bwd<64>(a, grids, s) : run_bwd<32>(a, grids, s);
 }
 
 }  // extern "C"

@@ -183,3 +183,22 @@ def test_grad_table_over_a_tensor_is_refused(L):
     for grad, out in ((at, at), (at + 0x8000, at), (at, at + 0x8000)):
         rc, _ = _list(L, [(grad, out, 64, L.NF4_DTYPE_F32)], table=C.c_void_p(at))
         _err(L, rc, L.NF4_E_ARG, "table overlaps")
+
+
+@pytest.mark.parametrize("T,n,hq,hkv,D,fits", [
+    (40, 1 << 13, 256, 256, 64, True),             # (T/64 + n) (hq + hkv) = 2^22, both kinds in one launch
+    (40, 1 << 14, 256, 256, 64, False),            # 2^23 and as many threads as pass 32 bits
+    (40, (1 << 14) - 32, 256, 256, 64, True),
+    (1 << 14, 1 << 14, 256, 256, 64, True),        # launches of their own, 2^22 and more workgroups each
+    (1 << 14, 1 << 14, 256, 256, 128, True),
+    (1 << 14, 1 << 14, 512, 512, 64, False),
+    (1 << 14, (1 << 14) - 192, 512, 512, 64, True),
+    (1 << 23, 0, 64, 64, 128, True),
+])
+def test_backward_grids_are_checked_launch_by_launch(L, T, n, hq, hkv, D, fits):
+    """Without a workspace: sizes whose launches fit are refused for that, others for their workgroups
+    (nothing is launched either way)."""
+    at = [C.c_void_p((1 << 44) * (i + 1)) for i in range(10)]
+    rc = L.raw().nf4_attn_bwd(at[0], at[1], at[2], at[3], at[4], at[5], T, hq, hkv, D, at[9] if n else None, n, 1, 0.125,
+                              at[6], at[7], at[8], None, 0, None)
+    _err(L, rc, *((L.NF4_E_ARG, "workspace") if fits else (L.NF4_E_SHAPE, "workgroups")))
