@@ -293,7 +293,9 @@ int nf4_rope(const uint16_t* q, const uint16_t* k, int64_t T, int64_t hq, int64_
  * The probabilities are rounded to bf16 for their product with v. A value of k or v that is
  * not finite makes rows of its own sequence not finite (also rows that a causal mask hides
  * it from), never rows of another. head_dim 32, 64 or 128; hkv | hq <= 1024; T <= 2^23;
- * n_seqs <= 2^20; T == 0 is a no-op. Sizes up to (T/64 + n_seqs) * hq = 2^22 fit one launch; those
+ * n_seqs <= 2^16 (each workgroup scans the bounds for its rows, which grows with the square of
+ * n_seqs: 256 sequences of one token of 28/4 heads of 64 take 55 us, 4096 take 3.8 ms); T == 0 is a
+ * no-op. Sizes up to (T/64 + n_seqs) * hq = 2^22 fit one launch; those
  * that do not are refused (NF4_E_SHAPE). q, k, v, o 16-byte aligned; an o or lse that overlaps
  * another argument is refused (NF4_E_ARG).
  */

@@ -33,6 +33,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeyWaves = 4;  // blocks of 32 keys of a dk/dv workgroup
+constexpr int64_t kMaxSeqs = int64_t(1) << 16;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
@@ -57,7 +58,10 @@ struct Tile {
 // Tile number g of the sequences' tiles of BM rows, numbered sequence after sequence: one
 // wave scans 64 sequences at a time. The bounds read from the device are clamped to
 // [0, T] and to non-negative lengths, so that no value of theirs leads outside the
-// tensors. False when there are fewer tiles.
+// tensors. False when there are fewer tiles. Every workgroup scans for itself, so that the scans
+// grow with the square of the sequences: sequences of one token, forward and backward, us: 256 of 28/4
+// heads of 64 55, 191; 1024 222, 961; 4096 3835, 8844; 16384 52 ms, 122 ms; 32768 of 4/1 29 ms, 74 ms.
+// kMaxSeqs keeps the largest calls that a grid holds to seconds.
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int bm, int g, Tile& t) {
     if (!a.cu) {
         t = {0, a.T, g * bm};
@@ -1007,8 +1011,8 @@ int check_attn(const char* fn, int64_t T, int64_t hq, int64_t hkv, int64_t D, co
     if (T < 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024)
         return fail(NF4_E_SHAPE, "%s: need 0 <= T <= 2^23 and hkv | hq <= 1024 (got T=%lld hq=%lld hkv=%lld)", fn,
                     (long long)T, (long long)hq, (long long)hkv);
-    if (cu ? (n_seqs < 1 || n_seqs > (int64_t(1) << 20)) : (n_seqs != 0 && n_seqs != 1))
-        return fail(NF4_E_SHAPE, "%s: need 1 <= n_seqs <= 2^20 with cu_seqlens, 0 or 1 without (got %lld)", fn,
+    if (cu ? (n_seqs < 1 || n_seqs > kMaxSeqs) : (n_seqs != 0 && n_seqs != 1))
+        return fail(NF4_E_SHAPE, "%s: need 1 <= n_seqs <= 2^16 with cu_seqlens, 0 or 1 without (got %lld)", fn,
                     (long long)n_seqs);
     if (causal != 0 && causal != 1) return fail(NF4_E_ARG, "%s: causal must be 0 or 1 (got %d)", fn, causal);
     if (!std::isfinite(scale) || scale <= 0.0f)

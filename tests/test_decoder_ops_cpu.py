@@ -202,3 +202,9 @@ def test_backward_grids_are_checked_launch_by_launch(L, T, n, hq, hkv, D, fits):
     rc = L.raw().nf4_attn_bwd(at[0], at[1], at[2], at[3], at[4], at[5], T, hq, hkv, D, at[9] if n else None, n, 1, 0.125,
                               at[6], at[7], at[8], None, 0, None)
     _err(L, rc, *((L.NF4_E_ARG, "workspace") if fits else (L.NF4_E_SHAPE, "workgroups")))
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+def test_more_sequences_than_the_scan_serves_are_refused(L, call):
+    _err(L, call(L, T=1 << 16, cu=FAKE, n=(1 << 16) + 1), L.NF4_E_SHAPE, "n_seqs <= 2^16")
+    _err(L, call(L, q=None, cu=FAKE, n=1 << 16), L.NF4_E_ARG, "NULL")   # as many pass this check
