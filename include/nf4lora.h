@@ -303,7 +303,8 @@ int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_
                  int64_t head_dim, const int32_t* cu_seqlens, int64_t n_seqs, int causal, float scale, uint16_t* o,
                  float* lse, nf4_stream stream);
 
-/* Bytes of device workspace nf4_attn_bwd needs for these sizes (n_seqs 0 or 1: no cu_seqlens). */
+/* Bytes of device workspace nf4_attn_bwd needs for these sizes (n_seqs 0 or 1: no cu_seqlens); 0 for head
+ * counts and widths, rows and sequences that it refuses, and for T == 0. */
 size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, int64_t n_seqs);
 
 /*

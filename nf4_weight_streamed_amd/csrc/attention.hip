@@ -1146,7 +1146,7 @@ int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_
 
 size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, int64_t n_seqs) {
     if (T <= 0 || T > (int64_t(1) << 23) || hkv <= 0 || hq <= 0 || hq % hkv != 0 || hq > 1024 || n_seqs < 0 ||
-        (head_dim != 32 && head_dim != 64 && head_dim != 128))
+        n_seqs > kMaxSeqs || (head_dim != 32 && head_dim != 64 && head_dim != 128))
         return 0;
     const AttnBwdPlan p = plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 1);  // enough with and without a mask
     return p.stats_bytes + std::max(p.part_bytes, plan_bwd_attn(T, hq, hkv, head_dim, n_seqs, 0).part_bytes);

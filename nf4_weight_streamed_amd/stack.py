@@ -39,6 +39,7 @@ a = attention(rope(q), rope(k), v), causal within each of the batch's packed seq
 from __future__ import annotations
 
 import contextlib
+import operator
 import time
 from dataclasses import dataclass
 
@@ -268,8 +269,17 @@ class NF4Stack:
             raise ValueError("mixing must be 'identity' or 'attention'")
         if seq_lens is not None and mixing == "identity":
             raise ValueError("seq_lens needs mixing='attention'")
-        if seq_lens is not None and (sum(seq_lens) != tokens or not seq_lens or min(seq_lens) < 0):
-            raise ValueError(f"seq_lens must be non-negative and add up to {tokens} tokens")
+        if seq_lens is not None:
+            seq_lens = [operator.index(n) for n in seq_lens]
+            if sum(seq_lens) != tokens or not seq_lens or min(seq_lens) < 0:
+                raise ValueError(f"seq_lens must be non-negative and add up to {tokens} tokens")
+        if mixing == "attention":
+            q, kv, hd, n = base.dims.q, base.dims.kv, base.dims.head_dim, len(seq_lens or ())
+            if hd not in (32, 64, 128) or q % hd or kv % hd or (
+                    tokens and not lib.attn_bwd_workspace_bytes(tokens, q // hd, kv // hd, hd, n)):
+                raise ValueError("mixing='attention' needs heads 32, 64 or 128 wide, kv heads that divide at most 1024 "
+                                 f"query heads, and the attention's limits on tokens and sequences (got q={q}, kv={kv}, "
+                                 f"head_dim={hd}, {tokens} tokens, {n} sequences)")
         self.mixing = mixing
         self.base, self.lora, self.T, self.alpha = base, lora, tokens, alpha
         self.mode, self.prefetch, self.remat = mode, prefetch, remat
@@ -343,7 +353,7 @@ class NF4Stack:
         }
         self.seqs = {"cu": None, "n": 0}
         if mixing == "attention":
-            lens = [T] if seq_lens is None else [int(n) for n in seq_lens]
+            lens = [T] if seq_lens is None else seq_lens
             self.inv_freq = lib.rope_inv_freq(d.head_dim, rope_theta)
             self.pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in lens]).to(dev)   # restart in each sequence
             if seq_lens is not None:

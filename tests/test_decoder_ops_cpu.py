@@ -2,6 +2,7 @@
 fails (or is a no-op) before anything reaches the device."""
 
 import ctypes as C
+from types import SimpleNamespace
 
 import pytest
 
@@ -208,3 +209,32 @@ def test_backward_grids_are_checked_launch_by_launch(L, T, n, hq, hkv, D, fits):
 def test_more_sequences_than_the_scan_serves_are_refused(L, call):
     _err(L, call(L, T=1 << 16, cu=FAKE, n=(1 << 16) + 1), L.NF4_E_SHAPE, "n_seqs <= 2^16")
     _err(L, call(L, q=None, cu=FAKE, n=1 << 16), L.NF4_E_ARG, "NULL")   # as many pass this check
+
+
+@pytest.mark.parametrize("dims,tokens,lens", [
+    (dict(q=96, kv=48, head_dim=48), 8, None),             # a head width without a kernel
+    (dict(q=128, kv=64, head_dim=0), 8, None),
+    (dict(q=100, kv=32, head_dim=32), 8, None),            # not whole heads
+    (dict(q=128, kv=40, head_dim=32), 8, None),
+    (dict(q=160, kv=64, head_dim=32), 8, None),            # 5 query heads over 2
+    (dict(q=2048 * 32, kv=32, head_dim=32), 8, None),
+    (dict(q=128, kv=32, head_dim=32), (1 << 23) + 1, None),
+    (dict(q=128, kv=32, head_dim=32), 1 << 17, [2] * (1 << 16) + [0]),
+])
+def test_stack_refuses_sizes_that_its_attention_does(L, dims, tokens, lens):
+    """Before anything is allocated or copied: the base here holds nothing but its sizes."""
+    from nf4_weight_streamed_amd import stack
+
+    base = SimpleNamespace(dims=stack.StackDims(hidden=128, inter=256, **dims))
+    with pytest.raises(ValueError, match="mixing='attention' needs"):
+        stack.NF4Stack(base, None, tokens, mixing="attention", seq_lens=lens)
+
+
+def test_stack_refuses_sequence_lengths_that_are_not_whole(L):
+    from nf4_weight_streamed_amd import stack
+
+    base = SimpleNamespace(dims=stack.StackDims(hidden=128, q=128, kv=32, inter=256, head_dim=32))
+    with pytest.raises(TypeError):
+        stack.NF4Stack(base, None, 8, mixing="attention", seq_lens=[4.5, 3.5])
+    with pytest.raises(ValueError, match="add up"):
+        stack.NF4Stack(base, None, 8, mixing="attention", seq_lens=iter([4, 5]))
