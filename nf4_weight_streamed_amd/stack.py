@@ -341,15 +341,13 @@ class NF4Stack:
                           "lse": torch.empty(d.q // d.head_dim, T, dtype=torch.float32, device=dev)})
         # scratch reused by every layer (stream order makes reuse safe)
         self.tmp = {
-            "q": torch.empty(T, d.q, **bf), "k": torch.empty(T, d.kv, **bf), "o": torch.empty(T, d.hidden, **bf),
-            "down": torch.empty(T, d.hidden, **bf),
+            "o": torch.empty(T, d.hidden, **bf), "down": torch.empty(T, d.hidden, **bf),
             "dm": torch.empty(T, d.inter, **bf), "dgate": torch.empty(T, d.inter, **bf),
             "dup": torch.empty(T, d.inter, **bf), "dhm_g": torch.empty(T, d.hidden, **bf),
             "dhm_u": torch.empty(T, d.hidden, **bf), "dhm": torch.empty(T, d.hidden, **bf),
             "dh1": torch.empty(T, d.hidden, **bf), "da": torch.empty(T, d.q, **bf), "dv": torch.empty(T, d.kv, **bf),
             "dha_v": torch.empty(T, d.hidden, **bf), "dha_q": torch.empty(T, d.hidden, **bf),
             "dha_k": torch.empty(T, d.hidden, **bf), "dha": torch.empty(T, d.hidden, **bf),
-            "zq": torch.zeros(T, d.q, **bf), "zkv": torch.zeros(T, d.kv, **bf),
         }
         self.seqs = {"cu": None, "n": 0}
         if mixing == "attention":
@@ -362,6 +360,9 @@ class NF4Stack:
             self.ws_a = lib.workspace(lib.attn_bwd_workspace_bytes(T, d.q // d.head_dim, d.kv // d.head_dim, d.head_dim,
                                                                    self.seqs["n"]))
             self.tmp.update({"dq": torch.empty(T, d.q, **bf), "dk": torch.empty(T, d.kv, **bf)})
+        else:                            # q and k that nothing reads, and their zero gradients
+            self.tmp.update({"q": torch.empty(T, d.q, **bf), "k": torch.empty(T, d.kv, **bf),
+                             "zq": torch.zeros(T, d.q, **bf), "zkv": torch.zeros(T, d.kv, **bf)})
         self._grad_list = None
         self.dh = [torch.empty(T, d.hidden, **bf) for _ in range(2)]
         self.grads = [{name: (torch.empty(r, shapes[name][1], dtype=torch.float32, device=dev),

@@ -127,3 +127,20 @@ def test_refusals(ST):
     for lens in ([4, 3], [9, -1], []):
         with pytest.raises(ValueError, match="seq_lens"):
             ST.NF4Stack(base, lora, 8, mixing="attention", seq_lens=lens)
+
+
+def test_every_scratch_buffer_is_used(ST):
+    """The scratch that a stack holds beside its activations is what a step writes: no buffer keeps the
+    pattern it was filled with before one, but for the identity mixing's zero gradients."""
+    dims = ST.StackDims(**TINY)
+    _, _, base, lora = _stack(ST, 1, 1, dims)
+    h0, dh = (to_dev_bf16(S.activations(8, dims.hidden, tensor=n)) for n in ("h0", "dH"))
+    for mixing in ("identity", "attention"):
+        st = ST.NF4Stack(base, lora, 8, 32.0, mixing=mixing)
+        scratch = {n: t for n, t in st.tmp.items() if mixing == "attention" or n not in ("zq", "zkv")}
+        for t in scratch.values():
+            t.view(torch.int16).fill_(0x7FA5)                  # a NaN that no step computes
+        st.step(h0, dh)
+        torch.cuda.synchronize()
+        assert [n for n, t in scratch.items() if bool((t.view(torch.int16) == 0x7FA5).any())] == []
+        st.close()
