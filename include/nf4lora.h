@@ -295,9 +295,9 @@ int nf4_rope(const uint16_t* q, const uint16_t* k, int64_t T, int64_t hq, int64_
  * it from), never rows of another. head_dim 32, 64 or 128; hkv | hq <= 1024; T <= 2^23;
  * n_seqs <= 2^16 (each workgroup scans the bounds for its rows, which grows with the square of
  * n_seqs: 256 sequences of one token of 28/4 heads of 64 take 55 us, 4096 take 3.8 ms); T == 0 is a
- * no-op. Sizes up to (T/64 + n_seqs) * hq = 2^22 fit one launch; those
- * that do not are refused (NF4_E_SHAPE). q, k, v, o 16-byte aligned; an o or lse that overlaps
- * another argument is refused (NF4_E_ARG).
+ * no-op. Sizes up to (T/64 + n_seqs) * hq = 2^22 fit one launch; those that do not are refused
+ * (NF4_E_SHAPE). q, k, v, o 16-byte aligned; an o or lse that overlaps another argument is
+ * refused (NF4_E_ARG).
  */
 int nf4_attn_fwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, int64_t T, int64_t hq, int64_t hkv,
                  int64_t head_dim, const int32_t* cu_seqlens, int64_t n_seqs, int causal, float scale, uint16_t* o,
@@ -322,9 +322,12 @@ size_t nf4_attn_bwd_workspace(int64_t T, int64_t hq, int64_t hkv, int64_t head_d
  *               aligned; its contents on entry are ignored. Calls that may run at the same
  *               time (two streams, two graphs) need one each.
  * P and dS are rounded to bf16 for their products (dS to the sum of two bf16 values in calls
- * of at most 64 rows, and for the dq of heads 32 wide); dq and dk of a sequence of one row are
- * exactly zero. Other arguments, limits and errors as nf4_attn_fwd, but for the launch:
- * sizes up to (T/64 + n_seqs) * (hq + hkv) = 2^22 fit.
+ * of at most 64 rows in all, and for the dq of heads 32 wide), and the order of a sum follows the
+ * call's sizes: what a sequence is packed with can change the last bits of its gradients. dq and
+ * dk of a sequence of one row are exactly zero. S and lse are fp32, so that P is off by about
+ * 2^-22 |lse| of itself; scores past 2^28 may give results that are not finite. Other
+ * arguments, limits and errors as nf4_attn_fwd, but for the launch: sizes up to
+ * (T/64 + n_seqs) * (hq + hkv) = 2^22 fit.
  */
 int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* o, const float* lse,
                  const uint16_t* dO, int64_t T, int64_t hq, int64_t hkv, int64_t head_dim, const int32_t* cu_seqlens,

@@ -8,9 +8,12 @@
 // (dk, dv also summed over the G query heads of a kv head). Scores are never stored: the
 // backward recomputes P from lse. Everything is fp32 except the operands of the second
 // products, which are P and dS rounded to bf16 for the bf16 MFMA: a relative error of at
-// most 2^-8 per term, which leaves the results about 1.4 times as far from exact as their own
-// rounding does. Where few terms carry a sum that is not enough (1.5 to 1.6 times): dS is then
-// the sum of two bf16 values, each multiplied (FINE below).
+// most 2^-8 per term, which leaves the results 1.40 to 1.45 times as far from exact (2-norm) as
+// their own rounding does, at every length (evaluated in fp64 on the CPU, 2 to 512 rows of one
+// head, q twice as long as k). In a short call, whose few errors do not average, a single result
+// scatters far above that: 2 rows up to 3.6 times, 16 up to 2.1, 64 up to 1.65, 512 up to 1.5. dS
+// is then the sum of two bf16 values, each multiplied (FINE below). What counts for that is a
+// call's rows, not its sequences', so the same sequence rounds otherwise in a longer call.
 //
 // MFMA layout used throughout (32x32x16): an accumulator lane l holds column l % 32 and
 // rows 8 (e / 4) + 4 (l / 32) + e % 4; an operand lane holds one row (or column) and 8
@@ -309,7 +312,7 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
     if (!pick_item(one_round ? snake(blockIdx.x, gridDim.x) : blockIdx.x, a.hkv, a.tiles * G, kvh, item)) return;
     const int head = kvh * G + item % G;
     Tile t;
-    if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;  // longest rows first
+    if (!find_tile(a, BM, a.tiles - 1 - item / G, t)) return;  // a sequence's longest rows first
     const int lane = threadIdx.x & 63, wave = uni(threadIdx.x >> 6), h = lane >> 5;
     const int wr = wave % R, wc = C == 1 ? 0 : wave / R, b0 = B * wc;  // row, place in it, first key block
     const int ldq = a.hq * D, ldk = a.hkv * D;
@@ -439,9 +442,9 @@ __global__ __launch_bounds__(64 * R * C, 2) void k_attn_fwd(AttnArgs a) {
 
 // As the forward, with dO beside Q in registers: per 64-key tile S^T = K Q^T,
 // dP^T = V dO^T, dS^T in place, dq^T += K^T dS^T. delta is formed here first (the dk/dv
-// kernel behind this one reads it). R, C and B as in the forward. FINE: for heads 32 wide, whose
-// scores spread further with the length of q than those of wider heads and leave a row to its
-// largest few, and for calls of at most 64 tokens. Measured (us, one bf16 value for dS and two):
+// kernel behind this one reads it). R, C and B as in the forward. FINE: for calls of at
+// most 64 rows, and for heads 32 wide, whose rounding grows with the length instead (dq 1.49 times
+// its own at 512 rows, 64 and 128 wide 1.44). Measured (us, one bf16 value for dS and two):
 // 4096 tokens of 4/1 heads of 32 48.1, 59.0; 64 tokens of 64/8 heads of 128 15.4, 15.6.
 // Bound as the forward: 8192 tokens of 64/8 heads of 128 1364 us, 1.21 PFLOP/s with its share
 // (S, dP and dq: 6 D operations a pair).
@@ -946,7 +949,8 @@ int64_t tiles_of(int64_t T, const void* cu, int64_t n_seqs, int bm) {
 // 2048 tokens of 40/8: 55.4, 64.3; 4096 tokens of 14/2 heads of 64: 57.4, 46.7.
 bool few_rows(int64_t T, int64_t hq, int64_t D) { return cdiv(T, 128) * hq < 256 * (D == 128 ? 2 : D == 64 ? 3 : 4); }
 
-// Calls whose dk has dS as two bf16 values (dq: those, and all heads 32 wide).
+// Calls whose dk has dS as two bf16 values (dq: those, and all heads 32 wide). By all rows of the
+// call, since the scatter of few results is what it bounds.
 bool fine_ds(int64_t T) { return T <= 64; }
 
 // Those of them whose dk and dv take a kv head's queries side by side (bwd_dkv_few) instead of
