@@ -343,7 +343,8 @@ int nf4_attn_bwd(const uint16_t* q, const uint16_t* k, const uint16_t* v, const 
  * description (nf4_grad_list_table() bytes, 256-byte aligned), must outlive its calls, those
  * of captured graphs among them.
  * nf4_grad_list_create copies the description there on `stream` and waits for the copy
- * (NF4_E_STATE while the stream is being captured).
+ * (NF4_E_STATE while the stream is being captured): about 60 us for 14 tensors, 1.5 ms for 1120
+ * with the binding's walk over them.
  *   tensors  HOST array of n descriptions (read during the call only); dtype bf16 or fp32,
  *            mixed freely; pointers aligned to their elements; count 0 allowed (pointers
  *            then ignored); out == grad scales in place
@@ -375,7 +376,8 @@ int nf4_grad_norm(const nf4_grad_list* list, float* norm, void* ws, size_t ws_by
 /* *norm = n (before clipping) and every out written; a tensor in place is left alone when
  * nothing has to be scaled. max_norm finite, >= 0. When a gradient is not finite,
  * neither is *norm, and the gradients are passed on unscaled: the caller sees it and skips
- * its step. */
+ * its step. A norm of finite gradients past fp32's range is infinite in *norm, and they are
+ * scaled by it all the same. */
 int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* ws, size_t ws_bytes,
                   nf4_stream stream);
 

@@ -4,7 +4,8 @@
 // where it is in place and nothing has to be scaled). The scaling goes from the last element
 // to the first, so that it finds in the last-level cache what the norm read last; in lists
 // larger than that cache the rest is read and the outputs are written past it: 842 MB of fp32
-// (1120 tensors) 497 -> 422 us, 6.0 TB/s of the three passes' bytes (norm 123 us, 6.8 TB/s).
+// (1120 tensors) 497 -> 422 us, 6.0 TB/s of the three passes' bytes (norm 123 us, 6.8 TB/s); in
+// place 428 us; of bf16 (421 MB) 210 us.
 // Squares and their sums are fp64, at the full rate of the vector ALUs beside these loads: no
 // overflow or underflow for any fp32 gradient, and sums over 10^9 elements stay exact far below
 // the fp32 result's rounding. No atomics: every workgroup leaves one fp64 share, and every

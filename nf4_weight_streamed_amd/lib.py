@@ -609,7 +609,7 @@ def attn_bwd_workspace_bytes(T: int, hq: int, hkv: int, head_dim: int, n_seqs: i
 
 def attn_fwd(q, k, v, head_dim: int, cu_seqlens=None, causal: bool = True, scale=None, o=None, lse=None, stream=None):
     """Softmax attention of q [T, hq * head_dim] over k, v [T, hkv * head_dim] (bf16), within the
-    sequences cu_seqlens (int32 [n + 1]; None: one sequence). Returns (o like q, lse fp32 [hq, T]);
+    sequences cu_seqlens (int32 [n + 1], n <= 65536; None: one sequence). Returns (o like q, lse fp32 [hq, T]);
     rows outside every sequence are not written."""
     (t, hq, hkv, n_seqs, scale), q_shape, _ = _attn_args(q, k, v, head_dim, cu_seqlens, scale)
     o = _empty(q_shape, torch.bfloat16, q.device, stream) if o is None else o
@@ -648,7 +648,8 @@ class GradList:
     """A training program's gradient tensors (bf16 or fp32, mixed freely) as one list for the
     global norm and clipping (nf4_grad_list_*): made once over the buffers, used every step.
     outs: where the scaled gradients go (default: in place). The tensors are kept alive with
-    this object, which has to outlive every graph that captured a call of it."""
+    this object, which has to outlive every graph that captured a call of it. Making one takes
+    about 1.3 us a tensor and a copy that it waits for (1120 tensors 1.5 ms)."""
 
     def __init__(self, grads, outs=None, stream=None):
         self._h = None
