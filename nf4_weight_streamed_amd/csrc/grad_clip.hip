@@ -104,6 +104,7 @@ __global__ __launch_bounds__(kThreads) void k_grad_norm(const Chunk* __restrict_
 }
 
 // The factor stays fp64: as fp32 it would lose bits below 2^-126, which bounds far below the norm reach.
+// bf16 is rounded by way of fp32.
 __device__ __forceinline__ float scaled(float v, double f) { return float(double(v) * f); }
 
 __device__ __forceinline__ u32x4 scale16(u32x4 v, double f, bool bf16) {

@@ -39,7 +39,6 @@ a = attention(rope(q), rope(k), v), causal within each of the batch's packed seq
 from __future__ import annotations
 
 import contextlib
-import operator
 import time
 from dataclasses import dataclass
 
@@ -270,9 +269,10 @@ class NF4Stack:
         if seq_lens is not None and mixing == "identity":
             raise ValueError("seq_lens needs mixing='attention'")
         if seq_lens is not None:
-            seq_lens = [operator.index(n) for n in seq_lens]
-            if sum(seq_lens) != tokens or not seq_lens or min(seq_lens) < 0:
-                raise ValueError(f"seq_lens must be non-negative and add up to {tokens} tokens")
+            given = list(seq_lens)
+            seq_lens = [int(n) for n in given]
+            if seq_lens != given or sum(seq_lens) != tokens or not seq_lens or min(seq_lens) < 0:
+                raise ValueError(f"seq_lens must be whole, non-negative and add up to {tokens} tokens")
         if mixing == "attention":
             q, kv, hd, n = base.dims.q, base.dims.kv, base.dims.head_dim, len(seq_lens or ())
             if hd not in (32, 64, 128) or q % hd or kv % hd or (

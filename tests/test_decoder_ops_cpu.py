@@ -234,7 +234,9 @@ def test_stack_refuses_sequence_lengths_that_are_not_whole(L):
     from nf4_weight_streamed_amd import stack
 
     base = SimpleNamespace(dims=stack.StackDims(hidden=128, q=128, kv=32, inter=256, head_dim=32))
-    with pytest.raises(TypeError):
+    with pytest.raises(ValueError, match="whole"):
         stack.NF4Stack(base, None, 8, mixing="attention", seq_lens=[4.5, 3.5])
+    with pytest.raises(AttributeError):                    # whole ones of any type pass: the base here has no more
+        stack.NF4Stack(base, None, 8, mixing="attention", seq_lens=[4.0, 4])
     with pytest.raises(ValueError, match="add up"):
         stack.NF4Stack(base, None, 8, mixing="attention", seq_lens=iter([4, 5]))
