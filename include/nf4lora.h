@@ -381,6 +381,117 @@ int nf4_grad_norm(const nf4_grad_list* list, float* norm, void* ws, size_t ws_by
 int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* ws, size_t ws_bytes,
                   nf4_stream stream);
 
+/* ------------------------------------------------------------------ activations in 8 bits
+ * What a training step keeps of its activations for its backward, at 1.0625 bytes an element
+ * instead of 2 ([consumer] "OOM playbook": activation memory grows with the sequence). A
+ * checkpoint of a bf16 matrix [rows][cols] (cols % 64 == 0) is
+ *   codes  device uint8 [rows][cols], 16-byte aligned
+ *   scale  device fp32 [rows][cols/64], 4-byte aligned; the step of each run of 64 elements
+ * with, for a run whose largest magnitude is a,
+ *   scale = RN32(a / 127)
+ *   code  = 128 + rne(x RN32(127 / a))        (the product exact; 1..255; a == 0: all 128)
+ *   value = RN32((code - 128) scale)
+ * so that a value is off by at most a / 254 and 2^-23 of itself. (For a < 2^-64 the code is that
+ * of 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The
+ * calls below take rows * cols <= 2^34; rows == 0 is a no-op; cols % 64 != 0 -> NF4_E_SHAPE.
+ * bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input of the call itself, any
+ * other overlap of an output is refused (NF4_E_ARG).
+ */
+
+/* codes and scale of x. */
+int nf4_act8_quantize(const uint16_t* x, int64_t rows, int64_t cols, uint8_t* codes, float* scale, nf4_stream stream);
+
+/* x = RNbf(value). */
+int nf4_act8_dequantize(const uint8_t* codes, const float* scale, int64_t rows, int64_t cols, uint16_t* x,
+                        nf4_stream stream);
+
+/* nf4_silu_mul_fwd with the checkpoints of both inputs: m = RNbf(SiLU(gate) * up), in one pass. */
+int nf4_silu_mul_fwd_act8(const uint16_t* gate, const uint16_t* up, int64_t rows, int64_t cols, uint16_t* m,
+                          uint8_t* gate_codes, float* gate_scale, uint8_t* up_codes, float* up_scale, nf4_stream stream);
+
+/* m again from the checkpoints' values: the down projection's input, rebuilt for its backward
+ * rather than kept. */
+int nf4_silu_mul_act8(const uint8_t* gate_codes, const float* gate_scale, const uint8_t* up_codes, const float* up_scale,
+                      int64_t rows, int64_t cols, uint16_t* m, nf4_stream stream);
+
+/* nf4_silu_mul_bwd at the checkpoints' values; dgate or dup may be dm itself. */
+int nf4_silu_mul_bwd_act8(const uint8_t* gate_codes, const float* gate_scale, const uint8_t* up_codes, const float* up_scale,
+                          const uint16_t* dm, int64_t rows, int64_t cols, uint16_t* dgate, uint16_t* dup,
+                          nf4_stream stream);
+
+/*
+ * nf4_lora_linear_bwd and nf4_lora_linear_bwd_bf16 with the forward's input as a checkpoint
+ * (x_codes [T][K], x_scale [T][K/64]): dA = s . g^T . RNbf(value), everything else, workspace
+ * sizes among it (nf4_lora_linear_bwd_workspace, nf4_lora_linear_bwd_bf16_workspace), as there.
+ * dX and dB are those calls', bit for bit.
+ */
+int nf4_lora_linear_bwd_act8(const uint8_t* codes, const float* absmax, int64_t N, int64_t K, const uint8_t* x_codes,
+                             const float* x_scale, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+                             const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws,
+                             size_t ws_bytes, nf4_stream stream);
+int nf4_lora_linear_bwd_bf16_act8(const uint16_t* w, int64_t N, int64_t K, const uint8_t* x_codes, const float* x_scale,
+                                  const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+                                  const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws,
+                                  size_t ws_bytes, nf4_stream stream);
+
+/*
+ * The residual stream around a block, in one pass: the block's output o joins the stream h and
+ * the stream is normalised for the next block. Per row of H elements, in fp32:
+ *     v = o                                                    (post_norm 0), or
+ *     v = o rstd_o (gain_offset + post_gain),  rstd_o = 1 / sqrt(mean o^2 + eps)   (post_norm 1)
+ *     s = h + scale * gate * v                                 (s = h when o is NULL)
+ *     h_out = RNbf(s),  rstd = 1 / sqrt(mean s^2 + eps)
+ *     n = RNbf(s rstd (gain_offset + gain))
+ *   h            device bf16 [T][H]
+ *   o            device bf16 [T][H], or NULL: the norm alone (h_out NULL too)
+ *   post_gain, gain  device bf16 [H], or NULL for a factor of 1 (gain_offset then has no part)
+ *   gate         device bf16: [H] (NF4_GATE_CHANNEL), [T][H] (NF4_GATE_TOKEN) or NULL (NF4_GATE_NONE)
+ *   h_out, n     device bf16 [T][H] (written; each may be h or o itself)
+ *   n_codes, n_scale  the 8-bit checkpoint of n as nf4_act8_quantize makes it of the rounded n
+ *                (H % 64 == 0), or NULL
+ *   rstd_o, rstd device fp32 [T] (written; rstd_o only with post_norm), for the backward
+ * 1 <= H <= 16384, T <= 2^23, T == 0 is a no-op. bf16 tensors need 2-byte alignment; rows of a
+ * multiple of 8 elements that are 16-byte aligned are faster. Other overlaps are refused.
+ */
+#define NF4_GATE_NONE 0
+#define NF4_GATE_CHANNEL 1
+#define NF4_GATE_TOKEN 2
+int nf4_residual_norm_fwd(const uint16_t* h, const uint16_t* o, int64_t T, int64_t H, int post_norm,
+                          const uint16_t* post_gain, int gate_kind, const uint16_t* gate, float scale,
+                          const uint16_t* gain, float gain_offset, float eps, uint16_t* h_out, uint16_t* n,
+                          uint8_t* n_codes, float* n_scale, float* rstd_o, float* rstd, nf4_stream stream);
+
+/* Bytes of device workspace nf4_residual_norm_bwd needs: sums != 0 when any of dgain, dpost_gain and
+ * a channel gate's dgate is asked for; 0 otherwise, for T == 0 and for sizes that it refuses. */
+size_t nf4_residual_norm_bwd_workspace(int64_t T, int64_t H, int sums);
+
+/*
+ * Backward of the same. With g = dn[0] + ... + dn[n_dn-1], b = h rstd or the checkpoint's
+ * value, w = g (gain_offset + gain), u = o rstd_o (or o without post_norm):
+ *     ds = dres + rstd (w - b mean(w b)),   dh = RNbf(ds),   dgain = sum_t g b
+ *     dv = scale ds,  dgate = dv v,  then dv <- dv gate
+ *     d_o = RNbf(dv), or with post_norm, p = dv (gain_offset + post_gain):
+ *     d_o = RNbf(rstd_o (p - u mean(p u))),  dpost_gain = sum_t dv u
+ *   dn           HOST array of 1 to 3 device bf16 [T][H]: the gradients of n, one a reader
+ *   dres         device bf16 [T][H], the gradient that reaches h_out past the norm, or NULL
+ *   h            device bf16 [T][H]: the stream that was normalised (h_out), or NULL with
+ *   n_codes, n_scale  the checkpoint of n, which stands in for it when there was no gain
+ *   o, rstd_o    the forward's (o: only for dgate, dpost_gain, and d_o with post_norm)
+ *   dh, d_o      device bf16 [T][H] (dh always written; d_o may be NULL: without post_norm, gate and
+ *                scale it equals dh). dh may be dres or one of dn, d_o may be o or one of dn
+ *   dgate        NULL, or device fp32 [H] (sum over t, NF4_GATE_CHANNEL), bf16 [T][H] (NF4_GATE_TOKEN)
+ *   dpost_gain, dgain  NULL, or device fp32 [H] (overwritten; zeros for T == 0)
+ *   ws           device workspace of at least nf4_residual_norm_bwd_workspace() bytes, 256-byte
+ *                aligned; contents on entry ignored; calls that may run at once need one each
+ * rstd_o and rstd are taken as given. Sums over t have a fixed order. Limits as in the forward.
+ */
+int nf4_residual_norm_bwd(const uint16_t* const* dn, int n_dn, const uint16_t* dres, const uint16_t* h,
+                          const uint8_t* n_codes, const float* n_scale, const float* rstd, const uint16_t* o,
+                          const float* rstd_o, int64_t T, int64_t H, int post_norm, const uint16_t* post_gain,
+                          int gate_kind, const uint16_t* gate, float scale, const uint16_t* gain, float gain_offset,
+                          uint16_t* dh, uint16_t* d_o, void* dgate, float* dpost_gain, float* dgain, void* ws,
+                          size_t ws_bytes, nf4_stream stream);
+
 /*
  * Instrumentation for measurement: the next nf4_lora_linear_fwd or
  * nf4_lora_linear_bwd call made by this host thread records `start` (a

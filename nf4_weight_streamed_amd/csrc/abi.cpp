@@ -306,16 +306,16 @@ int linear_fwd(const char* fn, const uint8_t* codes, const float* absmax, const 
 namespace {
 
 int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const uint16_t* wdense, int64_t N, int64_t K,
-               const uint16_t* x, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+               const SavedInput& x, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
                const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
                nf4_stream stream) {
     if (T == 0) return NF4_OK;
     if (!dy) return fail(NF4_E_ARG, "%s: dy must not be NULL", fn);
-    if (r > 0 && (!x || !u_save || !A || !B || !dA || !dB))
+    if (r > 0 && ((!x.x && !(x.codes && x.scale)) || !u_save || !A || !B || !dA || !dB))
         return fail(NF4_E_ARG, "%s: r=%d needs x, u_save, A, B, dA and dB", fn, r);
     if (!aligned(dy, 16) || (dx && !aligned(dx, 16)) ||
-        (r > 0 && (!aligned(x, 16) || !aligned(A, 16) || !aligned(B, 2) || !aligned(u_save, 4) || !aligned(dA, 16) ||
-                   !aligned(dB, 4))))
+        (r > 0 && (!aligned(x.x, 16) || !aligned(x.codes, 16) || !aligned(x.scale, 4) || !aligned(A, 16) || !aligned(B, 2) ||
+                   !aligned(u_save, 4) || !aligned(dA, 16) || !aligned(dB, 4))))
         return fail(NF4_E_ARG, "%s: misaligned pointer (dy, dx, x, A and dA need 16 bytes)", fn);
     const BwdPlan p = plan_bwd(T, N, K, r, wdense != nullptr);
     if (!ws || ws_bytes < p.ws_bytes || !aligned(ws, 256))
@@ -372,7 +372,7 @@ int nf4_lora_linear_bwd(const uint8_t* codes, const float* absmax, int64_t N, in
     const char* fn = "nf4_lora_linear_bwd";
     const int st = nf4::check_linear_common(fn, codes, absmax, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, x, u_save, dy, T, A, B, r, alpha, dx, dA, dB, ws,
+    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB, ws,
                            ws_bytes, stream);
 }
 
@@ -382,8 +382,30 @@ int nf4_lora_linear_bwd_bf16(const uint16_t* w, int64_t N, int64_t K, const uint
     const char* fn = "nf4_lora_linear_bwd_bf16";
     const int st = nf4::check_linear_dense(fn, w, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, x, u_save, dy, T, A, B, r, alpha, dx, dA, dB, ws, ws_bytes,
-                           stream);
+    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB,
+                           ws, ws_bytes, stream);
+}
+
+int nf4_lora_linear_bwd_act8(const uint8_t* codes, const float* absmax, int64_t N, int64_t K, const uint8_t* x_codes,
+                             const float* x_scale, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+                             const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws,
+                             size_t ws_bytes, nf4_stream stream) {
+    const char* fn = "nf4_lora_linear_bwd_act8";
+    const int st = nf4::check_linear_common(fn, codes, absmax, N, K, T, r, alpha);
+    if (st != NF4_OK) return st;
+    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx,
+                           dA, dB, ws, ws_bytes, stream);
+}
+
+int nf4_lora_linear_bwd_bf16_act8(const uint16_t* w, int64_t N, int64_t K, const uint8_t* x_codes, const float* x_scale,
+                                  const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+                                  const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws,
+                                  size_t ws_bytes, nf4_stream stream) {
+    const char* fn = "nf4_lora_linear_bwd_bf16_act8";
+    const int st = nf4::check_linear_dense(fn, w, N, K, T, r, alpha);
+    if (st != NF4_OK) return st;
+    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx, dA,
+                           dB, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -119,8 +119,16 @@ hipError_t launch_gemm_fwd(const FwdPlan& p, const uint8_t* codes, const float* 
                            uint16_t* y, float* u_save, void* ws, hipStream_t stream);
 hipError_t launch_lora_bwd_pre(const BwdPlan& p, const uint16_t* dy, const uint16_t* B, const float* u, int64_t T,
                                int64_t N, int r, float s, float* gpart, float* dB, float* dbpart, hipStream_t stream);
+// The linear's input as its forward left it: bf16, or (x NULL) an 8-bit checkpoint, whose values
+// are rounded to bf16 where dA is formed.
+struct SavedInput {
+    const uint16_t* x;     // [T][K]
+    const uint8_t* codes;  // [T][K]
+    const float* scale;    // [T][K/64]
+};
+
 hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
-                           const uint16_t* dy, const uint16_t* x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
+                           const uint16_t* dy, const SavedInput& x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
                            int r, float s, uint16_t* dx, float* dA, float* dB, void* ws, hipStream_t stream);
 
 hipError_t launch_skinny_fwd(const SkinnyPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* x,
@@ -128,7 +136,7 @@ hipError_t launch_skinny_fwd(const SkinnyPlan& p, const uint8_t* codes, const fl
                              uint16_t* y, float* u_save, void* ws, hipStream_t stream);
 // dX partials and the g / dB pre-pass in one launch, then the finish kernel (dX, dA)
 hipError_t launch_skinny_bwd(const SkinnyPlan& p, const BwdPlan& bp, const uint8_t* codes, const float* absmax,
-                             const uint16_t* dy, const uint16_t* x, const uint16_t* A, const uint16_t* B,
+                             const uint16_t* dy, const SavedInput& x, const uint16_t* A, const uint16_t* B,
                              const float* u, int64_t T, int64_t N, int64_t K, int r, float s, uint16_t* dx, float* dA,
                              float* dB, void* ws, hipStream_t stream);
 

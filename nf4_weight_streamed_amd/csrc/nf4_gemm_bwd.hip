@@ -19,6 +19,7 @@
 // paired across rows the same way, with nothing to dequantise.
 #include <type_traits>
 
+#include "act8.h"
 #include "common.h"
 #include "device.h"
 
@@ -66,13 +67,14 @@ struct BwdLora {
     const float* gpart;  // [parts][T][r] partials of g = dY.B
     int parts;
     const uint16_t* A;   // [r][K]
-    const uint16_t* x;   // [T][K]
+    SavedInput x;
     float* dapart;       // [token tiles][r][K] dA share of each token tile
     int r;
     float s;
 };
 
-template <int BM, bool kDense>
+// kAct8: x is an 8-bit checkpoint.
+template <int BM, bool kDense, bool kAct8>
 __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
     const uint16_t* __restrict__ dy, const void* __restrict__ weights, const float* __restrict__ absmax, int T,
     int N, int K, BwdTiles tl, BwdLora lora, uint16_t* __restrict__ dx, float* __restrict__ partial, Tables tab) {
@@ -324,7 +326,10 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         auto gpart_rsrc = [&](int p) {
             return make_rsrc(lora.gpart + (size_t(min(p, lora.parts - 1)) * T + m0) * r, gbytes);
         };
-        const auto rx = make_rsrc(lora.x + size_t(m0) * K, trows * uint32_t(K) * 2u);
+        const auto rx = kAct8 ? make_rsrc(lora.x.codes + size_t(m0) * K, trows * uint32_t(K))
+                              : make_rsrc(lora.x.x + size_t(m0) * K, trows * uint32_t(K) * 2u);
+        const auto rxs = make_rsrc(kAct8 ? lora.x.scale + size_t(m0) * (K / 64) : nullptr,
+                                   kAct8 ? trows * uint32_t(K / 64) * 4u : 0u);
         // every load of the staging is issued before the first is consumed (one memory
         // round trip at the end of the kernel, not one per loop trip)
         constexpr int XC = BM * (BK / 8) / NT;  // 16-byte x chunks per thread
@@ -349,10 +354,18 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         static_assert(XC == 8 && BM == 8 * (NT / 16) && BK == 16 * 8, "x tile: chunk blocks of 8 x 8, 16 across");
         const int xk8 = 8 * (tid & 15), xt0 = 8 * (tid >> 4);
         u32x4 xv[XC];
+        u32x2 xc[XC];
+        float xs[XC];
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
             // rows past T read zero; columns past K only feed dA columns never stored
-            xv[i] = buf_load16(rx, (uint32_t(xt0 + i) * uint32_t(K) + uint32_t(k0 + xk8)) * 2u);
+            const uint32_t at = uint32_t(xt0 + i) * uint32_t(K) + uint32_t(k0 + xk8);
+            if constexpr (kAct8) {
+                xc[i] = buf_load8(rx, at);
+                xs[i] = buf_load_f32(rxs, at / 64 * 4u);
+            } else {
+                xv[i] = buf_load16(rx, at * 2u);
+            }
         }
         constexpr int GR = 8;  // partials loaded per round (registers are free after the main loop)
         for (int jb = 0; jb < rp / 16; ++jb) {
@@ -391,6 +404,14 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
                     sg_hi[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, hh);
                     sg_lo[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, ll);
                 }
+            }
+        }
+        if constexpr (kAct8) {
+#pragma unroll
+            for (int i = 0; i < XC; ++i) {
+                float v[8];
+                act8_values8(xc[i], xs[i], v);
+                xv[i] = pack_octet(v);
             }
         }
         // x^T of columns kXCols h .. kXCols (h + 1) - 1 (with two halves a thread's chunks
@@ -623,7 +644,7 @@ BwdPlan plan_bwd(int64_t T, int64_t N, int64_t K, int r, bool dense) {
 }
 
 hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
-                           const uint16_t* dy, const uint16_t* x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
+                           const uint16_t* dy, const SavedInput& x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
                            int r, float s, uint16_t* dx, float* dA, float* dB, void* ws, hipStream_t stream) {
     char* w = static_cast<char*>(ws);
     // without dx only the LoRA part runs: one workgroup per tile, no contraction steps
@@ -634,18 +655,16 @@ hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* 
     float* dapart = reinterpret_cast<float*>(w + p.off_dapart);
     const BwdLora lora{reinterpret_cast<const float*>(w + p.off_gpart), p.gparts, A, x, dapart, r, s};
     if (dx) prof_gemm_begin(stream);
+    auto launch = [&](auto kernel, int threads, const void* weights) {
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, dy, weights, absmax, int(T), int(N), int(K), tl, lora, dx,
+                           partial, tables());
+    };
     if (wdense)
-        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<128, true>), grid, dim3(256), 0, stream, dy,
-                           static_cast<const void*>(wdense), nullptr, int(T), int(N), int(K), tl, lora, dx, partial,
-                           tables());
+        launch(x.codes ? k_nf4_gemm_bwd_dx<128, true, true> : k_nf4_gemm_bwd_dx<128, true, false>, 256, wdense);
     else if (p.bm == 256)
-        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<256, false>), grid, dim3(512), 0, stream, dy,
-                           static_cast<const void*>(codes), absmax, int(T), int(N), int(K), tl, lora, dx, partial,
-                           tables());
+        launch(x.codes ? k_nf4_gemm_bwd_dx<256, false, true> : k_nf4_gemm_bwd_dx<256, false, false>, 512, codes);
     else
-        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<128, false>), grid, dim3(256), 0, stream, dy,
-                           static_cast<const void*>(codes), absmax, int(T), int(N), int(K), tl, lora, dx, partial,
-                           tables());
+        launch(x.codes ? k_nf4_gemm_bwd_dx<128, false, true> : k_nf4_gemm_bwd_dx<128, false, false>, 256, codes);
     if (dx) prof_gemm_end(stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

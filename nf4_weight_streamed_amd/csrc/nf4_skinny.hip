@@ -665,9 +665,11 @@ __global__ __launch_bounds__(kThreads, kBOccupancy<TB>) void k_skinny_bwd(
 //    s . sum_j g[t][j] A[j][k] ), A[:, k0 .. k0 + 63] staged in LDS;
 //  - the rest: wave w takes ranks j = w, w + 4, ...: dA[j][k] = s . sum_t g[t][j] x[t][k],
 //    x[:, k0 .. k0 + 63] staged in LDS, tokens added in increasing order.
+// kAct8: x is an 8-bit checkpoint, its values rounded to bf16 like the 128-token kernels' operand.
+template <bool kAct8>
 __global__ __launch_bounds__(kThreads) void k_skinny_bwd_finish(
     const float* __restrict__ dxpart, int splits, const float* __restrict__ gpart, int gparts,
-    const uint16_t* __restrict__ A, const uint16_t* __restrict__ x, int T, int K, int r, float s, int col_blocks,
+    const uint16_t* __restrict__ A, SavedInput x, int T, int K, int r, float s, int col_blocks,
     int dx_blocks, uint16_t* __restrict__ dx, float* __restrict__ dA) {
     __shared__ float sg[kSkinnyMaxT * kMaxRank];   // g [t - t0][j]
     __shared__ float sw[kMaxRank * kFinF];  // A [j][k - k0] or x [t][k - k0]
@@ -679,14 +681,29 @@ __global__ __launch_bounds__(kThreads) void k_skinny_bwd_finish(
     // A rows (dX role) or x rows (dA role), columns k0 .. k0 + 63; every load of a role is
     // issued before the first is waited for (one memory round trip)
     const int wrows = dx_role ? r : T;
-    const auto rw = dx_role ? make_rsrc(A, uint32_t(r) * uint32_t(K) * 2u) : make_rsrc(x, uint32_t(T) * uint32_t(K) * 2u);
+    const auto rw = dx_role ? make_rsrc(A, uint32_t(r) * uint32_t(K) * 2u)
+                  : kAct8   ? make_rsrc(x.codes, uint32_t(T) * uint32_t(K))
+                            : make_rsrc(x.x, uint32_t(T) * uint32_t(K) * 2u);
     constexpr int WV = kMaxRank / kFinTk;  // rows wave + 4i
     uint32_t wv[WV];
+    float ws[WV];  // steps of the checkpoint's rows
+    if (kAct8 && !dx_role) {
+        const auto rs = make_rsrc(x.scale, uint32_t(T) * uint32_t(K / 64) * 4u);
 #pragma unroll
-    for (int i = 0; i < WV; ++i) {
-        const int row = wave + kFinTk * i;
-        wv[i] = __builtin_amdgcn_raw_buffer_load_b16(
-            rw, int(row < wrows && k < K ? (uint32_t(row) * uint32_t(K) + uint32_t(k)) * 2u : kOutOfRange), 0, 0);
+        for (int i = 0; i < WV; ++i) {
+            const int row = wave + kFinTk * i;
+            const uint32_t at = uint32_t(row) * uint32_t(K) + uint32_t(k);
+            const bool in = row < T && k < K;
+            wv[i] = __builtin_amdgcn_raw_buffer_load_b8(rw, int(in ? at : kOutOfRange), 0, 0);
+            ws[i] = buf_load_f32(rs, in ? at / 64 * 4u : kOutOfRange);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < WV; ++i) {
+            const int row = wave + kFinTk * i;
+            wv[i] = __builtin_amdgcn_raw_buffer_load_b16(
+                rw, int(row < wrows && k < K ? (uint32_t(row) * uint32_t(K) + uint32_t(k)) * 2u : kOutOfRange), 0, 0);
+        }
     }
     if (dx_role) {
         const int t = (b / col_blocks) * kFinTk + wave;
@@ -710,7 +727,9 @@ __global__ __launch_bounds__(kThreads) void k_skinny_bwd_finish(
     }
     stage_partial_sums(sg, stmp, gpart, gparts, T, r, 0, T, 0, r);  // ends with a barrier
 #pragma unroll
-    for (int i = 0; i < WV; ++i) sw[(wave + kFinTk * i) * kFinF + lane] = bf16_to_f32(uint16_t(wv[i]));
+    for (int i = 0; i < WV; ++i)
+        sw[(wave + kFinTk * i) * kFinF + lane] =
+            kAct8 ? float(__bf16((float(wv[i]) - 128.0f) * ws[i])) : bf16_to_f32(uint16_t(wv[i]));
     __syncthreads();
     if (k >= K) return;
     for (int j = wave; j < r; j += 4) {
@@ -830,7 +849,7 @@ void launch_bwd_rb(int rb, dim3 grid, const uint16_t* dy, const uint8_t* codes, 
 }
 
 hipError_t launch_skinny_bwd(const SkinnyPlan& p, const BwdPlan& bp, const uint8_t* codes, const float* absmax,
-                             const uint16_t* dy, const uint16_t* x, const uint16_t* A, const uint16_t* B,
+                             const uint16_t* dy, const SavedInput& x, const uint16_t* A, const uint16_t* B,
                              const float* u, int64_t T, int64_t N, int64_t K, int r, float s, uint16_t* dx, float* dA,
                              float* dB, void* ws, hipStream_t stream) {
     char* w = static_cast<char*>(ws);
@@ -861,8 +880,9 @@ hipError_t launch_skinny_bwd(const SkinnyPlan& p, const BwdPlan& bp, const uint8
     const int dx_blocks = dx ? col_blocks * int(cdiv(T, kFinTk)) : 0;
     const int da_blocks = r > 0 ? col_blocks : 0;
     if (dx_blocks + da_blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(k_skinny_bwd_finish, dim3(unsigned(dx_blocks + da_blocks)), dim3(kThreads), 0, stream, dxpart,
-                       p.splits, gpart, bp.gparts, A, x, int(T), int(K), r, s, col_blocks, dx_blocks, dx, dA);
+    hipLaunchKernelGGL(x.codes ? k_skinny_bwd_finish<true> : k_skinny_bwd_finish<false>,
+                       dim3(unsigned(dx_blocks + da_blocks)), dim3(kThreads), 0, stream, dxpart, p.splits, gpart,
+                       bp.gparts, A, x, int(T), int(K), r, s, col_blocks, dx_blocks, dx, dA);
     return hipGetLastError();
 }
 

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -22,6 +23,7 @@ NF4_E_ARG, NF4_E_SHAPE, NF4_E_OOM, NF4_E_HIP, NF4_E_STATE, NF4_E_BUSY = -1, -2, 
 NF4_BLOCK = 64
 NF4_MAX_RANK = 64
 NF4_DTYPE_BF16, NF4_DTYPE_F32 = 0, 1
+NF4_GATE_NONE, NF4_GATE_CHANNEL, NF4_GATE_TOKEN = 0, 1, 2
 _CODE_NAMES = {-1: "NF4_E_ARG", -2: "NF4_E_SHAPE", -3: "NF4_E_OOM", -4: "NF4_E_HIP", -5: "NF4_E_STATE",
                -6: "NF4_E_BUSY"}
 
@@ -101,6 +103,17 @@ def _load() -> C.CDLL:
         "nf4_grad_workspace": (sz, []),
         "nf4_grad_norm": (i32, [vp, vp, vp, sz, vp]),
         "nf4_grad_clip": (i32, [vp, f32, vp, vp, sz, vp]),
+        "nf4_act8_quantize": (i32, [vp, i64, i64, vp, vp, vp]),
+        "nf4_act8_dequantize": (i32, [vp, vp, i64, i64, vp, vp]),
+        "nf4_silu_mul_fwd_act8": (i32, [vp, vp, i64, i64, vp, vp, vp, vp, vp, vp]),
+        "nf4_silu_mul_act8": (i32, [vp, vp, vp, vp, i64, i64, vp, vp]),
+        "nf4_silu_mul_bwd_act8": (i32, [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp]),
+        "nf4_lora_linear_bwd_act8": (i32, [vp, vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]),
+        "nf4_lora_linear_bwd_bf16_act8": (i32, [vp, i64, i64, vp, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]),
+        "nf4_residual_norm_fwd": (i32, [vp, vp, i64, i64, i32, vp, i32, vp, f32, vp, f32, f32, vp, vp, vp, vp, vp, vp, vp]),
+        "nf4_residual_norm_bwd_workspace": (sz, [i64, i64, i32]),
+        "nf4_residual_norm_bwd": (i32, [C.POINTER(vp), i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, vp, i32, vp, f32, vp,
+                                        f32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "stream_pool_create": (i32, [C.POINTER(HostBlock), i32, vp, sz, i32, vp, C.POINTER(vp)]),
         "stream_pool_prefetch": (i32, [vp, i32]),
         "stream_pool_acquire": (i32, [vp, i32, vp, C.POINTER(vp)]),
@@ -714,6 +727,305 @@ class GradList:
             self.close()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- activations in 8 bits, fused residual norms
+
+class Act8(NamedTuple):
+    """The 8-bit checkpoint of a bf16 matrix [T, C]: codes uint8 [T, C] and one step for each 64
+    elements of a row, scale float32 [T, C / 64]; it stands for (codes - 128) * scale."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+
+def act8_empty(t: int, c: int, device="cuda", stream=None) -> Act8:
+    """Room for the checkpoint of a [t, c] activation (c a multiple of 64)."""
+    return Act8(_empty((t, c), torch.uint8, device, stream), _empty((t, c // NF4_BLOCK), torch.float32, device, stream))
+
+
+def _need_act8(a, name: str, shape: tuple) -> None:
+    if not isinstance(a, Act8):
+        raise TypeError(f"{name} must be an Act8")
+    _need(a.codes, name + ".codes", torch.uint8, shape)
+    _need(a.scale, name + ".scale", torch.float32, (shape[0], shape[1] // NF4_BLOCK))
+
+
+def _matrix(x, name: str) -> tuple:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(x.shape)}")
+    return tuple(x.shape)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def act8_quantize(x, out: Act8 | None = None, stream=None) -> Act8:
+    """The checkpoint of x [T, C] (bf16, C a multiple of 64)."""
+    shape = t, c = _matrix(x, "x")
+    _need(x, "x", torch.bfloat16, shape)
+    out = act8_empty(t, c, x.device, stream) if out is None else out
+    _need_act8(out, "out", shape)
+    _enqueue(_device(x, *out), stream, _lib.nf4_act8_quantize, x.data_ptr(), t, c, out.codes.data_ptr(), out.scale.data_ptr())
+    return out
+
+
+def _act8_shape(a, name: str) -> tuple:
+    if not isinstance(a, Act8):
+        raise TypeError(f"{name} must be an Act8")
+    return _matrix(a.codes, name + ".codes")
+
+
+def act8_dequantize(x8: Act8, out=None, stream=None):
+    """What a checkpoint stands for, rounded to bf16 [T, C]."""
+    shape = t, c = _act8_shape(x8, "x8")
+    _need_act8(x8, "x8", shape)
+    out = _empty(shape, torch.bfloat16, x8.codes.device, stream) if out is None else out
+    _need(out, "out", torch.bfloat16, shape)
+    _enqueue(_device(out, *x8), stream, _lib.nf4_act8_dequantize, x8.codes.data_ptr(), x8.scale.data_ptr(), t, c,
+             out.data_ptr())
+    return out
+
+
+def silu_mul_fwd_act8(gate, up, out=None, gate8: Act8 | None = None, up8: Act8 | None = None, stream=None):
+    """silu_mul_fwd with the checkpoints of its inputs: returns (m, gate8, up8)."""
+    shape = t, c = _matrix(gate, "gate")
+    _need(gate, "gate", torch.bfloat16, shape)
+    _need(up, "up", torch.bfloat16, shape)
+    out = _empty(shape, torch.bfloat16, gate.device, stream) if out is None else out
+    gate8 = act8_empty(t, c, gate.device, stream) if gate8 is None else gate8
+    up8 = act8_empty(t, c, gate.device, stream) if up8 is None else up8
+    _need(out, "out", torch.bfloat16, shape)
+    _need_act8(gate8, "gate8", shape)
+    _need_act8(up8, "up8", shape)
+    _enqueue(_device(gate, up, out, *gate8, *up8), stream, _lib.nf4_silu_mul_fwd_act8, gate.data_ptr(), up.data_ptr(), t, c,
+             out.data_ptr(), gate8.codes.data_ptr(), gate8.scale.data_ptr(), up8.codes.data_ptr(), up8.scale.data_ptr())
+    return out, gate8, up8
+
+
+def silu_mul_act8(gate8: Act8, up8: Act8, out=None, stream=None):
+    """SiLU(gate) * up at the checkpoints' values: the forward's product again, bf16."""
+    shape = t, c = _act8_shape(gate8, "gate8")
+    _need_act8(gate8, "gate8", shape)
+    _need_act8(up8, "up8", shape)
+    out = _empty(shape, torch.bfloat16, gate8.codes.device, stream) if out is None else out
+    _need(out, "out", torch.bfloat16, shape)
+    _enqueue(_device(out, *gate8, *up8), stream, _lib.nf4_silu_mul_act8, gate8.codes.data_ptr(), gate8.scale.data_ptr(),
+             up8.codes.data_ptr(), up8.scale.data_ptr(), t, c, out.data_ptr())
+    return out
+
+
+def silu_mul_bwd_act8(gate8: Act8, up8: Act8, dm, dgate=None, dup=None, stream=None):
+    """silu_mul_bwd at the checkpoints' values: returns (dgate, dup)."""
+    shape = t, c = _act8_shape(gate8, "gate8")
+    _need_act8(gate8, "gate8", shape)
+    _need_act8(up8, "up8", shape)
+    _need(dm, "dm", torch.bfloat16, shape)
+    dgate = _empty(shape, torch.bfloat16, dm.device, stream) if dgate is None else dgate
+    dup = _empty(shape, torch.bfloat16, dm.device, stream) if dup is None else dup
+    _need(dgate, "dgate", torch.bfloat16, shape)
+    _need(dup, "dup", torch.bfloat16, shape)
+    _enqueue(_device(dm, dgate, dup, *gate8, *up8), stream, _lib.nf4_silu_mul_bwd_act8, gate8.codes.data_ptr(),
+             gate8.scale.data_ptr(), up8.codes.data_ptr(), up8.scale.data_ptr(), dm.data_ptr(), t, c, dgate.data_ptr(),
+             dup.data_ptr())
+    return dgate, dup
+
+
+def _linear_bwd_act8(base, n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream, call, ws_bytes):
+    """The two calls below after their base tensors' checks."""
+    t = _matrix(dy, "dy")[0]
+    r = 0 if A is None else A.shape[0]
+    _need(dy, "dy", torch.bfloat16, (t, n))
+    if r:
+        _need_act8(x8, "x8", (t, k))
+        _need(u, "u", torch.float32, (t, r))
+        _need(A, "A", torch.bfloat16, (r, k))
+        _need(B, "B", torch.bfloat16, (n, r))
+        dA = _empty((r, k), torch.float32, dy.device, stream) if dA is None else dA
+        dB = _empty((n, r), torch.float32, dy.device, stream) if dB is None else dB
+        _need(dA, "dA", torch.float32, (r, k))
+        _need(dB, "dB", torch.float32, (n, r))
+    else:
+        x8, u, A, B, dA, dB = Act8(None, None), None, None, None, None, None
+    if need_dx and dx is None:
+        dx = _empty((t, k), torch.bfloat16, dy.device, stream)
+    if dx is not None:
+        _need(dx, "dx", torch.bfloat16, (t, k))
+    if ws is None:
+        ws = _empty(max(ws_bytes(t, n, k, r), 256), torch.uint8, dy.device, stream)
+    _enqueue(_device(dy, *base, x8.codes, x8.scale, u, A, B, dx, dA, dB, ws), stream, call, *(b.data_ptr() for b in base), n, k,
+             _opt(x8.codes), _opt(x8.scale), _opt(u), dy.data_ptr(), t, _opt(A), _opt(B), r, float(alpha), _opt(dx), _opt(dA),
+             _opt(dB), ws.data_ptr(), ws.numel() * ws.element_size())
+    return dx, dA, dB
+
+
+# of the sizes alone
+_bwd_ws = functools.lru_cache(maxsize=256)(bwd_workspace_bytes)
+_bwd_bf16_ws = functools.lru_cache(maxsize=256)(bwd_bf16_workspace_bytes)
+
+
+def lora_linear_bwd_act8(codes, absmax, x8: Act8, u, dy, A, B, alpha: float, dx=None, dA=None, dB=None, ws=None,
+                         need_dx: bool = True, stream=None):
+    """lora_linear_bwd with the forward's input as its checkpoint: returns (dx or None, dA, dB)."""
+    n, k = _matrix(codes, "codes")[0], codes.shape[1] * 2
+    _need(codes, "codes", torch.uint8, (n, k // 2))
+    _need(absmax, "absmax", torch.float32, (n, k // NF4_BLOCK))
+    return _linear_bwd_act8((codes, absmax), n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream,
+                            _lib.nf4_lora_linear_bwd_act8, _bwd_ws)
+
+
+def lora_linear_bwd_bf16_act8(w, x8: Act8, u, dy, A, B, alpha: float, dx=None, dA=None, dB=None, ws=None,
+                              need_dx: bool = True, stream=None):
+    """lora_linear_bwd_bf16 with the forward's input as its checkpoint: returns (dx or None, dA, dB)."""
+    n, k = _matrix(w, "w")
+    _need(w, "w", torch.bfloat16, (n, k))
+    return _linear_bwd_act8((w,), n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream,
+                            _lib.nf4_lora_linear_bwd_bf16_act8, _bwd_bf16_ws)
+
+
+class ResidualNorm(NamedTuple):
+    """What residual_norm_fwd returns: the stream h (its input where no block's output joined it),
+    the normalised n and its checkpoint (or None), the rows' 1 / rms of o (or None) and of the stream."""
+    h: torch.Tensor
+    n: torch.Tensor
+    n8: Act8 | None
+    rstd_o: torch.Tensor | None
+    rstd: torch.Tensor
+
+
+class ResidualNormGrads(NamedTuple):
+    """What residual_norm_bwd returns; None for what does not apply or was not asked for."""
+    dh: torch.Tensor
+    do: torch.Tensor | None
+    dgate: torch.Tensor | None
+    dpost_gain: torch.Tensor | None
+    dgain: torch.Tensor | None
+
+
+def _norm_params(t, c, post_norm, post_gain, gate, gain) -> int:
+    """Checks them; returns the gate's kind."""
+    if post_gain is not None:
+        if not post_norm:
+            raise ValueError("post_gain needs post_norm=True")
+        _need(post_gain, "post_gain", torch.bfloat16, (c,))
+    if gain is not None:
+        _need(gain, "gain", torch.bfloat16, (c,))
+    if gate is None:
+        return NF4_GATE_NONE
+    _need(gate, "gate", torch.bfloat16, (c,) if gate.dim() == 1 else (t, c))
+    return NF4_GATE_CHANNEL if gate.dim() == 1 else NF4_GATE_TOKEN
+
+
+def residual_norm_fwd(h, o=None, post_norm: bool = False, post_gain=None, gate=None, scale: float = 1.0, gain=None,
+                      gain_offset: float = 0.0, eps: float = 1e-6, checkpoint: bool = False, h_out=None, n=None,
+                      n8: Act8 | None = None, rstd_o=None, rstd=None, stream=None) -> ResidualNorm:
+    """A block's output o joins the stream h and the stream is normalised, in one pass (bf16 [T, H]):
+    h + scale * gate * o, with o normalised first under post_norm, and RMSNorm of that. gate: [H] or [T, H];
+    the norms' factors are gain_offset + their gain ([H]), or 1. o None: the norm alone. checkpoint=True
+    (or n8) also writes n's 8-bit checkpoint."""
+    shape = t, c = _matrix(h, "h")
+    _need(h, "h", torch.bfloat16, shape)
+    kind = _norm_params(t, c, post_norm, post_gain, gate, gain)
+    dev = h.device
+    if o is None:
+        if post_norm or gate is not None or h_out is not None:
+            raise ValueError("post_norm, gate and h_out need a block's output o")
+    else:
+        _need(o, "o", torch.bfloat16, shape)
+        h_out = _empty(shape, torch.bfloat16, dev, stream) if h_out is None else h_out
+        _need(h_out, "h_out", torch.bfloat16, shape)
+    n = _empty(shape, torch.bfloat16, dev, stream) if n is None else n
+    _need(n, "n", torch.bfloat16, shape)
+    if n8 is None and checkpoint:
+        n8 = act8_empty(t, c, dev, stream)
+    if n8 is not None:
+        _need_act8(n8, "n8", shape)
+    if not post_norm:
+        rstd_o = None
+    else:
+        rstd_o = _empty((t,), torch.float32, dev, stream) if rstd_o is None else rstd_o
+        _need(rstd_o, "rstd_o", torch.float32, (t,))
+    rstd = _empty((t,), torch.float32, dev, stream) if rstd is None else rstd
+    _need(rstd, "rstd", torch.float32, (t,))
+    codes, step = n8 or (None, None)
+    _enqueue(_device(h, o, post_gain, gate, gain, h_out, n, codes, step, rstd_o, rstd), stream, _lib.nf4_residual_norm_fwd,
+             h.data_ptr(), _opt(o), t, c, int(bool(post_norm)), _opt(post_gain), kind, _opt(gate), float(scale), _opt(gain),
+             float(gain_offset), float(eps), _opt(h_out), n.data_ptr(), _opt(codes), _opt(step), _opt(rstd_o),
+             rstd.data_ptr())
+    return ResidualNorm(h if o is None else h_out, n, n8, rstd_o, rstd)
+
+
+@functools.lru_cache(maxsize=256)
+def residual_norm_bwd_workspace_bytes(T: int, H: int, sums: bool = True) -> int:
+    return int(_lib.nf4_residual_norm_bwd_workspace(T, H, int(bool(sums))))
+
+
+def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=None, post_norm: bool = False, rstd_o=None,
+                      post_gain=None, gate=None, scale: float = 1.0, gain=None, gain_offset: float = 0.0,
+                      param_grads: bool = True, dh=None, do=None, dgate=None, dpost_gain=None, dgain=None, ws=None,
+                      stream=None) -> ResidualNormGrads:
+    """Backward of residual_norm_fwd. dn: the gradient of n, or a list of up to three (one for each of
+    its readers, added in fp32); dres: the gradient that reaches the stream past the norm; the stream as h
+    (the forward's result) or, without a gain, as n's checkpoint n8. With o (the block's output) the
+    branch's gradients come too: do, and dgate (bf16 [T, H], or float32 [H] for a gate a channel).
+    param_grads=False leaves out those of the gains and the gate (frozen parameters)."""
+    dn = [dn] if isinstance(dn, torch.Tensor) else list(dn)
+    if not 1 <= len(dn) <= 3:
+        raise ValueError(f"dn must be one to three tensors, got {len(dn)}")
+    shape = t, c = _matrix(dn[0], "dn")
+    for d in dn:
+        _need(d, "dn", torch.bfloat16, shape)
+    dev = dn[0].device
+    kind = _norm_params(t, c, post_norm, post_gain, gate, gain)
+    if (h is None) == (n8 is None):
+        raise ValueError("give the normalised stream as h or as n8")
+    if n8 is not None:
+        if gain is not None:
+            raise ValueError("n8 stands in for the stream only without a gain")
+        _need_act8(n8, "n8", shape)
+    _need(rstd, "rstd", torch.float32, (t,))
+    for x, name in ((h, "h"), (dres, "dres"), (o, "o")):
+        if x is not None:
+            _need(x, name, torch.bfloat16, shape)
+    dh = _empty(shape, torch.bfloat16, dev, stream) if dh is None else dh
+    _need(dh, "dh", torch.bfloat16, shape)
+    if o is None:
+        if post_norm or gate is not None or do is not None:
+            raise ValueError("post_norm, gate and do need the block's output o")
+    else:
+        do = _empty(shape, torch.bfloat16, dev, stream) if do is None else do
+        _need(do, "do", torch.bfloat16, shape)
+    if post_norm:
+        _need(rstd_o, "rstd_o", torch.float32, (t,))
+    else:
+        rstd_o = None
+
+    def param_grad(p, out, name, dtype, at):
+        if p is None or not param_grads:
+            if out is not None:
+                raise ValueError(f"{name} is not asked for")
+            return None
+        out = _empty(at, dtype, dev, stream) if out is None else out
+        _need(out, name, dtype, at)
+        return out
+
+    channel = kind == NF4_GATE_CHANNEL
+    dgate = param_grad(gate, dgate, "dgate", torch.float32 if channel else torch.bfloat16, (c,) if channel else shape)
+    dpost_gain = param_grad(post_gain, dpost_gain, "dpost_gain", torch.float32, (c,))
+    dgain = param_grad(gain, dgain, "dgain", torch.float32, (c,))
+    sums = dgain is not None or dpost_gain is not None or (channel and dgate is not None)
+    if ws is None and sums:
+        ws = _empty(max(residual_norm_bwd_workspace_bytes(t, c), 256), torch.uint8, dev, stream)
+    codes, step = n8 or (None, None)
+    arr = (C.c_void_p * len(dn))(*(d.data_ptr() for d in dn))
+    _enqueue(_device(*dn, dres, h, codes, step, rstd, o, rstd_o, post_gain, gate, gain, dh, do, dgate, dpost_gain, dgain, ws),
+             stream, _lib.nf4_residual_norm_bwd, arr, len(dn), _opt(dres), _opt(h), _opt(codes), _opt(step), rstd.data_ptr(),
+             _opt(o), _opt(rstd_o), t, c, int(bool(post_norm)), _opt(post_gain), kind, _opt(gate), float(scale), _opt(gain),
+             float(gain_offset), dh.data_ptr(), _opt(do), _opt(dgate), _opt(dpost_gain), _opt(dgain), _opt(ws),
+             0 if ws is None else ws.numel() * ws.element_size())
+    return ResidualNormGrads(dh, do, dgate, dpost_gain, dgain)
 
 
 def block_layout(shapes, layers: int, dense: bool = False):

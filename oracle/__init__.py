@@ -12,3 +12,4 @@ Pinning status of every function is listed in the module header of
 
 from .nf4_oracle import *  # noqa: F401,F403
 from .decoder_oracle import *  # noqa: F401,F403
+from .act8_oracle import *  # noqa: F401,F403
