@@ -331,7 +331,7 @@ int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const 
                                             ws, s),
                           "nf4_lora_linear_bwd (few-token path)");
     if (r > 0) {
-        int st = hip_status(launch_lora_bwd_pre(p, dy, B, u_save, T, N, r, scale,
+        int st = hip_status(launch_lora_bwd_pre(p, dy, B, u_save, T, N, r, scale, x.codes != nullptr,
                                                 reinterpret_cast<float*>(w + p.off_gpart), dB,
                                                 reinterpret_cast<float*>(w + p.off_dbpart), s),
                             "nf4_lora_linear_bwd (g, dB)");

@@ -117,8 +117,10 @@ hipError_t launch_lora_down(const FwdPlan& p, const uint16_t* x, const uint16_t*
 hipError_t launch_gemm_fwd(const FwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
                            const uint16_t* x, const uint16_t* B, int64_t T, int64_t N, int64_t K, int r, float s,
                            uint16_t* y, float* u_save, void* ws, hipStream_t stream);
+// three: dB from u as three bf16 instead of two
 hipError_t launch_lora_bwd_pre(const BwdPlan& p, const uint16_t* dy, const uint16_t* B, const float* u, int64_t T,
-                               int64_t N, int r, float s, float* gpart, float* dB, float* dbpart, hipStream_t stream);
+                               int64_t N, int r, float s, bool three, float* gpart, float* dB, float* dbpart,
+                               hipStream_t stream);
 // The linear's input as its forward left it: bf16, or (x NULL) an 8-bit checkpoint, whose values
 // are rounded to bf16 where dA is formed.
 struct SavedInput {

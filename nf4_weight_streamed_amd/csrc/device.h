@@ -49,6 +49,14 @@ __device__ __forceinline__ void split_bf16(float v, __bf16& hi, __bf16& lo) {
     lo = (__bf16)(v - (float)hi);
 }
 
+// Split into three: hi + mid + lo equals v to fp32's own precision.
+__device__ __forceinline__ void split_bf16(float v, __bf16& hi, __bf16& mid, __bf16& lo) {
+    hi = (__bf16)v;
+    const float rest = v - (float)hi;
+    mid = (__bf16)rest;
+    lo = (__bf16)(rest - (float)mid);
+}
+
 // The dispatcher hands workgroups to the 8 XCDs (each with its own L2) round-robin
 // in linear-id order. xcd_tile_order maps linear id L of a grid of `total`
 // workgroups to a tile index such that each XCD runs one contiguous range of tile

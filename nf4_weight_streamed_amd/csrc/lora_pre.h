@@ -35,11 +35,14 @@ struct GSmem {
     uint16_t bt[2][16 * RB][kGChunk + 8];
     float red[4][RB][64][4];
 };
-template <int RB, int DBT>
+// kThree: (s.u) as three bf16, so that dB is off by fp32's roundings alone (with two, by 2^-17 of
+// each term).
+template <int RB, int DBT, bool kThree>
 struct DbSmem {
     uint16_t dyt[64][DBT + 8];       // [n][t]
     uint16_t uh[16 * RB][DBT + 8];   // (s.u)^T hi [j][t]
     uint16_t ul[16 * RB][DBT + 8];   // lo
+    uint16_t ur[kThree ? 16 * RB : 1][DBT + 8];  // what both leave
 };
 
 // GRING chunks of loads in flight (1 or 2; 2 where the registers allow it)
@@ -173,9 +176,9 @@ __device__ void g_role(const uint16_t* __restrict__ dy, const uint16_t* __restri
 }
 
 // tokens [t_begin, t_end) of features 64 blk .. 64 blk + 63 -> dst [N][r]
-template <int RB, int DBT>
+template <int RB, int DBT, bool kThree>
 __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict__ u, int T, int N, int r, float s,
-                        int blk, int t_begin, int t_end, float* __restrict__ dst, DbSmem<RB, DBT>& sm) {
+                        int blk, int t_begin, int t_end, float* __restrict__ dst, DbSmem<RB, DBT, kThree>& sm) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int n0 = blk * 64;
     // dY: 16-byte pieces of tokens DV lt .. DV lt + DV - 1, features ln8 .. ln8 + 7 per
@@ -239,8 +242,16 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
         for (int q = 0; q < UV / 2; ++q) {
             const int o = tid + kThreads * q, j = o % (16 * RB), tp = o / (16 * RB);
             __bf16 h0, l0, h1, l1;
-            split_bf16(s * uv[2 * q], h0, l0);
-            split_bf16(s * uv[2 * q + 1], h1, l1);
+            if constexpr (kThree) {
+                __bf16 r0, r1;
+                split_bf16(s * uv[2 * q], h0, l0, r0);
+                split_bf16(s * uv[2 * q + 1], h1, l1, r1);
+                *reinterpret_cast<uint32_t*>(&sm.ur[j][2 * tp]) =
+                    uint32_t(__builtin_bit_cast(uint16_t, r0)) | (uint32_t(__builtin_bit_cast(uint16_t, r1)) << 16);
+            } else {
+                split_bf16(s * uv[2 * q], h0, l0);
+                split_bf16(s * uv[2 * q + 1], h1, l1);
+            }
             *reinterpret_cast<uint32_t*>(&sm.uh[j][2 * tp]) =
                 uint32_t(__builtin_bit_cast(uint16_t, h0)) | (uint32_t(__builtin_bit_cast(uint16_t, h1)) << 16);
             *reinterpret_cast<uint32_t*>(&sm.ul[j][2 * tp]) =
@@ -267,6 +278,9 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
                 const bf16x8 bl = as_bf16x8(*reinterpret_cast<const u32x4*>(&sm.ul[16 * b + (lane & 15)][32 * kk + kof]));
                 acc[b] = mfma16x16x32(a, bh, acc[b]);
                 acc[b] = mfma16x16x32(a, bl, acc[b]);
+                if constexpr (kThree)
+                    acc[b] = mfma16x16x32(
+                        a, as_bf16x8(*reinterpret_cast<const u32x4*>(&sm.ur[16 * b + (lane & 15)][32 * kk + kof])), acc[b]);
             }
         }
     }
@@ -279,10 +293,10 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
         }
 }
 
-template <int RB, int DBT>
+template <int RB, int DBT, bool kThree>
 union PreSmem {
     GSmem<RB> g;
-    DbSmem<RB, DBT> d;
+    DbSmem<RB, DBT, kThree> d;
 };
 
 }  // namespace pre

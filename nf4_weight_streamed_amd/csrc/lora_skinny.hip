@@ -83,13 +83,13 @@ using pre::kGChunk;
 using pre::kTC;
 using pre::PreSmem;
 
-template <int RB>
+template <int RB, bool kThree>
 __global__ __launch_bounds__(kThreads) void k_lora_bwd_pre(const uint16_t* __restrict__ dy,
                                                            const uint16_t* __restrict__ B,
                                                            const float* __restrict__ u, int T, int N, int r, float s,
                                                            int gsteps, int gblocks, int dbtokens, float* __restrict__ gpart,
                                                            float* __restrict__ dB, float* __restrict__ dbpart) {
-    __shared__ __align__(16) PreSmem<RB, pre::kDbTLong> sm;
+    __shared__ __align__(16) PreSmem<RB, pre::kDbTLong, kThree> sm;
     if (int(blockIdx.x) < gblocks) {
         g_role<RB, (RB <= 2 ? 2 : 1)>(dy, B, T, N, r, gsteps, blockIdx.x, gpart, sm.g);  // two chunks in flight where the registers allow
         return;
@@ -97,7 +97,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_bwd_pre(const uint16_t* __res
     const int nblocks = (N + 63) / 64, d = int(blockIdx.x) - gblocks;
     const int chunk = d / nblocks, t_begin = chunk * dbtokens;
     float* dst = dbtokens >= T ? dB : dbpart + size_t(chunk) * N * r;
-    db_role<RB, pre::kDbTLong>(dy, u, T, N, r, s, d % nblocks, t_begin, min(T, t_begin + dbtokens), dst, sm.d);
+    db_role<RB, pre::kDbTLong, kThree>(dy, u, T, N, r, s, d % nblocks, t_begin, min(T, t_begin + dbtokens), dst, sm.d);
 }
 
 template <int RB>
@@ -109,11 +109,12 @@ void launch_down_rb(const FwdPlan& p, const uint16_t* x, const uint16_t* A, int6
 
 template <int RB>
 void launch_pre_rb(const BwdPlan& p, const uint16_t* dy, const uint16_t* B, const float* u, int64_t T, int64_t N,
-                   int r, float s, float* gpart, float* dB, float* dbpart, hipStream_t stream) {
+                   int r, float s, bool three, float* gpart, float* dB, float* dbpart, hipStream_t stream) {
     const int gblocks = int(cdiv(T, kTC)) * p.gparts;
     const int dblocks = int(cdiv(N, 64)) * p.dbchunks;
-    hipLaunchKernelGGL(k_lora_bwd_pre<RB>, dim3(unsigned(gblocks + dblocks)), dim3(kThreads), 0, stream, dy, B, u,
-                       int(T), int(N), r, s, p.gsteps, gblocks, p.dbtokens, gpart, dB, dbpart);
+    hipLaunchKernelGGL((three ? k_lora_bwd_pre<RB, true> : k_lora_bwd_pre<RB, false>), dim3(unsigned(gblocks + dblocks)),
+                       dim3(kThreads), 0, stream, dy, B, u, int(T), int(N), r, s, p.gsteps, gblocks, p.dbtokens, gpart, dB,
+                       dbpart);
 }
 
 }  // namespace
@@ -152,12 +153,13 @@ hipError_t launch_lora_down(const FwdPlan& p, const uint16_t* x, const uint16_t*
 }
 
 hipError_t launch_lora_bwd_pre(const BwdPlan& p, const uint16_t* dy, const uint16_t* B, const float* u, int64_t T,
-                               int64_t N, int r, float s, float* gpart, float* dB, float* dbpart, hipStream_t stream) {
+                               int64_t N, int r, float s, bool three, float* gpart, float* dB, float* dbpart,
+                               hipStream_t stream) {
     switch ((r + 15) / 16) {
-        case 1: launch_pre_rb<1>(p, dy, B, u, T, N, r, s, gpart, dB, dbpart, stream); break;
-        case 2: launch_pre_rb<2>(p, dy, B, u, T, N, r, s, gpart, dB, dbpart, stream); break;
-        case 3: launch_pre_rb<3>(p, dy, B, u, T, N, r, s, gpart, dB, dbpart, stream); break;
-        default: launch_pre_rb<4>(p, dy, B, u, T, N, r, s, gpart, dB, dbpart, stream); break;
+        case 1: launch_pre_rb<1>(p, dy, B, u, T, N, r, s, three, gpart, dB, dbpart, stream); break;
+        case 2: launch_pre_rb<2>(p, dy, B, u, T, N, r, s, three, gpart, dB, dbpart, stream); break;
+        case 3: launch_pre_rb<3>(p, dy, B, u, T, N, r, s, three, gpart, dB, dbpart, stream); break;
+        default: launch_pre_rb<4>(p, dy, B, u, T, N, r, s, three, gpart, dB, dbpart, stream); break;
     }
     return hipGetLastError();
 }

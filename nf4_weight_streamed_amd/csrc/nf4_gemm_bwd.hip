@@ -73,7 +73,8 @@ struct BwdLora {
     float s;
 };
 
-// kAct8: x is an 8-bit checkpoint.
+// kAct8: x is an 8-bit checkpoint, and dA takes s.g as three bf16, so that it is off by fp32's
+// roundings alone (with two, by 2^-17 of each term).
 template <int BM, bool kDense, bool kAct8>
 __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
     const uint16_t* __restrict__ dy, const void* __restrict__ weights, const float* __restrict__ absmax, int T,
@@ -91,11 +92,12 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
     // table; LoRA epilogue: (s.g)^T hi/lo for up to 64 ranks and the x tile transposed
     // (one 64-column half at a time with 128 tokens, all 128 columns with 256).
     constexpr int kTP = BM + 8;  // pitch of the epilogue's [.][t] tiles
-    constexpr int kXHalves = BM == 256 ? 1 : 2;
+    constexpr int kParts = kAct8 ? 3 : 2;         // bf16 values of an s.g
+    constexpr int kXHalves = BM == 256 && !kAct8 ? 1 : 2;
     constexpr int kXCols = BK / kXHalves;         // x columns staged at once
     constexpr int kBuf = BM * kLds + BK * kLdsW;  // one buffer: dY tile, then weight tile
     constexpr int kMain = 2 * kBuf + 2 * 512;
-    constexpr int kEpi = (2 * 64 + kXCols) * kTP;
+    constexpr int kEpi = (kParts * 64 + kXCols) * kTP;
     __shared__ __align__(16) uint16_t smem[kMain > kEpi ? kMain : kEpi];
     float* const sLut = reinterpret_cast<float*>(smem + 2 * kBuf);
 
@@ -316,7 +318,8 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         if (nb_begin >= nb_end) __syncthreads();
         uint16_t* const sg_hi = smem;             // [64][kTP]
         uint16_t* const sg_lo = smem + 64 * kTP;  // [64][kTP]
-        uint16_t* const sxt = smem + 128 * kTP;   // [BK / 2][kTP]
+        uint16_t* const sg_rest = smem + 128 * kTP;  // kAct8: [64][kTP], what both leave
+        uint16_t* const sxt = smem + kParts * 64 * kTP;  // [kXCols][kTP]
         const int rp = (r + 15) & ~15;
         // one descriptor per partial over this tile's rows, so sizes and offsets stay
         // small for any token count; 12 bytes of slack keep the last 16-byte load (4-byte
@@ -400,7 +403,14 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     __bf16 hh, ll;
-                    split_bf16(j + c < r ? lora.s * v[c] : 0.0f, hh, ll);
+                    const float sg = j + c < r ? lora.s * v[c] : 0.0f;
+                    if constexpr (kAct8) {
+                        __bf16 rr;
+                        split_bf16(sg, hh, ll, rr);
+                        sg_rest[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, rr);
+                    } else {
+                        split_bf16(sg, hh, ll);
+                    }
                     sg_hi[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, hh);
                     sg_lo[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, ll);
                 }
@@ -463,8 +473,11 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         }
 
         // dA share of this token tile: D[k][j] over t, 16x16x32 MFMAs; per staged group
-        // of kXCols columns, wave w owns the K sub-block w (16 columns)
-        static_assert(kXCols == 16 * (NT / 64), "one 16-column K sub-block per wave");
+        // of kXCols columns, wave w owns the K sub-block w (16 columns) modulo their number, and
+        // where the waves are more, every kTurns-th block of 16 ranks
+        constexpr int kSubs = kXCols / 16, kTurns = NT / 64 / kSubs;
+        static_assert(kSubs * kTurns == NT / 64, "a whole number of waves per 16-column K sub-block");
+        const int sub = wave % kSubs;
         const int l16 = lane & 15, t8 = 8 * (lane >> 4);
         float* dpart = lora.dapart + size_t(tm) * r * K;
         for (int h = 0; h < kXHalves; ++h) {
@@ -473,19 +486,22 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
                 stage_x(h);
                 __syncthreads();
             }
-            for (int jb = 0; jb < rp / 16; ++jb) {
+            for (int jb = wave / kSubs; jb < rp / 16; jb += kTurns) {
                 f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ts = 0; ts < BM / 32; ++ts) {
                     const int tt = 32 * ts + t8;
-                    const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[(16 * wave + l16) * kTP + tt]));
+                    const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[(16 * sub + l16) * kTP + tt]));
                     const bf16x8 gh = as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_hi[(16 * jb + l16) * kTP + tt]));
                     const bf16x8 gl = as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_lo[(16 * jb + l16) * kTP + tt]));
                     d = mfma16x16x32(xa, gh, d);
                     d = mfma16x16x32(xa, gl, d);
+                    if constexpr (kAct8)
+                        d = mfma16x16x32(
+                            xa, as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_rest[(16 * jb + l16) * kTP + tt])), d);
                 }
-                // lane holds D[k = 64 h + 16 wave + 4 (lane / 16) + e][j = 16 jb + lane % 16]
-                const int j = 16 * jb + l16, kq = k0 + kXCols * h + 16 * wave + 4 * (lane >> 4);
+                // lane holds D[k = kXCols h + 16 sub + 4 (lane / 16) + e][j = 16 jb + lane % 16]
+                const int j = 16 * jb + l16, kq = k0 + kXCols * h + 16 * sub + 4 * (lane >> 4);
                 if (j < r && kq < K) *reinterpret_cast<f32x4*>(&dpart[size_t(j) * K + kq]) = d;
             }
         }

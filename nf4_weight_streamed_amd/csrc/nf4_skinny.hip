@@ -634,7 +634,7 @@ __device__ __forceinline__ void skinny_bwd_dx(const uint16_t* __restrict__ dy, c
 // column block and split each), then the LoRA pre-pass roles, numbered from dx_total:
 // g workgroups [0, gblocks), dB workgroups [gblocks, gblocks + dblocks). The roles share
 // no data inside the launch (g is summed by the finish kernel, dB is final).
-template <int RB, int TB>
+template <int RB, int TB, bool kThree>
 __global__ __launch_bounds__(kThreads, kBOccupancy<TB>) void k_skinny_bwd(
     const uint16_t* __restrict__ dy, const uint8_t* __restrict__ codes, const float* __restrict__ absmax,
     const uint16_t* __restrict__ B, const float* __restrict__ u, int T, int N, int K, int r, float s,
@@ -642,7 +642,7 @@ __global__ __launch_bounds__(kThreads, kBOccupancy<TB>) void k_skinny_bwd(
     float* __restrict__ gpart, float* __restrict__ dB, Tables tab) {
     __shared__ __align__(16) union {
         BwdSmem<TB> dx;
-        pre::PreSmem<RB, pre::kTC> pre;
+        pre::PreSmem<RB, pre::kTC, kThree> pre;
     } sm;
     // dX workgroups in an XCD-aware order (each XCD runs a contiguous range of (column
     // block, split) pairs, column block fastest): the eight column blocks whose scales
@@ -656,7 +656,7 @@ __global__ __launch_bounds__(kThreads, kBOccupancy<TB>) void k_skinny_bwd(
     if (blk < gblocks)
         pre::g_role<RB, 1>(dy, B, T, N, r, gsteps, blk, gpart, sm.pre.g);
     else if (blk < gblocks + dblocks)
-        pre::db_role<RB, pre::kTC>(dy, u, T, N, r, s, blk - gblocks, 0, T, dB, sm.pre.d);
+        pre::db_role<RB, pre::kTC, kThree>(dy, u, T, N, r, s, blk - gblocks, 0, T, dB, sm.pre.d);
 }
 
 // Backward finish, two kinds of workgroups in one launch (64 features each, lane =
@@ -827,24 +827,20 @@ hipError_t launch_skinny_fwd(const SkinnyPlan& p, const uint8_t* codes, const fl
     return hipGetLastError();
 }
 
-template <int TB>
+template <int TB, bool kThree>
 void launch_bwd_rb(int rb, dim3 grid, const uint16_t* dy, const uint8_t* codes, const float* absmax,
                    const uint16_t* B, const float* u, int64_t T, int64_t N, int64_t K, int r, float s,
                    int steps_per_split, int dx_cols, int dx_total, int gsteps, int gblocks, int dblocks, float* dxpart,
                    float* gpart, float* dB, hipStream_t stream) {
+    auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, dy, codes, absmax, B, u, int(T), int(N), int(K), r, s,
+                           steps_per_split, dx_cols, dx_total, gsteps, gblocks, dblocks, dxpart, gpart, dB, tables());
+    };
     switch (rb) {
-        case 1: hipLaunchKernelGGL((k_skinny_bwd<1, TB>), grid, dim3(kThreads), 0, stream, dy, codes, absmax, B, u,
-                                   int(T), int(N), int(K), r, s, steps_per_split, dx_cols, dx_total, gsteps, gblocks,
-                                   dblocks, dxpart, gpart, dB, tables()); break;
-        case 2: hipLaunchKernelGGL((k_skinny_bwd<2, TB>), grid, dim3(kThreads), 0, stream, dy, codes, absmax, B, u,
-                                   int(T), int(N), int(K), r, s, steps_per_split, dx_cols, dx_total, gsteps, gblocks,
-                                   dblocks, dxpart, gpart, dB, tables()); break;
-        case 3: hipLaunchKernelGGL((k_skinny_bwd<3, TB>), grid, dim3(kThreads), 0, stream, dy, codes, absmax, B, u,
-                                   int(T), int(N), int(K), r, s, steps_per_split, dx_cols, dx_total, gsteps, gblocks,
-                                   dblocks, dxpart, gpart, dB, tables()); break;
-        default: hipLaunchKernelGGL((k_skinny_bwd<4, TB>), grid, dim3(kThreads), 0, stream, dy, codes, absmax, B, u,
-                                    int(T), int(N), int(K), r, s, steps_per_split, dx_cols, dx_total, gsteps, gblocks,
-                                    dblocks, dxpart, gpart, dB, tables()); break;
+        case 1: launch(k_skinny_bwd<1, TB, kThree>); break;
+        case 2: launch(k_skinny_bwd<2, TB, kThree>); break;
+        case 3: launch(k_skinny_bwd<3, TB, kThree>); break;
+        default: launch(k_skinny_bwd<4, TB, kThree>); break;
     }
 }
 
@@ -866,12 +862,10 @@ hipError_t launch_skinny_bwd(const SkinnyPlan& p, const BwdPlan& bp, const uint8
         const dim3 grid(unsigned(dx_total + gblocks + dblocks));
         if (dx) prof_gemm_begin(stream);
         const int rb = std::max(1, (r + 15) / 16);
-        if (T <= 16)
-            launch_bwd_rb<1>(rb, grid, dy, codes, absmax, B, u, T, N, K, r, s, p.steps_per_split, dx_cols, dx_total,
-                             bp.gsteps, gblocks, dblocks, dxpart, gpart, dB, stream);
-        else
-            launch_bwd_rb<2>(rb, grid, dy, codes, absmax, B, u, T, N, K, r, s, p.steps_per_split, dx_cols, dx_total,
-                             bp.gsteps, gblocks, dblocks, dxpart, gpart, dB, stream);
+        const auto launch = T <= 16 ? (x.codes ? launch_bwd_rb<1, true> : launch_bwd_rb<1, false>)
+                                    : (x.codes ? launch_bwd_rb<2, true> : launch_bwd_rb<2, false>);
+        launch(rb, grid, dy, codes, absmax, B, u, T, N, K, r, s, p.steps_per_split, dx_cols, dx_total, bp.gsteps, gblocks,
+               dblocks, dxpart, gpart, dB, stream);
         if (dx) prof_gemm_end(stream);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;

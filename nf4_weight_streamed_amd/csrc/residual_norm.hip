@@ -25,36 +25,68 @@ namespace {
 constexpr int64_t kMaxWidth = 16384;
 constexpr int64_t kMaxGrid = int64_t(1) << 21;  // workgroups; rows past it are looped over
 
-// Eight elements of a row from column `at` on; zeros past its end. kRagged: rows that are no
-// whole number of 16-byte pieces, or not aligned to them.
+// A row belongs to a wave (kWave: widths up to 512, four rows a workgroup) or to a workgroup of as
+// many waves as its octets need at N octets a thread: octet n of thread t is at column 8 (n TR + t).
+template <bool kWave>
+struct Place {
+    int t, TR, first, step;  // the thread within its row's TR; the first row and the step to the next
+    __device__ __forceinline__ Place()
+        : t(kWave ? threadIdx.x & 63 : threadIdx.x), TR(kWave ? 64 : blockDim.x),
+          first(kWave ? __builtin_amdgcn_readfirstlane(int(blockIdx.x) * 4 + (threadIdx.x >> 6)) : blockIdx.x),
+          step(gridDim.x * (kWave ? 4 : 1)) {}
+    __device__ __forceinline__ int at(int n) const { return 8 * (n * TR + t); }
+};
+
+// A thread's octets of one row, zeros past its end. Rows of whole, aligned 16-byte pieces go through
+// a descriptor over the row, which also stands for an absent tensor (p NULL: zeros, nothing stored)
+// without a branch, so that the loads of a row are issued back to back. kRagged: any others.
 struct __attribute__((packed, aligned(2))) LooseOctet {
     u32x4 w;
 };
 
-template <bool kRagged>
-__device__ __forceinline__ u32x4 load_octet(const uint16_t* row, int at, int H) {
-    if constexpr (!kRagged) return at < H ? *reinterpret_cast<const u32x4*>(row + at) : u32x4{0, 0, 0, 0};
-    if (at + 8 <= H) return reinterpret_cast<const LooseOctet*>(row + at)->w;
-    u32x4 x = {0, 0, 0, 0};
+template <bool kRagged, int N, bool kWave>
+__device__ __forceinline__ void load_line(const uint16_t* p, int64_t base, int H, const Place<kWave>& pl, u32x4 (&x)[N]) {
+    if constexpr (!kRagged) {
+        const auto r = make_rsrc(p ? p + base : nullptr, p ? uint32_t(H) * 2u : 0u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (at + e < H) x[e / 2] |= uint32_t(row[at + e]) << (16 * (e % 2));
-    return x;
+        for (int n = 0; n < N; ++n) x[n] = buf_load16(r, uint32_t(pl.at(n)) * 2u);
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = pl.at(n);
+            x[n] = u32x4{0, 0, 0, 0};
+            if (!p) continue;
+            if (at + 8 <= H) {
+                x[n] = reinterpret_cast<const LooseOctet*>(p + base + at)->w;
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e < H) x[n][e / 2] |= uint32_t(p[base + at + e]) << (16 * (e % 2));
+        }
+    }
 }
 
-template <bool kRagged>
-__device__ __forceinline__ void store_octet(uint16_t* row, int at, int H, u32x4 x) {
+template <bool kRagged, int N, bool kWave>
+__device__ __forceinline__ void store_line(uint16_t* p, int64_t base, int H, const Place<kWave>& pl, const u32x4 (&x)[N]) {
     if constexpr (!kRagged) {
-        if (at < H) *reinterpret_cast<u32x4*>(row + at) = x;
-        return;
-    }
-    if (at + 8 <= H) {
-        reinterpret_cast<LooseOctet*>(row + at)->w = x;
-        return;
-    }
+        const auto r = make_rsrc(p ? p + base : nullptr, p ? uint32_t(H) * 2u : 0u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (at + e < H) row[at + e] = uint16_t(x[e / 2] >> (16 * (e % 2)));
+        for (int n = 0; n < N; ++n) __builtin_amdgcn_raw_buffer_store_b128(x[n], r, pl.at(n) * 2, 0, 0);
+    } else {
+        if (!p) return;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int at = pl.at(n);
+            if (at + 8 <= H) {
+                reinterpret_cast<LooseOctet*>(p + base + at)->w = x[n];
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (at + e < H) p[base + at + e] = uint16_t(x[n][e / 2] >> (16 * (e % 2)));
+        }
+    }
 }
 
 __device__ __forceinline__ float lane_sum(float v) {
@@ -71,112 +103,121 @@ __device__ __forceinline__ float lane_sum(float v) {
     return __uint_as_float(y[0]) + __uint_as_float(y[1]);
 }
 
-// Sum over the TR threads of a row, in a fixed order. Two slots taken in turn need one barrier
-// a sum: whoever writes a slot again has met the barrier that followed its last reads.
-template <int TR>
+// Threads of a workgroup by the widths it takes: 256, a wave a row, up to 512 elements; up to 512, a row
+// of at most 8192; up to 1024 for wider ones.
+constexpr int kWaveRows = 256, kRows = 512, kWideRows = 1024;
+constexpr int kMaxWaves = 16;  // of a workgroup
+
+// Sum over a row's threads - a wave's lanes, or the whole workgroup - in a fixed order. Two slots
+// taken in turn need one barrier a sum: whoever writes a slot again has met the barrier that
+// followed its last reads.
+template <bool kWave>
 struct RowSum {
-    float (&slots)[2][16];
+    float (&slots)[2][kMaxWaves];
     int turn = 0;
+    __device__ __forceinline__ explicit RowSum(float (&s)[2][kMaxWaves]) : slots(s) {
+        // places without a wave add zeros; the first sum's barrier comes before its reads
+        const int i = threadIdx.x, waves = blockDim.x >> 6;
+        if (!kWave && i < kMaxWaves && i >= waves) slots[0][i] = slots[1][i] = 0.0f;
+    }
     __device__ __forceinline__ float operator()(float v) {
         v = lane_sum(v);
-        if constexpr (TR == 64) return v;
-        float(&slot)[16] = slots[turn];
+        if constexpr (kWave) return v;
+        float(&slot)[kMaxWaves] = slots[turn];
         turn ^= 1;
         if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
         __syncthreads();
-        float s = slot[0];
+        float s = 0.0f;
 #pragma unroll
-        for (int i = 1; i < TR / 64; ++i) s += slot[i];
+        for (int i = 0; i < kMaxWaves; i += 4) s += (slot[i] + slot[i + 1]) + (slot[i + 2] + slot[i + 3]);
         return s;
     }
 };
-
-// TR threads a row, N octets a thread: octet n of thread t starts at column 8 (n TR + t).
-template <int TR>
-constexpr int kRowsOf = TR < 256 ? 256 / TR : 1;  // rows of a workgroup
-template <int TR>
-constexpr int kBlock = TR < 256 ? 256 : TR;
 
 struct FwdArgs {
     const uint16_t *h, *o, *post_gain, *gate, *gain;
     uint16_t *h_out, *n;
     uint8_t* codes;
     float *n_scale, *rstd_o, *rstd;
-    int64_t T;
-    int H, post, gate_kind;
+    int T, H, gate_kind;
     float scale, offset, eps;
 };
 
-// factor of column at + e: 1 without a gain
-template <bool kRagged>
-__device__ __forceinline__ void gain_octet(const uint16_t* gain, float offset, int at, int H, float (&f)[8]) {
-    if (!gain) {
+// A gain's factors, 1 without one.
+__device__ __forceinline__ void gain_octet(bool has, u32x4 w, float offset, float (&f)[8]) {
+    unpack_octet(w, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 1.0f;
-        return;
-    }
-    unpack_octet(load_octet<kRagged>(gain, at, H), f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] += offset;
+    for (int e = 0; e < 8; ++e) f[e] = has ? f[e] + offset : 1.0f;
 }
 
-template <int TR, int N, bool kRagged>
-__global__ __launch_bounds__(kBlock<TR>) void k_residual_norm_fwd(FwdArgs a) {
-    constexpr int R = kRowsOf<TR>;
-    __shared__ float slots[2][16];
-    RowSum<TR> row_sum{slots};
-    const int t = threadIdx.x % TR, H = a.H;
+// kBlock: 0 the norm alone, 1 a block's output joins, 2 it is normalised first. With many rows a
+// workgroup takes several, the next one's loads under way while a row is reduced.
+template <int N, bool kRagged, int kThreads, int kBlock>
+__global__ __launch_bounds__(kThreads) void k_residual_norm_fwd(FwdArgs a) {
+    constexpr bool kWave = kThreads == kWaveRows;
+    constexpr bool kAhead = kBlock > 1;
+    __shared__ float slots[2][kMaxWaves];
+    RowSum<kWave> row_sum(slots);
+    const Place<kWave> p;
+    const int H = a.H;
     const float mean = 1.0f / float(H);
-    for (int64_t row = int64_t(blockIdx.x) * R + threadIdx.x / TR; row < a.T; row += int64_t(gridDim.x) * R) {
-        const int64_t base = row * H;
-        u32x4 hw[N], ow[N], gw[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) hw[n] = load_octet<kRagged>(a.h + base, 8 * (n * TR + t), H);
-        if (a.o) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) ow[n] = load_octet<kRagged>(a.o + base, 8 * (n * TR + t), H);
-            if (a.gate_kind != NF4_GATE_NONE) {
-                const uint16_t* g = a.gate + (a.gate_kind == NF4_GATE_TOKEN ? base : 0);
-#pragma unroll
-                for (int n = 0; n < N; ++n) gw[n] = load_octet<kRagged>(g, 8 * (n * TR + t), H);
-            }
-        }
+    struct {
+        u32x4 o[kBlock ? N : 1], h[N], gate[kBlock ? N : 1];
+    } next;
+    auto load = [&](int row) {  // in the order of their use
+        const int64_t base = int64_t(row) * H;
+        if constexpr (kBlock > 0) load_line<kRagged>(a.o, base, H, p, next.o);
+        load_line<kRagged>(a.h, base, H, p, next.h);
+        if constexpr (kBlock > 0) load_line<kRagged>(a.gate, a.gate_kind == NF4_GATE_TOKEN ? base : 0, H, p, next.gate);
+    };
+    u32x4 fw[N], pw[kBlock > 1 ? N : 1];  // the same for all rows
+    if (p.first < a.T) load(p.first);
+    if constexpr (kBlock > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw);
+    load_line<kRagged>(a.gain, 0, H, p, fw);
+    for (int row = p.first; row < a.T; row += p.step) {
+        const int64_t base = int64_t(row) * H;
+        if (!kAhead && row != p.first) load(row);
+        const auto in = next;
+        u32x4 out[N];
+        if (kAhead && row + p.step < a.T) load(row + p.step);
         float s[N][8];
-#pragma unroll
-        for (int n = 0; n < N; ++n) unpack_octet(hw[n], s[n]);
-        if (a.o) {
+        if constexpr (kBlock > 0) {
             float r = 1.0f;
-            if (a.post) {
+            if constexpr (kBlock > 1) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int n = 0; n < N; ++n) {
                     float v[8];
-                    unpack_octet(ow[n], v);
+                    unpack_octet(in.o[n], v);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(v[e], v[e], ss);
                 }
                 r = 1.0f / sqrtf(row_sum(ss) * mean + a.eps);
-                if (t == 0) a.rstd_o[row] = r;
+                if (p.t == 0) a.rstd_o[row] = r;
             }
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                const int at = 8 * (n * TR + t);
                 float v[8], f[8];
-                unpack_octet(ow[n], v);
-                if (a.post) {
-                    gain_octet<kRagged>(a.post_gain, a.offset, at, H, f);
+                unpack_octet(in.h[n], s[n]);
+                unpack_octet(in.o[n], v);
+                if constexpr (kBlock > 1) {
+                    gain_octet(a.post_gain != nullptr, pw[n], a.offset, f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] = v[e] * r * f[e];
                 }
                 if (a.gate_kind != NF4_GATE_NONE) {
-                    unpack_octet(gw[n], f);
+                    unpack_octet(in.gate[n], f);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) v[e] *= f[e];
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) s[n][e] = __builtin_fmaf(a.scale, v[e], s[n][e]);
-                store_octet<kRagged>(a.h_out + base, at, H, pack_octet(s[n]));
+                out[n] = pack_octet(s[n]);
             }
+            store_line<kRagged>(a.h_out, base, H, p, out);
+        } else {
+#pragma unroll
+            for (int n = 0; n < N; ++n) unpack_octet(in.h[n], s[n]);
         }
         float ss = 0.0f;
 #pragma unroll
@@ -184,20 +225,24 @@ __global__ __launch_bounds__(kBlock<TR>) void k_residual_norm_fwd(FwdArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(s[n][e], s[n][e], ss);
         const float r = 1.0f / sqrtf(row_sum(ss) * mean + a.eps);
-        if (t == 0) a.rstd[row] = r;
+        if (p.t == 0) a.rstd[row] = r;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int at = 8 * (n * TR + t);
             float f[8];
-            gain_octet<kRagged>(a.gain, a.offset, at, H, f);
+            gain_octet(a.gain != nullptr, fw[n], a.offset, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] *= s[n][e] * r;
-            const u32x4 w = pack_octet(f);
-            store_octet<kRagged>(a.n + base, at, H, w);
-            if (a.codes && at < H) {  // H % 64 == 0: the 8 lanes of a block are all in or all out
+            out[n] = pack_octet(f);
+        }
+        store_line<kRagged>(a.n, base, H, p, out);
+        if (a.codes) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int at = p.at(n);
+                if (at >= H) continue;  // H % 64 == 0: the 8 lanes of a block are all in or all out
                 float step;
-                *reinterpret_cast<u32x2*>(a.codes + base + at) = act8_quantize8(w, step);
-                if ((t & 7) == 0) a.n_scale[(base + at) >> 6] = step;
+                *reinterpret_cast<u32x2*>(a.codes + base + at) = act8_quantize8(out[n], step);
+                if ((p.t & 7) == 0) a.n_scale[(base + at) >> 6] = step;
             }
         }
     }
@@ -210,90 +255,124 @@ struct BwdArgs {
     uint16_t *dh, *d_o, *dgate_rows;
     float* part;  // [workgroups][dgain, dpost_gain, dgate][H]; which are wanted:
     int sums;     // bit 0, 1, 2
-    int64_t T;
-    int H, n_dn, post, gate_kind;
+    int T, H, n_dn, gate_kind;
     float scale, offset;
 };
 
-// kSums: sums over rows are wanted; a workgroup then takes every gridDim-th row.
-template <int TR, int N, bool kRagged, bool kSums>
-__global__ __launch_bounds__(kBlock<TR>) void k_residual_norm_bwd(BwdArgs a) {
-    constexpr int R = kRowsOf<TR>;
-    static_assert(!kSums || R == 1, "the columns of a thread are one row's");
-    __shared__ float slots[2][16];
-    RowSum<TR> row_sum{slots};
-    const int t = threadIdx.x % TR, H = a.H;
+// A row's inputs as loaded.
+template <int N, int kBranch>
+struct RowIn {
+    u32x4 d[3][N], h[N], res[N];  // h: bf16, or two dwords of codes and their scale
+    u32x4 o[kBranch ? N : 1], gate[kBranch ? N : 1];
+    float r, r_o;
+};
+
+template <int N, bool kRagged, int kBranch, bool kWave>
+__device__ __forceinline__ void load_row(const BwdArgs& a, const Place<kWave>& p, int row, RowIn<N, kBranch>& in) {
+    const int64_t base = int64_t(row) * a.H;
+    const int H = a.H;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) load_line<kRagged>(a.dn[i], base, H, p, in.d[i]);
+    if (a.codes) {
+        const auto rc = make_rsrc(a.codes + base, uint32_t(H));
+        const auto rs = make_rsrc(a.n_scale + int64_t(row) * (H / 64), uint32_t(H / 64) * 4u);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const u32x2 c = buf_load8(rc, uint32_t(p.at(n)));
+            in.h[n] = u32x4{c.x, c.y, buf_load_u32(rs, uint32_t(p.at(n)) / 64 * 4u), 0};
+        }
+    } else {
+        load_line<kRagged>(a.h, base, H, p, in.h);
+    }
+    in.r = a.rstd[row];
+    load_line<kRagged>(a.dres, base, H, p, in.res);
+    if constexpr (kBranch > 0) {
+        load_line<kRagged>(a.o, base, H, p, in.o);
+        load_line<kRagged>(a.gate, a.gate_kind == NF4_GATE_TOKEN ? base : 0, H, p, in.gate);
+        in.r_o = kBranch > 1 ? a.rstd_o[row] : 1.0f;
+    }
+}
+
+// kBranch: gradients of the block's side are wanted, 2 with its norm. kSums: sums over rows are; a
+// workgroup then takes many rows, and the next row's loads are under way while a row is reduced.
+template <int N, bool kRagged, int kThreads, int kBranch, bool kSums>
+__global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
+    constexpr bool kWave = kThreads == kWaveRows, kWide = kThreads == kWideRows;
+    constexpr bool kAhead = (kSums || kBranch > 1) && !kWide;
+    constexpr int kKinds = !kSums ? 1 : kBranch ? 3 : 1;
+    __shared__ float slots[2][kMaxWaves];
+    RowSum<kWave> row_sum(slots);
+    const Place<kWave> p;
+    const int H = a.H;
     const float mean = 1.0f / float(H);
-    float acc[kSums ? 3 : 1][N][8];
+    // the sums over rows: dgain, and with a branch dpost_gain and dgate. At four octets a thread the
+    // latter two are kept in LDS (in registers, which they overflow, 4096 rows of 16384 took 792 us)
+    constexpr bool kInLds = kKinds > 1 && kWide;
+    constexpr int kHeld = kInLds ? 1 : kKinds;
+    float acc[kHeld][N][8];
+    __shared__ f32x4 wide[kInLds ? 2 * N * 2 * kThreads : 1];  // [kind][octet][half][thread]
+    auto wide_at = [&](int kind, int n, int half) -> f32x4& {
+        return wide[(((kind - 1) * N + n) * 2 + half) * kThreads + threadIdx.x];
+    };
+    auto add = [&](int kind, int n, const float (&x)[8]) {
+        if constexpr (kInLds) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                wide_at(kind, n, half) += f32x4{x[4 * half], x[4 * half + 1], x[4 * half + 2], x[4 * half + 3]};
+        } else if constexpr (kSums) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[kind][n][e] += x[e];
+        }
+    };
     if constexpr (kSums) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
+        for (int n = 0; n < N; ++n) {
 #pragma unroll
-            for (int n = 0; n < N; ++n)
+            for (int i = 0; i < kHeld; ++i)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[i][n][e] = 0.0f;
-    }
-    for (int64_t row = int64_t(blockIdx.x) * R + threadIdx.x / TR; row < a.T; row += int64_t(gridDim.x) * R) {
-        const int64_t base = row * H;
-        u32x4 dw[N], rw[N], ow[N], gw[N], hw[N];
-        u32x2 cw[N];
-        float cs[N];
-        float g[N][8], b[N][8];
+            if constexpr (kInLds) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) dw[n] = load_octet<kRagged>(a.dn[0] + base, 8 * (n * TR + t), H);
-        if (a.codes) {
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                const int at = 8 * (n * TR + t);
-                cw[n] = at < H ? *reinterpret_cast<const u32x2*>(a.codes + base + at) : u32x2{0, 0};
-                cs[n] = at < H ? a.n_scale[(base + at) >> 6] : 0.0f;
+                for (int i = 0; i < 4; ++i) wide_at(1 + i / 2, n, i % 2) = f32x4{0, 0, 0, 0};
             }
-        } else {
-#pragma unroll
-            for (int n = 0; n < N; ++n) hw[n] = load_octet<kRagged>(a.h + base, 8 * (n * TR + t), H);
         }
-        if (a.dres) {
+    }
+    RowIn<N, kBranch> next;
+    u32x4 fw[N], pw[kBranch > 1 ? N : 1];  // the same for all rows
+    if (p.first < a.T) load_row<N, kRagged>(a, p, p.first, next);
+    load_line<kRagged>(a.gain, 0, H, p, fw);
+    if constexpr (kBranch > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw);
+    for (int row = p.first; row < a.T; row += p.step) {
+        const int64_t base = int64_t(row) * H;
+        if (!kAhead && row != p.first) load_row<N, kRagged>(a, p, row, next);
+        const RowIn<N, kBranch> in = next;
+        float g[N][8], b[N][8];
+        u32x4 out[N];
 #pragma unroll
-            for (int n = 0; n < N; ++n) rw[n] = load_octet<kRagged>(a.dres + base, 8 * (n * TR + t), H);
-        }
-        if (a.o) {
+        for (int n = 0; n < N; ++n) {
+            float d[8];
+            unpack_octet(in.d[0][n], g[n]);
 #pragma unroll
-            for (int n = 0; n < N; ++n) ow[n] = load_octet<kRagged>(a.o + base, 8 * (n * TR + t), H);
-        }
-        if (a.gate_kind != NF4_GATE_NONE) {
-            const uint16_t* gate = a.gate + (a.gate_kind == NF4_GATE_TOKEN ? base : 0);
-#pragma unroll
-            for (int n = 0; n < N; ++n) gw[n] = load_octet<kRagged>(gate, 8 * (n * TR + t), H);
-        }
-        const float r = a.rstd[row], r_o = a.post ? a.rstd_o[row] : 1.0f;
-#pragma unroll
-        for (int n = 0; n < N; ++n) unpack_octet(dw[n], g[n]);
-        for (int i = 1; i < a.n_dn; ++i) {
-            const uint16_t* more = (i == 1 ? a.dn[1] : a.dn[2]) + base;
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                float d[8];
-                unpack_octet(load_octet<kRagged>(more, 8 * (n * TR + t), H), d);
+            for (int i = 1; i < 3; ++i) {
+                if (i >= a.n_dn) continue;
+                unpack_octet(in.d[i][n], d);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[n][e] += d[e];
             }
-        }
-        if (a.codes) {
+            if (a.codes) {
+                act8_values8(u32x2{in.h[n][0], in.h[n][1]}, __uint_as_float(in.h[n][2]), b[n]);
+            } else {
+                unpack_octet(in.h[n], b[n]);
 #pragma unroll
-            for (int n = 0; n < N; ++n) act8_values8(cw[n], cs[n], b[n]);
-        } else {
-#pragma unroll
-            for (int n = 0; n < N; ++n) {
-                unpack_octet(hw[n], b[n]);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) b[n][e] *= r;
+                for (int e = 0; e < 8; ++e) b[n][e] *= in.r;
             }
         }
+        if (kAhead && row + p.step < a.T) load_row<N, kRagged>(a, p, row + p.step, next);
         float dot = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float f[8];
-            gain_octet<kRagged>(a.gain, a.offset, 8 * (n * TR + t), H, f);
+            gain_octet(a.gain != nullptr, fw[n], a.offset, f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if constexpr (kSums) acc[0][n][e] = __builtin_fmaf(g[n][e], b[n][e], acc[0][n][e]);
@@ -305,79 +384,95 @@ __global__ __launch_bounds__(kBlock<TR>) void k_residual_norm_bwd(BwdArgs a) {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             float d[8];
-            if (a.dres) {
-                unpack_octet(rw[n], d);
-            } else {
+            unpack_octet(in.res[n], d);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[n][e] = __builtin_fmaf(r, __builtin_fmaf(-b[n][e], c, g[n][e]), d[e]);  // ds
-            store_octet<kRagged>(a.dh + base, 8 * (n * TR + t), H, pack_octet(g[n]));
+            for (int e = 0; e < 8; ++e) g[n][e] = __builtin_fmaf(in.r, __builtin_fmaf(-b[n][e], c, g[n][e]), d[e]);  // ds
+            out[n] = pack_octet(g[n]);
         }
-        if (!a.d_o && !a.dgate_rows && !(kSums && (a.sums & 6))) continue;  // uniform
-        // from here on g is dv, and b is u
-        dot = 0.0f;
+        store_line<kRagged>(a.dh, base, H, p, out);
+        if constexpr (kBranch > 0) {
+            // from here on g is dv, and b is u
+            dot = 0.0f;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int at = 8 * (n * TR + t);
-            float f[8], gate[8];
-            if (a.o) {
-                unpack_octet(ow[n], b[n]);
+            for (int n = 0; n < N; ++n) {
+                float f[8], x[8];
+                unpack_octet(in.o[n], b[n]);
+                if constexpr (kBranch > 1) {
+                    gain_octet(a.post_gain != nullptr, pw[n], a.offset, f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) b[n][e] *= r_o;
-            }
-            if (a.post) gain_octet<kRagged>(a.post_gain, a.offset, at, H, f);
+                    for (int e = 0; e < 8; ++e) b[n][e] *= in.r_o;
+                }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[n][e] *= a.scale;
-            if (a.gate_kind != NF4_GATE_NONE) {
-                unpack_octet(gw[n], gate);
-                if (a.dgate_rows || (kSums && (a.sums & 4))) {
-                    float x[8];
+                for (int e = 0; e < 8; ++e) g[n][e] *= a.scale;
+                if (a.gate_kind != NF4_GATE_NONE) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = g[n][e] * (a.post ? b[n][e] * f[e] : b[n][e]);
-                    if (a.dgate_rows) store_octet<kRagged>(a.dgate_rows + base, at, H, pack_octet(x));
-                    if constexpr (kSums) {
+                    for (int e = 0; e < 8; ++e) x[e] = g[n][e] * (kBranch > 1 ? b[n][e] * f[e] : b[n][e]);
+                    if constexpr (kSums) add(2, n, x);
+                    out[n] = pack_octet(x);
+                    unpack_octet(in.gate[n], x);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[2][n][e] += x[e];
+                    for (int e = 0; e < 8; ++e) g[n][e] *= x[e];
+                }
+                if constexpr (kBranch > 1) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = g[n][e] * b[n][e];
+                    if constexpr (kSums) add(1, n, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        g[n][e] *= f[e];
+                        dot = __builtin_fmaf(g[n][e], b[n][e], dot);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[n][e] *= gate[e];
             }
-            if (a.post) {
+            if (a.dgate_rows) store_line<kRagged>(a.dgate_rows, base, H, p, out);
+            if constexpr (kBranch > 1) {
+                const float c_o = row_sum(dot) * mean;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if constexpr (kSums) acc[1][n][e] = __builtin_fmaf(g[n][e], b[n][e], acc[1][n][e]);
-                    g[n][e] *= f[e];
-                    dot = __builtin_fmaf(g[n][e], b[n][e], dot);
-                }
+                for (int n = 0; n < N; ++n)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[n][e] = in.r_o * __builtin_fmaf(-b[n][e], c_o, g[n][e]);
             }
+#pragma unroll
+            for (int n = 0; n < N; ++n) out[n] = pack_octet(g[n]);
+            store_line<kRagged>(a.d_o, base, H, p, out);
         }
-        if (!a.d_o) continue;
-        if (a.post) {
-            const float c_o = row_sum(dot) * mean;
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) g[n][e] = r_o * __builtin_fmaf(-b[n][e], c_o, g[n][e]);
-        }
-#pragma unroll
-        for (int n = 0; n < N; ++n) store_octet<kRagged>(a.d_o + base, 8 * (n * TR + t), H, pack_octet(g[n]));
     }
     if constexpr (kSums) {
         // the partial rows are whole and aligned (pitch: octets)
         const int64_t pitch = int64_t((H + 7) / 8) * 8;
+        __shared__ float share[kWave ? 3 * 64 * 8 : 1];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kKinds; ++i) {
             if (!(a.sums >> i & 1)) continue;
-            float* p = a.part + (int64_t(blockIdx.x) * 3 + i) * pitch;
+            const int k = kInLds ? 0 : i;
+            if constexpr (kWave) {  // the workgroup's four waves, in order
+                const int wave = threadIdx.x >> 6;
+                __syncthreads();
+                if (wave > 0) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) share[((wave - 1) * 8 + e) * 64 + p.t] = acc[k][0][e];
+                }
+                __syncthreads();
+                if (wave > 0) continue;
+#pragma unroll
+                for (int w = 0; w < 3; ++w)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[k][0][e] += share[(w * 8 + e) * 64 + p.t];
+            }
+            float* q = a.part + (int64_t(blockIdx.x) * 3 + i) * pitch;
 #pragma unroll
             for (int n = 0; n < N; ++n) {
-                const int at = 8 * (n * TR + t);
+                const int at = p.at(n);
                 if (at >= H) continue;
-                *reinterpret_cast<f32x4*>(p + at) = f32x4{acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]};
-                *reinterpret_cast<f32x4*>(p + at + 4) = f32x4{acc[i][n][4], acc[i][n][5], acc[i][n][6], acc[i][n][7]};
+                if constexpr (kInLds) {
+                    if (i > 0) {
+                        *reinterpret_cast<f32x4*>(q + at) = wide_at(i, n, 0);
+                        *reinterpret_cast<f32x4*>(q + at + 4) = wide_at(i, n, 1);
+                        continue;
+                    }
+                }
+                *reinterpret_cast<f32x4*>(q + at) = f32x4{acc[k][n][0], acc[k][n][1], acc[k][n][2], acc[k][n][3]};
+                *reinterpret_cast<f32x4*>(q + at + 4) = f32x4{acc[k][n][4], acc[k][n][5], acc[k][n][6], acc[k][n][7]};
             }
         }
     }
@@ -389,15 +484,16 @@ struct SumArgs {
     int groups, H;
 };
 
-// out[i][column] = the workgroups' sums: 64 columns a workgroup, its four waves a quarter of the
-// workgroups each, in order.
-__global__ __launch_bounds__(256) void k_residual_norm_sums(SumArgs a) {
-    __shared__ float share[4][64];
+// out[i][column] = the workgroups' sums: 64 columns a workgroup, each of its waves a run of the
+// workgroups, in order.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(64 * kSumWaves) void k_residual_norm_sums(SumArgs a) {
+    __shared__ float share[kSumWaves][64];
     float* out = blockIdx.y == 0 ? a.out[0] : blockIdx.y == 1 ? a.out[1] : a.out[2];
     if (!out) return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = int(blockIdx.x) * 64 + lane;
     const int64_t pitch = int64_t((a.H + 7) / 8) * 8;
-    const int g0 = int(int64_t(a.groups) * wave / 4), g1 = int(int64_t(a.groups) * (wave + 1) / 4);
+    const int g0 = a.groups * wave / kSumWaves, g1 = a.groups * (wave + 1) / kSumWaves;
     float s = 0.0f;
     if (col < a.H) {
         const float* p = a.part + int64_t(blockIdx.y) * pitch + col;
@@ -406,33 +502,32 @@ __global__ __launch_bounds__(256) void k_residual_norm_sums(SumArgs a) {
     }
     share[wave][lane] = s;
     __syncthreads();
-    if (wave == 0 && col < a.H) out[col] = ((share[0][lane] + share[1][lane]) + share[2][lane]) + share[3][lane];
+    if (wave > 0 || col >= a.H) return;
+#pragma unroll
+    for (int w = 1; w < kSumWaves; ++w) s += share[w][lane];
+    out[col] = s;
 }
 
-// Threads a row and octets a thread.
 struct Split {
-    int threads, octets;
+    int octets, kind, threads;  // octets a thread; kWaveRows, kRows or kWideRows; the workgroup's threads
 };
 
 Split split_of(int64_t H) {
-    if (H <= 512) return {64, 1};
-    if (H <= 2048) return {256, 1};
-    if (H <= 4096) return {256, 2};
-    if (H <= 8192) return {256, 4};
-    return {1024, 2};
+    const int64_t all = cdiv(H, 8);
+    if (all <= 64) return {1, kWaveRows, 256};
+    const int n = all <= 512 ? 1 : 2;
+    return {n, all <= 1024 ? kRows : kWideRows, int(cdiv(cdiv(all, n), 64) * 64)};
 }
 
-// With sums over rows a thread holds three more values a column.
-Split split_of_sums(int64_t H) {
-    if (H <= 2048) return {256, 1};
-    if (H <= 4096) return {512, 1};
-    if (H <= 8192) return {1024, 1};
-    return {1024, 2};
-}
-
+// Workgroups that sum over rows: eight waves a CU (at least one workgroup), which the next row's loads
+// keep busy; more only add to the shares that the second kernel reads (8192 rows of 1024, gains and a
+// gate a token: 4, 8, 16, 32 waves 45.7, 42.7, 49.9, 56.2 us). Two rows a workgroup at least once
+// there are 128 of them.
 int64_t sum_groups(int64_t T, int64_t H) {
-    const int64_t most = 262144 / split_of_sums(H).threads;  // half of what the card holds at once
-    return std::min(T, most);
+    const Split p = split_of(H);
+    const int64_t rows = p.kind == kWaveRows ? 4 : 1;
+    const int64_t most = kChipCUs * std::max(1, 512 / p.threads);
+    return std::min(std::max<int64_t>(cdiv(T, rows * 2), std::min<int64_t>(cdiv(T, rows), 128)), most);
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -488,22 +583,39 @@ struct Buffers {
     }
 };
 
-template <int TR, int N>
-void launch_fwd(const FwdArgs& a, bool ragged, hipStream_t s) {
-    const dim3 grid(unsigned(std::min(cdiv(a.T, kRowsOf<TR>), kMaxGrid)));
-    if (ragged)
-        hipLaunchKernelGGL((k_residual_norm_fwd<TR, N, true>), grid, dim3(kBlock<TR>), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_residual_norm_fwd<TR, N, false>), grid, dim3(kBlock<TR>), 0, s, a);
+// kernel<octets a thread, ragged, kind of rows>, picked by width and alignment.
+template <template <int, bool, int> class Kernel, typename Args>
+void launch(const Args& a, int64_t H, bool ragged, unsigned grid, hipStream_t s) {
+    const Split p = split_of(H);
+    const auto kernel =
+        p.kind == kWaveRows   ? (ragged ? Kernel<1, true, kWaveRows>::get() : Kernel<1, false, kWaveRows>::get())
+        : p.kind == kWideRows ? (ragged ? Kernel<2, true, kWideRows>::get() : Kernel<2, false, kWideRows>::get())
+        : p.octets == 1       ? (ragged ? Kernel<1, true, kRows>::get() : Kernel<1, false, kRows>::get())
+                              : (ragged ? Kernel<2, true, kRows>::get() : Kernel<2, false, kRows>::get());
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(p.threads), 0, s, a);
 }
 
-template <int TR, int N, bool kSums>
-void launch_bwd(const BwdArgs& a, int64_t groups, bool ragged, hipStream_t s) {
-    const dim3 grid(unsigned(kSums ? groups : std::min(cdiv(a.T, kRowsOf<TR>), kMaxGrid)));
-    if (ragged)
-        hipLaunchKernelGGL((k_residual_norm_bwd<TR, N, true, kSums>), grid, dim3(kBlock<TR>), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_residual_norm_bwd<TR, N, false, kSums>), grid, dim3(kBlock<TR>), 0, s, a);
+template <int kBlock>
+struct Fwd {
+    template <int N, bool kRagged, int kThreads>
+    struct Kernel {
+        static auto get() { return k_residual_norm_fwd<N, kRagged, kThreads, kBlock>; }
+    };
+};
+
+template <int kBranch, bool kSums>
+struct Bwd {
+    template <int N, bool kRagged, int kThreads>
+    struct Kernel {
+        static auto get() { return k_residual_norm_bwd<N, kRagged, kThreads, kBranch, kSums>; }
+    };
+};
+
+// Workgroups of a row, or of four rows of a wave each. loop: as many as the card holds.
+unsigned rows_grid(int64_t T, int64_t H, bool loop) {
+    const Split p = split_of(H);
+    const int64_t most = loop ? (p.octets == 2 ? 131072 : 262144) / std::min(p.threads, kRows) : kMaxGrid;
+    return unsigned(std::min(cdiv(T, p.kind == kWaveRows ? 4 : 1), most));
 }
 
 }  // namespace
@@ -543,16 +655,16 @@ extern "C" int nf4_residual_norm_fwd(const uint16_t* h, const uint16_t* o, int64
     for (const void* p : {(const void*)h, (const void*)o, (const void*)post_gain, (const void*)gate, (const void*)gain,
                           (const void*)h_out, (const void*)n})
         ragged = ragged || !aligned(p, 16);
-    const FwdArgs a{h, o, post_gain, gate, gain, h_out, n, n_codes, n_scale, rstd_o, rstd, T, int(H), post_norm, gate_kind,
+    const FwdArgs a{h, o, post_gain, gate, gain, h_out, n, n_codes, n_scale, rstd_o, rstd, int(T), int(H), gate_kind,
                     scale, gain_offset, eps};
     hipStream_t s = static_cast<hipStream_t>(stream);
-    switch (const Split p = split_of(H); p.threads * 8 + p.octets) {
-        case 64 * 8 + 1: launch_fwd<64, 1>(a, ragged, s); break;
-        case 256 * 8 + 1: launch_fwd<256, 1>(a, ragged, s); break;
-        case 256 * 8 + 2: launch_fwd<256, 2>(a, ragged, s); break;
-        case 256 * 8 + 4: launch_fwd<256, 4>(a, ragged, s); break;
-        default: launch_fwd<1024, 2>(a, ragged, s); break;
-    }
+    const unsigned grid = rows_grid(T, H, post_norm && !ragged);
+    if (!o)
+        launch<Fwd<0>::Kernel>(a, H, ragged, grid, s);
+    else if (!post_norm)
+        launch<Fwd<1>::Kernel>(a, H, ragged, grid, s);
+    else
+        launch<Fwd<2>::Kernel>(a, H, ragged, grid, s);
     return check_launch(fn);
 }
 
@@ -622,29 +734,30 @@ extern "C" int nf4_residual_norm_bwd(const uint16_t* const* dn, int n_dn, const 
     a.o = need_o ? o : nullptr, a.rstd_o = rstd_o, a.dh = dh, a.d_o = d_o, a.part = static_cast<float*>(ws), a.sums = sums;
     a.dgate_rows = channel ? nullptr : static_cast<uint16_t*>(dgate);
     // the branch's gate is not read where nothing of the branch is wanted
-    a.gate_kind = branch ? gate_kind : NF4_GATE_NONE, a.gate = gate, a.post = branch && post_norm, a.T = T, a.H = int(H);
+    a.gate_kind = branch ? gate_kind : NF4_GATE_NONE, a.gate = gate, a.T = int(T), a.H = int(H);
     a.n_dn = n_dn, a.scale = scale, a.offset = gain_offset;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t groups = T > 0 ? sum_groups(T, H) : 0;
+    const unsigned grid = sums ? unsigned(groups) : rows_grid(T, H, branch && post_norm && !ragged);
+    const int kind = !branch ? 0 : post_norm ? 2 : 1;
     if (T > 0 && sums) {
-        switch (const Split p = split_of_sums(H); p.threads * 8 + p.octets) {
-            case 256 * 8 + 1: launch_bwd<256, 1, true>(a, groups, ragged, s); break;
-            case 512 * 8 + 1: launch_bwd<512, 1, true>(a, groups, ragged, s); break;
-            case 1024 * 8 + 1: launch_bwd<1024, 1, true>(a, groups, ragged, s); break;
-            default: launch_bwd<1024, 2, true>(a, groups, ragged, s); break;
-        }
+        if (kind == 0)
+            launch<Bwd<0, true>::Kernel>(a, H, ragged, grid, s);
+        else if (kind == 1)
+            launch<Bwd<1, true>::Kernel>(a, H, ragged, grid, s);
+        else
+            launch<Bwd<2, true>::Kernel>(a, H, ragged, grid, s);
     } else if (T > 0) {
-        switch (const Split p = split_of(H); p.threads * 8 + p.octets) {
-            case 64 * 8 + 1: launch_bwd<64, 1, false>(a, 0, ragged, s); break;
-            case 256 * 8 + 1: launch_bwd<256, 1, false>(a, 0, ragged, s); break;
-            case 256 * 8 + 2: launch_bwd<256, 2, false>(a, 0, ragged, s); break;
-            case 256 * 8 + 4: launch_bwd<256, 4, false>(a, 0, ragged, s); break;
-            default: launch_bwd<1024, 2, false>(a, 0, ragged, s); break;
-        }
+        if (kind == 0)
+            launch<Bwd<0, false>::Kernel>(a, H, ragged, grid, s);
+        else if (kind == 1)
+            launch<Bwd<1, false>::Kernel>(a, H, ragged, grid, s);
+        else
+            launch<Bwd<2, false>::Kernel>(a, H, ragged, grid, s);
     }
     if (sums) {
         const SumArgs q{a.part, {dgain, dpost_gain, channel ? static_cast<float*>(dgate) : nullptr}, int(groups), int(H)};
-        hipLaunchKernelGGL(k_residual_norm_sums, dim3(unsigned(cdiv(H, 64)), 3), dim3(256), 0, s, q);
+        hipLaunchKernelGGL(k_residual_norm_sums, dim3(unsigned(cdiv(H, 64)), 3), dim3(64 * kSumWaves), 0, s, q);
     }
     return check_launch(fn);
 }
