@@ -34,6 +34,15 @@ h'' = h' + L_down(SiLU(L_gate(h_m)) * L_up(h_m)). q and k are computed and
 receive a zero gradient. With mixing="attention" the layer is a whole decoder layer:
 a = attention(rope(q), rope(k), v), causal within each of the batch's packed sequences
 (seq_lens), and every projection receives its gradient.
+
+With checkpoints="int8" what a layer keeps for its backward is held in 8 bits where the
+backward allows it: h_a and h_m (which serve the projections' adapter gradients and the
+norms' own backward), gate and up; the down projection's input is rebuilt from the latter
+two, and no hidden state is kept. Rotated q and k, v, a and the softmax statistics stay as
+they are. The forward's residual add and norm are one pass, which normalises h' before
+its rounding to bf16 (the bf16 stack after it), so that the two forwards differ by that
+rounding; the gradients are those at the checkpoints' values. Streamed, resident and
+rematerialised runs stay bitwise equal to one another.
 """
 
 from __future__ import annotations
@@ -261,11 +270,16 @@ class NF4Stack:
     def __init__(self, base: HostNF4Base, lora: LoraParams, tokens: int, alpha: float = 32.0,
                  mode: str = "streamed", n_slots: int = 2, prefetch: bool = True, remat: bool = False,
                  layer_parts: bool = True, max_ahead: int = 2, mixing: str = "identity", seq_lens=None,
-                 rope_theta: float = 1e6):
+                 rope_theta: float = 1e6, checkpoints: str = "bf16"):
         if mode not in ("streamed", "resident"):
             raise ValueError("mode must be 'streamed' or 'resident'")
         if mixing not in ("identity", "attention"):
             raise ValueError("mixing must be 'identity' or 'attention'")
+        if checkpoints not in ("bf16", "int8"):
+            raise ValueError("checkpoints must be 'bf16' or 'int8'")
+        if checkpoints == "int8" and (base.dims.hidden % 64 or base.dims.inter % 64 or base.dims.hidden > 16384):
+            raise ValueError("checkpoints='int8' needs widths of multiples of 64 and a hidden width of at most 16384 (got "
+                             f"hidden={base.dims.hidden}, inter={base.dims.inter})")
         if seq_lens is not None and mixing == "identity":
             raise ValueError("seq_lens needs mixing='attention'")
         if seq_lens is not None:
@@ -281,6 +295,7 @@ class NF4Stack:
                                  f"query heads, and the attention's limits on tokens and sequences (got q={q}, kv={kv}, "
                                  f"head_dim={hd}, {tokens} tokens, {n} sequences)")
         self.mixing = mixing
+        self.int8 = checkpoints == "int8"
         self.base, self.lora, self.T, self.alpha = base, lora, tokens, alpha
         self.mode, self.prefetch, self.remat = mode, prefetch, remat
         # layer_parts: each layer of a block is a part of its own (copied separately,
@@ -322,20 +337,25 @@ class NF4Stack:
         # block-boundary hidden states
         n_sets = base.block_size if remat else L
         self.acts = []
-        for _ in range(n_sets + 1):
-            self.acts.append({"h": torch.empty(T, d.hidden, **bf)})
+        # with 8-bit checkpoints nothing reads a layer's input in its backward: two buffers in turn
+        streams = [torch.empty(T, d.hidden, **bf) for _ in range(2 if self.int8 else n_sets + 1)]
+        for i in range(n_sets + 1):
+            self.acts.append({"h": streams[i % len(streams)]})
         self.boundary = [torch.empty(T, d.hidden, **bf) for _ in range(base.n_blocks + 1)] if remat else None
+        passing = {"ha": d.hidden, "hm": d.hidden, "h1": d.hidden, "gate": d.inter, "up": d.inter, "m": d.inter}
         for li in range(n_sets):
             a = self.acts[li]
             a.update({
-                "ha": torch.empty(T, d.hidden, **bf), "v": torch.empty(T, d.kv, **bf), "a": torch.empty(T, d.q, **bf),
-                "h1": torch.empty(T, d.hidden, **bf), "hm": torch.empty(T, d.hidden, **bf),
-                "gate": torch.empty(T, d.inter, **bf), "up": torch.empty(T, d.inter, **bf),
-                "m": torch.empty(T, d.inter, **bf),
+                "v": torch.empty(T, d.kv, **bf), "a": torch.empty(T, d.q, **bf),
                 "rs_h": torch.empty(T, dtype=torch.float32, device=dev),
                 "rs_h1": torch.empty(T, dtype=torch.float32, device=dev),
                 "u": {name: torch.empty(T, r, dtype=torch.float32, device=dev) for name in PROJS},
             })
+            if self.int8:
+                a.update({"ha8": lib.act8_empty(T, d.hidden), "hm8": lib.act8_empty(T, d.hidden),
+                          "gate8": lib.act8_empty(T, d.inter), "up8": lib.act8_empty(T, d.inter)})
+            else:
+                a.update({n: torch.empty(T, w, **bf) for n, w in passing.items()})
             if mixing == "attention":    # rotated q and k, and the softmax statistics, for the backward
                 a.update({"q": torch.empty(T, d.q, **bf), "k": torch.empty(T, d.kv, **bf),
                           "lse": torch.empty(d.q // d.head_dim, T, dtype=torch.float32, device=dev)})
@@ -349,6 +369,10 @@ class NF4Stack:
             "dha_v": torch.empty(T, d.hidden, **bf), "dha_q": torch.empty(T, d.hidden, **bf),
             "dha_k": torch.empty(T, d.hidden, **bf), "dha": torch.empty(T, d.hidden, **bf),
         }
+        if self.int8:                    # what a layer's forward writes and only its own forward or backward reads
+            self.tmp.update({n: torch.empty(T, w, **bf) for n, w in passing.items()})
+            for n in ("dhm", "dha"):     # the norms' backward adds the projections' gradients itself
+                del self.tmp[n]
         self.seqs = {"cu": None, "n": 0}
         if mixing == "attention":
             lens = [T] if seq_lens is None else seq_lens
@@ -423,8 +447,12 @@ class NF4Stack:
 
     def activation_bytes(self) -> int:
         """Device bytes held for activations between the forward and the backward pass."""
-        n = sum(t.numel() * t.element_size() for a in self.acts for t in a.values() if isinstance(t, torch.Tensor))
-        n += sum(t.numel() * t.element_size() for a in self.acts if "u" in a for t in a["u"].values())
+        held = {}                        # by address: the 8-bit stack's hidden states share two buffers
+        for a in self.acts:
+            for t in a.values():
+                group = t.values() if isinstance(t, dict) else t if isinstance(t, lib.Act8) else (t,)
+                held.update({x.data_ptr(): x.numel() * x.element_size() for x in group})
+        n = sum(held.values())
         if self.boundary is not None:
             n += sum(t.numel() * t.element_size() for t in self.boundary)
         return n
@@ -439,48 +467,69 @@ class NF4Stack:
         lib.lora_linear_fwd(c, a, x, p[0], p[1], self.alpha, y=y, u=u, ws=self.ws_f)
 
     def _bwd(self, w, name, x, u, dy, dx):
+        """x: the projection's input, bf16 or its checkpoint."""
         p = self.lora.p[self._layer][name]
         dA, dB = self.grads[self._layer][name]
+        act8 = isinstance(x, lib.Act8)
         if self.base.dense:
-            lib.lora_linear_bwd_bf16(w[name][0], x, u, dy, p[0], p[1], self.alpha, dx=dx, dA=dA, dB=dB, ws=self.ws_b,
-                                     need_dx=dx is not None)
+            call = lib.lora_linear_bwd_bf16_act8 if act8 else lib.lora_linear_bwd_bf16
+            call(w[name][0], x, u, dy, p[0], p[1], self.alpha, dx=dx, dA=dA, dB=dB, ws=self.ws_b, need_dx=dx is not None)
             return
         c, a = w[name]
-        lib.lora_linear_bwd(c, a, x, u, dy, p[0], p[1], self.alpha, dx=dx, dA=dA, dB=dB, ws=self.ws_b,
-                            need_dx=dx is not None)
+        call = lib.lora_linear_bwd_act8 if act8 else lib.lora_linear_bwd
+        call(c, a, x, u, dy, p[0], p[1], self.alpha, dx=dx, dA=dA, dB=dB, ws=self.ws_b, need_dx=dx is not None)
 
     def _layer_forward(self, li: int, w):
         d, A, t = self.dims, self._act(li), self.tmp
         self._layer = li
-        attention = self.mixing == "attention"
+        attention, int8 = self.mixing == "attention", self.int8
         q, k = (A["q"], A["k"]) if attention else (t["q"], t["k"])
-        lib.rmsnorm_fwd(A["h"], RMS_EPS, out=A["ha"], rstd=A["rs_h"])
-        self._fwd(w, "q", A["ha"], q, A["u"]["q"])
-        self._fwd(w, "k", A["ha"], k, A["u"]["k"])
-        self._fwd(w, "v", A["ha"], A["v"], A["u"]["v"])
+        B = t if int8 else A                                              # where the forward's own tensors go
+        if int8:
+            lib.residual_norm_fwd(A["h"], eps=RMS_EPS, n=B["ha"], n8=A["ha8"], rstd=A["rs_h"])
+        else:
+            lib.rmsnorm_fwd(A["h"], RMS_EPS, out=A["ha"], rstd=A["rs_h"])
+        self._fwd(w, "q", B["ha"], q, A["u"]["q"])
+        self._fwd(w, "k", B["ha"], k, A["u"]["k"])
+        self._fwd(w, "v", B["ha"], A["v"], A["u"]["v"])
         if attention:
             lib.rope(q, k, d.head_dim, self.pos, self.inv_freq, q_out=q, k_out=k)
             lib.attn_fwd(q, k, A["v"], d.head_dim, self.seqs["cu"], o=A["a"], lse=A["lse"])
         else:
             lib.repeat_kv_fwd(A["v"], d.q, d.head_dim, out=A["a"])
         self._fwd(w, "o", A["a"], t["o"], A["u"]["o"])
-        lib.add_bf16(A["h"], t["o"], out=A["h1"])
-        lib.rmsnorm_fwd(A["h1"], RMS_EPS, out=A["hm"], rstd=A["rs_h1"])
-        self._fwd(w, "gate", A["hm"], A["gate"], A["u"]["gate"])
-        self._fwd(w, "up", A["hm"], A["up"], A["u"]["up"])
-        lib.silu_mul_fwd(A["gate"], A["up"], out=A["m"])
-        self._fwd(w, "down", A["m"], t["down"], A["u"]["down"])
-        lib.add_bf16(A["h1"], t["down"], out=self._h_out(li))
+        if int8:
+            lib.residual_norm_fwd(A["h"], t["o"], eps=RMS_EPS, h_out=B["h1"], n=B["hm"], n8=A["hm8"], rstd=A["rs_h1"])
+        else:
+            lib.add_bf16(A["h"], t["o"], out=A["h1"])
+            lib.rmsnorm_fwd(A["h1"], RMS_EPS, out=A["hm"], rstd=A["rs_h1"])
+        self._fwd(w, "gate", B["hm"], B["gate"], A["u"]["gate"])
+        self._fwd(w, "up", B["hm"], B["up"], A["u"]["up"])
+        if int8:
+            lib.silu_mul_fwd_act8(B["gate"], B["up"], out=B["m"], gate8=A["gate8"], up8=A["up8"])
+        else:
+            lib.silu_mul_fwd(A["gate"], A["up"], out=A["m"])
+        self._fwd(w, "down", B["m"], t["down"], A["u"]["down"])
+        lib.add_bf16(B["h1"], t["down"], out=self._h_out(li))
 
     def _layer_backward(self, li: int, w, dh_out, dh_in):
         d, A, t = self.dims, self._act(li), self.tmp
         self._layer = li
-        self._bwd(w, "down", A["m"], A["u"]["down"], dh_out, t["dm"])
-        lib.silu_mul_bwd(A["gate"], A["up"], t["dm"], dgate=t["dgate"], dup=t["dup"])
-        self._bwd(w, "gate", A["hm"], A["u"]["gate"], t["dgate"], t["dhm_g"])
-        self._bwd(w, "up", A["hm"], A["u"]["up"], t["dup"], t["dhm_u"])
-        lib.add_bf16(t["dhm_g"], t["dhm_u"], out=t["dhm"])
-        lib.rmsnorm_bwd(A["h1"], A["rs_h1"], t["dhm"], dres=dh_out, out=t["dh1"])
+        int8 = self.int8
+        ha, hm = (A["ha8"], A["hm8"]) if int8 else (A["ha"], A["hm"])
+        m = lib.silu_mul_act8(A["gate8"], A["up8"], out=t["m"]) if int8 else A["m"]
+        self._bwd(w, "down", m, A["u"]["down"], dh_out, t["dm"])
+        if int8:
+            lib.silu_mul_bwd_act8(A["gate8"], A["up8"], t["dm"], dgate=t["dgate"], dup=t["dup"])
+        else:
+            lib.silu_mul_bwd(A["gate"], A["up"], t["dm"], dgate=t["dgate"], dup=t["dup"])
+        self._bwd(w, "gate", hm, A["u"]["gate"], t["dgate"], t["dhm_g"])
+        self._bwd(w, "up", hm, A["u"]["up"], t["dup"], t["dhm_u"])
+        if int8:
+            lib.residual_norm_bwd((t["dhm_g"], t["dhm_u"]), A["rs_h1"], n8=hm, dres=dh_out, dh=t["dh1"])
+        else:
+            lib.add_bf16(t["dhm_g"], t["dhm_u"], out=t["dhm"])
+            lib.rmsnorm_bwd(A["h1"], A["rs_h1"], t["dhm"], dres=dh_out, out=t["dh1"])
         self._bwd(w, "o", A["a"], A["u"]["o"], t["dh1"], t["da"])
         if self.mixing == "attention":
             dq, dk = t["dq"], t["dk"]
@@ -490,11 +539,14 @@ class NF4Stack:
         else:
             lib.repeat_kv_bwd(t["da"], d.kv, d.head_dim, out=t["dv"])
             dq, dk = t["zq"], t["zkv"]                                    # identity mixing: zero gradient
-        self._bwd(w, "v", A["ha"], A["u"]["v"], t["dv"], t["dha_v"])
-        self._bwd(w, "q", A["ha"], A["u"]["q"], dq, t["dha_q"])
-        self._bwd(w, "k", A["ha"], A["u"]["k"], dk, t["dha_k"])
-        lib.add_bf16(t["dha_v"], t["dha_q"], t["dha_k"], out=t["dha"])
-        lib.rmsnorm_bwd(A["h"], A["rs_h"], t["dha"], dres=t["dh1"], out=dh_in)
+        self._bwd(w, "v", ha, A["u"]["v"], t["dv"], t["dha_v"])
+        self._bwd(w, "q", ha, A["u"]["q"], dq, t["dha_q"])
+        self._bwd(w, "k", ha, A["u"]["k"], dk, t["dha_k"])
+        if int8:
+            lib.residual_norm_bwd((t["dha_v"], t["dha_q"], t["dha_k"]), A["rs_h"], n8=ha, dres=t["dh1"], dh=dh_in)
+        else:
+            lib.add_bf16(t["dha_v"], t["dha_q"], t["dha_k"], out=t["dha"])
+            lib.rmsnorm_bwd(A["h"], A["rs_h"], t["dha"], dres=t["dh1"], out=dh_in)
 
     # ------------------------------------------------------------------ stack passes
     def _layers_of(self, b: int):

@@ -4,7 +4,8 @@ values) and of the residual add fused with the norms around a block, forward and
 TEST INFRASTRUCTURE ONLY (see ``oracle/__init__.py``): plain numpy from the definitions.
 
 Pins (tests/test_oracle_act8.py): act8_quantize by exact rational arithmetic and by its error
-bound; residual_norm_bwd and silu_mul_bwd by central finite differences of their forwards.
+bound; residual_norm_bwd and silu_mul_bwd by central finite differences of their forwards;
+decoder_backward_act8, with checkpoints that hold their values exactly, by decoder_backward.
 """
 
 from __future__ import annotations
@@ -13,9 +14,11 @@ from fractions import Fraction
 
 import numpy as np
 
-from .nf4_oracle import _as_f64, silu, silu_grad
+from .decoder_oracle import attention_bwd, rope
+from .nf4_oracle import RMS_EPS, _as_f64, _layer_f64, _lin_bwd, round_bf16, silu, silu_grad
 
-__all__ = ["act8_quantize", "act8_values", "silu_mul", "silu_mul_bwd", "residual_norm_fwd", "residual_norm_bwd"]
+__all__ = ["act8_quantize", "act8_values", "silu_mul", "silu_mul_bwd", "residual_norm_fwd", "residual_norm_bwd",
+           "decoder_backward_act8"]
 
 BLOCK = 64
 
@@ -101,3 +104,39 @@ def residual_norm_bwd(dn, rstd, b, dres=None, o=None, post_norm=False, rstd_o=No
         dv = _as_f64(rstd_o)[:, None] * (p - u * np.mean(p * u, axis=1, keepdims=True))
     out["do"] = dv
     return out
+
+
+def decoder_backward_act8(dh, layers, dims, alpha, saved, pos, inv_freq, lens=None, keep=None):
+    """decoder_backward where ha, hm, gate and up are what their 8-bit checkpoints stand for, m is
+    formed again from the latter two, and the norms go back through their own results (ha, hm) and
+    1 / rms. keep(x) gives a checkpoint's values (default: act8_quantize's)."""
+    keep = keep or (lambda x: act8_values(*act8_quantize(x)).astype(np.float64))
+    dh, d, grads = _as_f64(dh), dims.head_dim, [None] * len(layers)
+
+    def norm_back(n, h, dres, dys):
+        rstd = 1.0 / np.sqrt(np.mean(h * h, axis=1) + RMS_EPS)
+        return round_bf16(residual_norm_bwd(dys, rstd, n, dres)["dh"])
+
+    for li in range(len(layers) - 1, -1, -1):
+        p, st, g = _layer_f64(layers[li]), saved[li], {}
+        ha, hm, gate, up = (keep(st[n]) for n in ("ha", "hm", "gate", "up"))
+
+        def lin(x, name, dy):
+            dx, g[name + "_dA"], g[name + "_dB"] = _lin_bwd(x, p[name], alpha, dy)
+            return round_bf16(dx)
+
+        dm = lin(round_bf16(silu_mul(gate, up)), "down", dh)
+        dgate, dup = (round_bf16(x) for x in silu_mul_bwd(gate, up, dm))
+        dhm = [lin(round_bf16(hm), n, dy) for n, dy in (("gate", dgate), ("up", dup))]
+        dh1 = norm_back(hm, st["h1"], dh, dhm)
+        da = lin(st["a"], "o", dh1)
+        dq, dk, dv = (round_bf16(x) for x in attention_bwd(st["q"], st["k"], st["v"], st["a"], st["lse"], da, d, lens))
+        dq, dk = (round_bf16(rope(x, d, pos, inv_freq, inverse=True)) for x in (dq, dk))
+        dha = [lin(round_bf16(ha), n, dy) for n, dy in (("v", dv), ("q", dq), ("k", dk))]
+        # dB's products read u = x A^T of the forward's own x
+        for n, x, dy in (("gate", "hm", dgate), ("up", "hm", dup), ("v", "ha", dv), ("q", "ha", dq), ("k", "ha", dk),
+                         ("down", "m", dh)):
+            g[n + "_dB"] = _lin_bwd(st[x], p[n], alpha, dy)[2]
+        dh = norm_back(ha, st["h"], dh1, dha)
+        grads[li] = g
+    return dh, grads

@@ -93,3 +93,24 @@ def test_residual_norm_backward_by_differences(post, gated, gained):
         if name in p:
             d = got[grad].sum(0) if grad == "dgate" and gated == "channel" else got[grad]
             _differences(lambda v: loss(**{name: v}), p[name], d)
+
+
+def test_stack_backward_with_exact_checkpoints_is_the_plain_one():
+    """With checkpoints that keep every value, the stack's backward differs from decoder_backward's only in
+    which sums are rounded to bf16 (the projections' gradients before a norm) and in n taken for h / rms
+    (its rounding): a few steps of 2^-9 in quadrature on the way through two layers."""
+    dims = O.StackLayerDims(128, 128, 32, 256, 32)
+    rng = np.random.default_rng(6)
+    shapes = {"q": (128, 128), "k": (32, 128), "v": (32, 128), "o": (128, 128), "gate": (256, 128), "up": (256, 128),
+              "down": (128, 256)}
+    layers = [{n: (_bits(0.08 * rng.normal(size=s)), _bits(rng.normal(size=(8, s[1])) * 0.1), _bits(rng.normal(size=(s[0], 8)) * 0.05))
+               for n, s in shapes.items()} for _ in range(2)]
+    h0, dh = _bits(rng.normal(size=(9, 128))), _bits(rng.normal(size=(9, 128)))
+    pos, inv = np.arange(9), 1e6 ** (-np.arange(0, 32, 2) / 32)
+    _, saved = O.decoder_forward(h0, layers, dims, 16.0, pos, inv)
+    want, grads = O.decoder_backward(dh, layers, dims, 16.0, saved, pos, inv)
+    got, grads8 = O.decoder_backward_act8(dh, layers, dims, 16.0, saved, pos, inv, keep=lambda x: np.asarray(x, np.float64))
+    assert O.rel_l2(got, want) <= 8 * 2.0 ** -9
+    for a, b in zip(grads8, grads):
+        for key in b:
+            assert O.rel_l2(a[key], b[key]) <= 8 * 2.0 ** -9, key
