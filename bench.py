@@ -588,7 +588,8 @@ def _stack_run(torch, ST, base, lora, tokens, h0, dh, steps, **kw) -> dict:
 
 
 def stream_bench(torch, model: str, block_sizes, tokens_list, steps: int, h2d_gbs: float, base_kind: str = "nf4",
-                 slot_counts=(2,), remat: bool = True, layer_parts: bool = True, max_ahead: int = 2) -> dict:
+                 slot_counts=(2,), remat: bool = True, layer_parts: bool = True, max_ahead: int = 2,
+                 checkpoints: str = "bf16") -> dict:
     """Streamed vs resident step time of a Qwen2.5-shaped identity-mixing stack for each
     (tokens, block size), with the bitwise check, H2D traffic, and the copy/compute
     overlap measured by the pool's own events: copy_ms = device time of the H2D copies
@@ -602,7 +603,8 @@ def stream_bench(torch, model: str, block_sizes, tokens_list, steps: int, h2d_gb
     recomputed in its backward visit). layer_parts: the pool copies and releases each
     layer of a block on its own instead of one copy per block, and the compute stream
     waits for each layer's copy instead of the whole block's. max_ahead: blocks the host
-    may run ahead of the device (stream_pool_set_max_ahead; 0 = no bound)."""
+    may run ahead of the device (stream_pool_set_max_ahead; 0 = no bound). checkpoints: how the
+    stacks hold activations for the backward (NF4Stack's argument)."""
     from nf4_weight_streamed_amd import stack as ST
 
     dims, n_layers = ST.QWEN25[model]
@@ -616,7 +618,7 @@ def stream_bench(torch, model: str, block_sizes, tokens_list, steps: int, h2d_gb
     for tokens in tokens_list:
         h0, dh = _stack_inputs(torch, tokens, dims.hidden)
         flops = n_layers * sum(4 * tokens * n * k + 6 * tokens * RANK * (n + k) for n, k in dims.shapes().values())
-        res = _stack_run(torch, ST, base, lora, tokens, h0, dh, steps, mode="resident")
+        res = _stack_run(torch, ST, base, lora, tokens, h0, dh, steps, mode="resident", checkpoints=checkpoints)
         print(f"[stream_bench] {model} T={tokens}: resident {res['s'] * 1e3:.1f} ms per step", file=sys.stderr,
               flush=True)
         for i, (bs, n_slots) in enumerate((bs, k) for bs in block_sizes for k in slot_counts):
@@ -624,7 +626,7 @@ def stream_bench(torch, model: str, block_sizes, tokens_list, steps: int, h2d_gb
             if n_slots >= b.n_blocks:
                 continue
             got = _stack_run(torch, ST, b, lora, tokens, h0, dh, steps, mode="streamed", n_slots=n_slots,
-                             layer_parts=layer_parts, max_ahead=max_ahead)
+                             layer_parts=layer_parts, max_ahead=max_ahead, checkpoints=checkpoints)
             r_s, s_s, nbytes = res["s"], got["s"], got["bytes"]
             print(f"[stream_bench] {model} T={tokens} bs={bs} slots={n_slots}: streamed {s_s * 1e3:.1f} ms per step",
                   file=sys.stderr, flush=True)
@@ -667,9 +669,11 @@ def stream_bench(torch, model: str, block_sizes, tokens_list, steps: int, h2d_gb
                                   "acquire-wait spans on the compute stream",
                 "host_base_gb": round(base.total_bytes() / 1e9, 3),
             }
+            if checkpoints != "bf16":
+                row.update(checkpoints=checkpoints, activation_gb=round(got["act"] / 1e9, 3))
             if remat and i == 0:
                 rm = _stack_run(torch, ST, b, lora, tokens, h0, dh, steps, mode="streamed", n_slots=n_slots,
-                                remat=True, layer_parts=layer_parts, max_ahead=max_ahead)
+                                remat=True, layer_parts=layer_parts, max_ahead=max_ahead, checkpoints=checkpoints)
                 row["remat"] = {
                     "bitwise_equal_to_resident": bool(torch.equal(res["y"], rm["y"]) and torch.equal(res["dx"], rm["dx"])),
                     "streamed_ms_per_step": round(rm["s"] * 1e3, 3),
@@ -937,6 +941,8 @@ def main() -> int:
     ap.add_argument("--stream-base", default="nf4", choices=("nf4", "bf16"),
                     help="format of the streamed base: nf4, or dense bf16 (the bf16_bitwise mode)")
     ap.add_argument("--stack-tokens", default="512", help="comma-separated token counts of the streamed stacks")
+    ap.add_argument("--checkpoints", default="bf16", choices=("bf16", "int8"),
+                    help="what the streamed stacks hold of their activations for the backward")
     ap.add_argument("--no-remat", action="store_true", help="skip the rematerialisation run of the streamed stacks")
     ap.add_argument("--block-copies", action="store_true",
                     help="streamed stacks: one copy per block and one wait for it (default: each layer of a block "
@@ -1116,7 +1122,7 @@ def main() -> int:
         out["denominators"]["h2d_pinned_gbs_measured"] = round(h2d, 2)
         runs = [stream_bench(torch, m, block_sizes, stack_tokens, args.stack_steps, h2d, args.stream_base, slot_counts,
                              remat=not args.no_remat, layer_parts=not args.block_copies,
-                             max_ahead=args.max_ahead)
+                             max_ahead=args.max_ahead, checkpoints=args.checkpoints)
                 for m in models]
         out["streamed"] = dict(runs[0]["rows"][0], load=runs[0]["load"])
         out["streamed_all"] = runs

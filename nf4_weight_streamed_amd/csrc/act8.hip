@@ -15,36 +15,61 @@ constexpr int64_t kMaxElems = int64_t(1) << 34;  // a launch holds 2^32 threads
 
 __device__ __forceinline__ int64_t first_octet() { return int64_t(blockIdx.x) * kThreads + threadIdx.x; }
 
-__device__ __forceinline__ u32x4 octet(const uint16_t* p, int64_t i) { return reinterpret_cast<const u32x4*>(p)[i]; }
-__device__ __forceinline__ u32x2 codes8(const uint8_t* p, int64_t i) { return reinterpret_cast<const u32x2*>(p)[i]; }
+// Results are stored past the caches: the next operator finds them no later (a training step of four
+// 7B layers takes the same time) and this one loses less of its inputs (512 x 18944 SiLU product
+// 14.6 -> 13.4 us, its backward 14.3 -> 12.7). Inputs are loaded past them too (kStream) where a call
+// moves more than the last-level cache holds: 8192 x 29568 forward 322 -> 313 us, m again 160 -> 146,
+// backward 331 -> 312; at 512 rows, whose inputs the previous operator has just written, 13.4 -> 15.0
+// and 12.7 -> 15.0. Quantising takes neither (125 us; 127 and 131).
+constexpr size_t kLastLevelCache = size_t(256) << 20;
+
+template <bool kStream, typename V>
+__device__ __forceinline__ V load(const void* p, int64_t i) {
+    const V* q = static_cast<const V*>(p) + i;
+    return kStream ? __builtin_nontemporal_load(q) : *q;
+}
+
+__device__ __forceinline__ void store_octet(uint16_t* p, int64_t i, const float (&v)[8]) {
+    __builtin_nontemporal_store(pack_octet(v), reinterpret_cast<u32x4*>(p) + i);
+}
 
 struct Checkpoint {
     const uint8_t* codes;
     const float* scale;
-    __device__ __forceinline__ void read(int64_t i, float (&v)[8]) const { act8_values8(codes8(codes, i), scale[i >> 3], v); }
+    template <bool kStream>
+    __device__ __forceinline__ void read(int64_t i, float (&v)[8]) const {
+        act8_values8(load<kStream, u32x2>(codes, i), scale[i >> 3], v);
+    }
 };
 
 struct CheckpointOut {
     uint8_t* codes;
     float* scale;
+    template <bool kPast>
     __device__ __forceinline__ void write(int64_t i, u32x4 x) const {
         float s;
-        reinterpret_cast<u32x2*>(codes)[i] = act8_quantize8(x, s);
+        const u32x2 c = act8_quantize8(x, s);
+        u32x2* q = reinterpret_cast<u32x2*>(codes) + i;
+        if constexpr (kPast)
+            __builtin_nontemporal_store(c, q);
+        else
+            *q = c;
         if ((i & 7) == 0) scale[i >> 3] = s;
     }
 };
 
 __global__ __launch_bounds__(kThreads) void k_act8_quantize(const uint16_t* x, int64_t octets, CheckpointOut out) {
     const int64_t i = first_octet();
-    if (i < octets) out.write(i, octet(x, i));
+    if (i < octets) out.write<false>(i, load<false, u32x4>(x, i));
 }
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void k_act8_dequantize(Checkpoint in, int64_t octets, uint16_t* out) {
     const int64_t i = first_octet();
     if (i >= octets) return;
     float v[8];
-    in.read(i, v);
-    reinterpret_cast<u32x4*>(out)[i] = pack_octet(v);
+    in.read<kStream>(i, v);
+    store_octet(out, i, v);
 }
 
 // 1 / (1 + e^-z): the hardware's exponential and reciprocal are off by about 2^-22 of the result
@@ -53,48 +78,51 @@ __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * z));
 }
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void k_silu_mul_fwd_act8(const uint16_t* gate, const uint16_t* up, int64_t octets,
                                                                 uint16_t* m, CheckpointOut g8, CheckpointOut u8) {
     const int64_t i = first_octet();
     if (i >= octets) return;
-    const u32x4 gw = octet(gate, i), uw = octet(up, i);
+    const u32x4 gw = load<kStream, u32x4>(gate, i), uw = load<kStream, u32x4>(up, i);
     float g[8], u[8];
     unpack_octet(gw, g);
     unpack_octet(uw, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] *= g[e] * sigmoid(g[e]);
-    reinterpret_cast<u32x4*>(m)[i] = pack_octet(u);
-    g8.write(i, gw);
-    u8.write(i, uw);
+    store_octet(m, i, u);
+    g8.write<true>(i, gw);
+    u8.write<true>(i, uw);
 }
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void k_silu_mul_act8(Checkpoint g8, Checkpoint u8, int64_t octets, uint16_t* m) {
     const int64_t i = first_octet();
     if (i >= octets) return;
     float g[8], u[8];
-    g8.read(i, g);
-    u8.read(i, u);
+    g8.read<kStream>(i, g);
+    u8.read<kStream>(i, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) u[e] *= g[e] * sigmoid(g[e]);
-    reinterpret_cast<u32x4*>(m)[i] = pack_octet(u);
+    store_octet(m, i, u);
 }
 
+template <bool kStream>
 __global__ __launch_bounds__(kThreads) void k_silu_mul_bwd_act8(Checkpoint g8, Checkpoint u8, const uint16_t* dm, int64_t octets,
                                                                 uint16_t* dgate, uint16_t* dup) {
     const int64_t i = first_octet();
     if (i >= octets) return;
     float g[8], u[8], d[8];
-    unpack_octet(octet(dm, i), d);
-    g8.read(i, g);
-    u8.read(i, u);
+    unpack_octet(load<kStream, u32x4>(dm, i), d);
+    g8.read<kStream>(i, g);
+    u8.read<kStream>(i, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const float s = sigmoid(g[e]), t = g[e] * s;
         u[e] *= d[e] * (s + t * (1.0f - s));
         d[e] *= t;
     }
-    reinterpret_cast<u32x4*>(dgate)[i] = pack_octet(u);
-    reinterpret_cast<u32x4*>(dup)[i] = pack_octet(d);
+    store_octet(dgate, i, u);
+    store_octet(dup, i, d);
 }
 
 bool aligned(const void* p, size_t a) { return p && reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -119,6 +147,11 @@ public:
     bool nothing() const { return status_ != NF4_OK || elems_ == 0; }
     int status() const { return status_; }
     int64_t octets() const { return elems_ / 8; }
+    bool large() const {  // no cache holds what the call moves
+        size_t bytes = 0;
+        for (int i = 0; i < n_; ++i) bytes += range_[i].bytes;
+        return bytes > kLastLevelCache;
+    }
     dim3 grid() const { return dim3(unsigned(cdiv(octets(), kThreads))); }
 
 private:
@@ -168,8 +201,8 @@ int nf4_act8_dequantize(const uint8_t* codes, const float* scale, int64_t rows, 
     Call c("nf4_act8_dequantize", rows, cols);
     c.read8(codes, scale).write(x);
     if (c.nothing()) return c.status();
-    hipLaunchKernelGGL(k_act8_dequantize, c.grid(), dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                       Checkpoint{codes, scale}, c.octets(), x);
+    hipLaunchKernelGGL((c.large() ? k_act8_dequantize<true> : k_act8_dequantize<false>), c.grid(), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), Checkpoint{codes, scale}, c.octets(), x);
     return check_launch("nf4_act8_dequantize");
 }
 
@@ -178,8 +211,9 @@ int nf4_silu_mul_fwd_act8(const uint16_t* gate, const uint16_t* up, int64_t rows
     Call c("nf4_silu_mul_fwd_act8", rows, cols);
     c.read(gate).read(up).write(m).write8(gate_codes, gate_scale).write8(up_codes, up_scale);
     if (c.nothing()) return c.status();
-    hipLaunchKernelGGL(k_silu_mul_fwd_act8, c.grid(), dim3(kThreads), 0, static_cast<hipStream_t>(stream), gate, up,
-                       c.octets(), m, CheckpointOut{gate_codes, gate_scale}, CheckpointOut{up_codes, up_scale});
+    hipLaunchKernelGGL((c.large() ? k_silu_mul_fwd_act8<true> : k_silu_mul_fwd_act8<false>), c.grid(), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), gate, up, c.octets(), m,
+                       CheckpointOut{gate_codes, gate_scale}, CheckpointOut{up_codes, up_scale});
     return check_launch("nf4_silu_mul_fwd_act8");
 }
 
@@ -188,8 +222,9 @@ int nf4_silu_mul_act8(const uint8_t* gate_codes, const float* gate_scale, const 
     Call c("nf4_silu_mul_act8", rows, cols);
     c.read8(gate_codes, gate_scale).read8(up_codes, up_scale).write(m);
     if (c.nothing()) return c.status();
-    hipLaunchKernelGGL(k_silu_mul_act8, c.grid(), dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                       Checkpoint{gate_codes, gate_scale}, Checkpoint{up_codes, up_scale}, c.octets(), m);
+    hipLaunchKernelGGL((c.large() ? k_silu_mul_act8<true> : k_silu_mul_act8<false>), c.grid(), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), Checkpoint{gate_codes, gate_scale},
+                       Checkpoint{up_codes, up_scale}, c.octets(), m);
     return check_launch("nf4_silu_mul_act8");
 }
 
@@ -199,8 +234,9 @@ int nf4_silu_mul_bwd_act8(const uint8_t* gate_codes, const float* gate_scale, co
     Call c("nf4_silu_mul_bwd_act8", rows, cols);
     c.read8(gate_codes, gate_scale).read8(up_codes, up_scale).read(dm).write(dgate).write(dup);
     if (c.nothing()) return c.status();
-    hipLaunchKernelGGL(k_silu_mul_bwd_act8, c.grid(), dim3(kThreads), 0, static_cast<hipStream_t>(stream),
-                       Checkpoint{gate_codes, gate_scale}, Checkpoint{up_codes, up_scale}, dm, c.octets(), dgate, dup);
+    hipLaunchKernelGGL((c.large() ? k_silu_mul_bwd_act8<true> : k_silu_mul_bwd_act8<false>), c.grid(), dim3(kThreads), 0,
+                       static_cast<hipStream_t>(stream), Checkpoint{gate_codes, gate_scale},
+                       Checkpoint{up_codes, up_scale}, dm, c.octets(), dgate, dup);
     return check_launch("nf4_silu_mul_bwd_act8");
 }
 

@@ -22,6 +22,7 @@ namespace nf4 {
 
 namespace {
 
+constexpr size_t kLastLevelCache = size_t(256) << 20;
 constexpr int64_t kMaxWidth = 16384;
 constexpr int64_t kMaxGrid = int64_t(1) << 21;  // workgroups; rows past it are looped over
 
@@ -44,12 +45,12 @@ struct __attribute__((packed, aligned(2))) LooseOctet {
     u32x4 w;
 };
 
-template <bool kRagged, int N, bool kWave>
+template <bool kRagged, bool kStream = false, int N, bool kWave>
 __device__ __forceinline__ void load_line(const uint16_t* p, int64_t base, int H, const Place<kWave>& pl, u32x4 (&x)[N]) {
     if constexpr (!kRagged) {
         const auto r = make_rsrc(p ? p + base : nullptr, p ? uint32_t(H) * 2u : 0u);
 #pragma unroll
-        for (int n = 0; n < N; ++n) x[n] = buf_load16(r, uint32_t(pl.at(n)) * 2u);
+        for (int n = 0; n < N; ++n) x[n] = kStream ? buf_load16_nt(r, uint32_t(pl.at(n)) * 2u) : buf_load16(r, uint32_t(pl.at(n)) * 2u);
     } else {
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -72,7 +73,7 @@ __device__ __forceinline__ void store_line(uint16_t* p, int64_t base, int H, con
     if constexpr (!kRagged) {
         const auto r = make_rsrc(p ? p + base : nullptr, p ? uint32_t(H) * 2u : 0u);
 #pragma unroll
-        for (int n = 0; n < N; ++n) __builtin_amdgcn_raw_buffer_store_b128(x[n], r, pl.at(n) * 2, 0, 0);
+        for (int n = 0; n < N; ++n) __builtin_amdgcn_raw_buffer_store_b128(x[n], r, pl.at(n) * 2, 0, 2);
     } else {
         if (!p) return;
 #pragma unroll
@@ -139,7 +140,7 @@ struct FwdArgs {
     uint16_t *h_out, *n;
     uint8_t* codes;
     float *n_scale, *rstd_o, *rstd;
-    int T, H, gate_kind;
+    int T, H, gate_kind, stream;
     float scale, offset, eps;
 };
 
@@ -164,12 +165,14 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_fwd(FwdArgs a) {
     struct {
         u32x4 o[kBlock ? N : 1], h[N], gate[kBlock ? N : 1];
     } next;
-    auto load = [&](int row) {  // in the order of their use
+    auto load_as = [&](int row, auto stream) {  // in the order of their use
+        constexpr bool kStream = decltype(stream)::value;
         const int64_t base = int64_t(row) * H;
-        if constexpr (kBlock > 0) load_line<kRagged>(a.o, base, H, p, next.o);
-        load_line<kRagged>(a.h, base, H, p, next.h);
+        if constexpr (kBlock > 0) load_line<kRagged, kStream>(a.o, base, H, p, next.o);
+        load_line<kRagged, kStream>(a.h, base, H, p, next.h);
         if constexpr (kBlock > 0) load_line<kRagged>(a.gate, a.gate_kind == NF4_GATE_TOKEN ? base : 0, H, p, next.gate);
     };
+    auto load = [&](int row) { a.stream ? load_as(row, std::true_type{}) : load_as(row, std::false_type{}); };
     u32x4 fw[N], pw[kBlock > 1 ? N : 1];  // the same for all rows
     if (p.first < a.T) load(p.first);
     if constexpr (kBlock > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw);
@@ -255,7 +258,7 @@ struct BwdArgs {
     uint16_t *dh, *d_o, *dgate_rows;
     float* part;  // [workgroups][dgain, dpost_gain, dgate][H]; which are wanted:
     int sums;     // bit 0, 1, 2
-    int T, H, n_dn, gate_kind;
+    int T, H, n_dn, gate_kind, stream;
     float scale, offset;
 };
 
@@ -267,30 +270,38 @@ struct RowIn {
     float r, r_o;
 };
 
-template <int N, bool kRagged, int kBranch, bool kWave>
-__device__ __forceinline__ void load_row(const BwdArgs& a, const Place<kWave>& p, int row, RowIn<N, kBranch>& in) {
+template <int N, bool kRagged, bool kStream, int kBranch, bool kWave>
+__device__ __forceinline__ void load_row_as(const BwdArgs& a, const Place<kWave>& p, int row, RowIn<N, kBranch>& in) {
     const int64_t base = int64_t(row) * a.H;
     const int H = a.H;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) load_line<kRagged>(a.dn[i], base, H, p, in.d[i]);
+    for (int i = 0; i < 3; ++i) load_line<kRagged, kStream>(a.dn[i], base, H, p, in.d[i]);
     if (a.codes) {
         const auto rc = make_rsrc(a.codes + base, uint32_t(H));
         const auto rs = make_rsrc(a.n_scale + int64_t(row) * (H / 64), uint32_t(H / 64) * 4u);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const u32x2 c = buf_load8(rc, uint32_t(p.at(n)));
+            const u32x2 c = kStream ? buf_load8_nt(rc, uint32_t(p.at(n))) : buf_load8(rc, uint32_t(p.at(n)));
             in.h[n] = u32x4{c.x, c.y, buf_load_u32(rs, uint32_t(p.at(n)) / 64 * 4u), 0};
         }
     } else {
-        load_line<kRagged>(a.h, base, H, p, in.h);
+        load_line<kRagged, kStream>(a.h, base, H, p, in.h);
     }
     in.r = a.rstd[row];
-    load_line<kRagged>(a.dres, base, H, p, in.res);
+    load_line<kRagged, kStream>(a.dres, base, H, p, in.res);
     if constexpr (kBranch > 0) {
-        load_line<kRagged>(a.o, base, H, p, in.o);
+        load_line<kRagged, kStream>(a.o, base, H, p, in.o);
         load_line<kRagged>(a.gate, a.gate_kind == NF4_GATE_TOKEN ? base : 0, H, p, in.gate);
         in.r_o = kBranch > 1 ? a.rstd_o[row] : 1.0f;
     }
+}
+
+template <int N, bool kRagged, int kBranch, bool kWave>
+__device__ __forceinline__ void load_row(const BwdArgs& a, const Place<kWave>& p, int row, RowIn<N, kBranch>& in) {
+    if (a.stream)
+        load_row_as<N, kRagged, true>(a, p, row, in);
+    else
+        load_row_as<N, kRagged, false>(a, p, row, in);
 }
 
 // kBranch: gradients of the block's side are wanted, 2 with its norm. kSums: sums over rows are; a
@@ -655,8 +666,9 @@ extern "C" int nf4_residual_norm_fwd(const uint16_t* h, const uint16_t* o, int64
     for (const void* p : {(const void*)h, (const void*)o, (const void*)post_gain, (const void*)gate, (const void*)gain,
                           (const void*)h_out, (const void*)n})
         ragged = ragged || !aligned(p, 16);
+    const int large = all * (n_codes ? 5 : 4) / 2 * (o ? 2 : 1) > kLastLevelCache;
     const FwdArgs a{h, o, post_gain, gate, gain, h_out, n, n_codes, n_scale, rstd_o, rstd, int(T), int(H), gate_kind,
-                    scale, gain_offset, eps};
+                    large, scale, gain_offset, eps};
     hipStream_t s = static_cast<hipStream_t>(stream);
     const unsigned grid = rows_grid(T, H, post_norm && !ragged);
     if (!o)
@@ -735,7 +747,7 @@ extern "C" int nf4_residual_norm_bwd(const uint16_t* const* dn, int n_dn, const 
     a.dgate_rows = channel ? nullptr : static_cast<uint16_t*>(dgate);
     // the branch's gate is not read where nothing of the branch is wanted
     a.gate_kind = branch ? gate_kind : NF4_GATE_NONE, a.gate = gate, a.T = int(T), a.H = int(H);
-    a.n_dn = n_dn, a.scale = scale, a.offset = gain_offset;
+    a.n_dn = n_dn, a.stream = all * (n_dn + 3 + (branch ? 2 : 0)) > kLastLevelCache, a.scale = scale, a.offset = gain_offset;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t groups = T > 0 ? sum_groups(T, H) : 0;
     const unsigned grid = sums ? unsigned(groups) : rows_grid(T, H, branch && post_norm && !ragged);
