@@ -421,11 +421,13 @@ int nf4_silu_mul_bwd_act8(const uint8_t* gate_codes, const float* gate_scale, co
 
 /*
  * nf4_lora_linear_bwd and nf4_lora_linear_bwd_bf16 with the forward's input as a checkpoint
- * (x_codes [T][K], x_scale [T][K/64]): dA = s . g^T . RNbf(value), everything else, workspace
- * sizes among it (nf4_lora_linear_bwd_workspace, nf4_lora_linear_bwd_bf16_workspace), as there.
- * dX is those calls', bit for bit; the products of dA and dB take their fp32 operands (s.g, s.u) as
- * three bf16 values instead of two, so that both are off by fp32's roundings alone.
+ * (x_codes [T][K], x_scale [T][K/64]): dA = s . g^T . RNbf(value), everything else as there but the
+ * sizes of the workspace, which are the two functions' below. The products of dA and dB take
+ * their fp32 operands (s.g, s.u) as three bf16 values instead of two, so that both are off by fp32's
+ * roundings alone; dX is rounded to bf16 from sums in fp32 there and here, in other orders.
  */
+size_t nf4_lora_linear_bwd_act8_workspace(int64_t T, int64_t N, int64_t K, int r);
+size_t nf4_lora_linear_bwd_bf16_act8_workspace(int64_t T, int64_t N, int64_t K, int r);
 int nf4_lora_linear_bwd_act8(const uint8_t* codes, const float* absmax, int64_t N, int64_t K, const uint8_t* x_codes,
                              const float* x_scale, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
                              const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws,

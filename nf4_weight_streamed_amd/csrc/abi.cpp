@@ -271,6 +271,16 @@ size_t nf4_lora_linear_bwd_bf16_workspace(int64_t T, int64_t N, int64_t K, int r
     return plan_bwd(T, N, K, r, true).ws_bytes;
 }
 
+size_t nf4_lora_linear_bwd_act8_workspace(int64_t T, int64_t N, int64_t K, int r) {
+    if (T <= 0 || N <= 0 || K <= 0 || K % NF4_BLOCK != 0 || r < 0 || r > NF4_MAX_RANK) return 0;
+    return plan_bwd_act8(T, N, K, r, false).ws_bytes;
+}
+
+size_t nf4_lora_linear_bwd_bf16_act8_workspace(int64_t T, int64_t N, int64_t K, int r) {
+    if (T <= 0 || N <= 0 || K <= 0 || K % NF4_BLOCK != 0 || r < 0 || r > NF4_MAX_RANK) return 0;
+    return plan_bwd_act8(T, N, K, r, true).ws_bytes;
+}
+
 }  // extern "C"
 
 namespace nf4 {
@@ -305,8 +315,9 @@ int linear_fwd(const char* fn, const uint8_t* codes, const float* absmax, const 
 
 namespace {
 
+// The backward after the base-specific checks; act8: the input is a checkpoint (with r = 0 there is none).
 int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const uint16_t* wdense, int64_t N, int64_t K,
-               const SavedInput& x, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
+               bool act8, const SavedInput& x, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
                const uint16_t* B, int r, float alpha, uint16_t* dx, float* dA, float* dB, void* ws, size_t ws_bytes,
                nf4_stream stream) {
     if (T == 0) return NF4_OK;
@@ -317,7 +328,7 @@ int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const 
         (r > 0 && (!aligned(x.x, 16) || !aligned(x.codes, 16) || !aligned(x.scale, 4) || !aligned(A, 16) || !aligned(B, 2) ||
                    !aligned(u_save, 4) || !aligned(dA, 16) || !aligned(dB, 4))))
         return fail(NF4_E_ARG, "%s: misaligned pointer (dy, dx, x, A and dA need 16 bytes)", fn);
-    const BwdPlan p = plan_bwd(T, N, K, r, wdense != nullptr);
+    const BwdPlan p = act8 ? plan_bwd_act8(T, N, K, r, wdense != nullptr) : plan_bwd(T, N, K, r, wdense != nullptr);
     if (!ws || ws_bytes < p.ws_bytes || !aligned(ws, 256))
         return fail(NF4_E_ARG, "%s: workspace of %zu bytes (256-byte aligned) needed for T=%lld N=%lld K=%lld r=%d, got %zu",
                     fn, p.ws_bytes, (long long)T, (long long)N, (long long)K, r, ws_bytes);
@@ -331,14 +342,15 @@ int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const 
                                             ws, s),
                           "nf4_lora_linear_bwd (few-token path)");
     if (r > 0) {
-        int st = hip_status(launch_lora_bwd_pre(p, dy, B, u_save, T, N, r, scale, x.codes != nullptr,
+        int st = hip_status(launch_lora_bwd_pre(p, dy, B, u_save, T, N, r, scale, act8,
                                                 reinterpret_cast<float*>(w + p.off_gpart), dB,
                                                 reinterpret_cast<float*>(w + p.off_dbpart), s),
                             "nf4_lora_linear_bwd (g, dB)");
         if (st != NF4_OK) return st;
     }
     // dX (when requested) with its LoRA term, and dA
-    return hip_status(launch_gemm_bwd(p, codes, absmax, wdense, dy, x, A, T, N, K, r, scale, dx, dA, dB, ws, s),
+    return hip_status(act8 ? launch_gemm_bwd_act8(p, codes, absmax, wdense, dy, x, A, T, N, K, r, scale, dx, dA, dB, ws, s)
+                           : launch_gemm_bwd(p, codes, absmax, wdense, dy, x.x, A, T, N, K, r, scale, dx, dA, dB, ws, s),
                       "nf4_lora_linear_bwd (dX, dA)");
 }
 
@@ -372,7 +384,7 @@ int nf4_lora_linear_bwd(const uint8_t* codes, const float* absmax, int64_t N, in
     const char* fn = "nf4_lora_linear_bwd";
     const int st = nf4::check_linear_common(fn, codes, absmax, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB, ws,
+    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, false, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB, ws,
                            ws_bytes, stream);
 }
 
@@ -382,7 +394,7 @@ int nf4_lora_linear_bwd_bf16(const uint16_t* w, int64_t N, int64_t K, const uint
     const char* fn = "nf4_lora_linear_bwd_bf16";
     const int st = nf4::check_linear_dense(fn, w, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB,
+    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, false, {x, nullptr, nullptr}, u_save, dy, T, A, B, r, alpha, dx, dA, dB,
                            ws, ws_bytes, stream);
 }
 
@@ -393,7 +405,7 @@ int nf4_lora_linear_bwd_act8(const uint8_t* codes, const float* absmax, int64_t 
     const char* fn = "nf4_lora_linear_bwd_act8";
     const int st = nf4::check_linear_common(fn, codes, absmax, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx,
+    return nf4::linear_bwd(fn, codes, absmax, nullptr, N, K, true, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx,
                            dA, dB, ws, ws_bytes, stream);
 }
 
@@ -404,7 +416,7 @@ int nf4_lora_linear_bwd_bf16_act8(const uint16_t* w, int64_t N, int64_t K, const
     const char* fn = "nf4_lora_linear_bwd_bf16_act8";
     const int st = nf4::check_linear_dense(fn, w, N, K, T, r, alpha);
     if (st != NF4_OK) return st;
-    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx, dA,
+    return nf4::linear_bwd(fn, nullptr, nullptr, w, N, K, true, {nullptr, x_codes, x_scale}, u_save, dy, T, A, B, r, alpha, dx, dA,
                            dB, ws, ws_bytes, stream);
 }
 

@@ -38,8 +38,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kKeyWaves = 4;  // blocks of 32 keys of a dk/dv workgroup
 constexpr int64_t kMaxSeqs = int64_t(1) << 16;
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
 struct AttnArgs {
@@ -169,14 +167,6 @@ struct LdsMap {
 };
 
 __device__ __forceinline__ bf16x8 lds_frag(const char* p) { return as_bf16x8(*reinterpret_cast<const u32x4*>(p)); }
-
-// 8 contraction indices (two groups of 4 rows) of one column, from row-major LDS.
-__device__ __forceinline__ bf16x8 lds_frag_tr(const char* p0, const char* p1) {
-    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
-    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
-    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
-    return as_bf16x8(u32x4{x.x, x.y, y.x, y.y});
-}
 
 __device__ __forceinline__ bf16x8 pack8(const f32x16& v, int g) {
     return as_bf16x8(u32x4{pack_bf16x2(v[8 * g], v[8 * g + 1]), pack_bf16x2(v[8 * g + 2], v[8 * g + 3]),

@@ -104,6 +104,7 @@ struct BwdPlan {
     int dbchunks, dbtokens;  // token ranges of dB (1: written directly), tokens each
     size_t off_dbpart;     // dB shares [dbchunks][N][r] when dbchunks > 1
     size_t off_gpart, off_dapart, off_dx;  // workspace offsets (bytes)
+    size_t off_sg;         // plan_bwd_act8: s.g as bf16 parts
     size_t ws_bytes;
     bool skinny;           // few-token path: g partials and dX partials (sk) at off_gpart / off_dx
     SkinnyPlan sk;
@@ -121,6 +122,10 @@ hipError_t launch_gemm_fwd(const FwdPlan& p, const uint8_t* codes, const float* 
 hipError_t launch_lora_bwd_pre(const BwdPlan& p, const uint16_t* dy, const uint16_t* B, const float* u, int64_t T,
                                int64_t N, int r, float s, bool three, float* gpart, float* dB, float* dbpart,
                                hipStream_t stream);
+hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
+                           const uint16_t* dy, const uint16_t* x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
+                           int r, float s, uint16_t* dx, float* dA, float* dB, void* ws, hipStream_t stream);
+
 // The linear's input as its forward left it: bf16, or (x NULL) an 8-bit checkpoint, whose values
 // are rounded to bf16 where dA is formed.
 struct SavedInput {
@@ -129,9 +134,14 @@ struct SavedInput {
     const float* scale;    // [T][K/64]
 };
 
-hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
-                           const uint16_t* dy, const SavedInput& x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
-                           int r, float s, uint16_t* dx, float* dA, float* dB, void* ws, hipStream_t stream);
+// The backward from a checkpoint, for more than 32 tokens (any number with a dense base): tiles of bm x 256,
+// `full` of them (a multiple of the CUs) whole, the contraction of the last `tail` cut into pieces,
+// `pieces` in all.
+BwdPlan plan_bwd_act8(int64_t T, int64_t N, int64_t K, int r, bool dense);
+hipError_t launch_gemm_bwd_act8(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
+                                const uint16_t* dy, const SavedInput& x, const uint16_t* A, int64_t T, int64_t N,
+                                int64_t K, int r, float s, uint16_t* dx, float* dA, float* dB, void* ws,
+                                hipStream_t stream);
 
 hipError_t launch_skinny_fwd(const SkinnyPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* x,
                              const uint16_t* A, const uint16_t* B, int64_t T, int64_t N, int64_t K, int r, float s,

@@ -15,6 +15,9 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
 // Two float32 -> one dword of two bf16 (round to nearest even; one v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
     bf16x2 v = {(__bf16)lo, (__bf16)hi};
@@ -26,6 +29,14 @@ __device__ __forceinline__ uint16_t bf16_bits(float f) { return __builtin_bit_ca
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(uint32_t(b) << 16); }
 
 __device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// 8 contraction indices (two groups of 4 rows) of one column, from row-major LDS.
+__device__ __forceinline__ bf16x8 lds_frag_tr(const char* p0, const char* p1) {
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p0));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p1));
+    const u32x2 x = __builtin_bit_cast(u32x2, a), y = __builtin_bit_cast(u32x2, b);
+    return as_bf16x8(u32x4{x.x, x.y, y.x, y.y});
+}
 
 // D(32x32, fp32) += A(32x16, bf16) * B(16x32, bf16).
 // Lane l holds A row (l % 32), B column (l % 32), both at k = 8*(l/32) .. +7;

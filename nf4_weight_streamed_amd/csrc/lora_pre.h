@@ -39,7 +39,7 @@ struct GSmem {
 // each term).
 template <int RB, int DBT, bool kThree>
 struct DbSmem {
-    uint16_t dyt[64][DBT + 8];       // [n][t]
+    uint16_t dyt[64][DBT + 8];       // [n][t ^ (n & (DBT - 8))]: the transposing stores do not meet in a bank
     uint16_t uh[16 * RB][DBT + 8];   // (s.u)^T hi [j][t]
     uint16_t ul[16 * RB][DBT + 8];   // lo
     uint16_t ur[kThree ? 16 * RB : 1][DBT + 8];  // what both leave
@@ -213,12 +213,13 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
                                                                : kOutOfRange);
         }
     };
+    const int swz = ln8 & (DBT - 8);
     auto sstore = [&]() {
         if constexpr (DV == 1) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t w = vdy[0][e >> 1];
-                sm.dyt[ln8 + e][lt] = uint16_t((e & 1) ? (w >> 16) : (w & 0xFFFF));
+                sm.dyt[ln8 + e][lt ^ swz] = uint16_t((e & 1) ? (w >> 16) : (w & 0xFFFF));
             }
         } else {
 #pragma unroll
@@ -230,11 +231,11 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
                 for (int p = 0; p < DV / 2; ++p)
                     col[p] = __builtin_amdgcn_perm(vdy[2 * p + 1][e >> 1], vdy[2 * p][e >> 1], sel);
                 if constexpr (DV == 4)
-                    *reinterpret_cast<u32x2*>(&sm.dyt[ln8 + e][DV * lt]) = u32x2{col[0], col[1]};
+                    *reinterpret_cast<u32x2*>(&sm.dyt[ln8 + e][(DV * lt) ^ swz]) = u32x2{col[0], col[1]};
                 else
 #pragma unroll
                     for (int p = 0; p < DV / 2; ++p)
-                        *reinterpret_cast<uint32_t*>(&sm.dyt[ln8 + e][DV * lt + 2 * p]) = col[p];
+                        *reinterpret_cast<uint32_t*>(&sm.dyt[ln8 + e][(DV * lt + 2 * p) ^ swz]) = col[p];
             }
         }
         // (s.u)^T hi / lo as bf16 token pairs
@@ -270,8 +271,8 @@ __device__ void db_role(const uint16_t* __restrict__ dy, const float* __restrict
         gload(t0 + DBT);  // past the end: zeros
 #pragma unroll
         for (int kk = 0; kk < DBT / 32; ++kk) {  // tokens in increasing order
-            const bf16x8 a =
-                as_bf16x8(*reinterpret_cast<const u32x4*>(&sm.dyt[16 * wave + (lane & 15)][32 * kk + kof]));
+            const int row = 16 * wave + (lane & 15);
+            const bf16x8 a = as_bf16x8(*reinterpret_cast<const u32x4*>(&sm.dyt[row][(32 * kk + kof) ^ (row & (DBT - 8))]));
 #pragma unroll
             for (int b = 0; b < RB; ++b) {
                 const bf16x8 bh = as_bf16x8(*reinterpret_cast<const u32x4*>(&sm.uh[16 * b + (lane & 15)][32 * kk + kof]));

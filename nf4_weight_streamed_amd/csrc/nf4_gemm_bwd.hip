@@ -19,9 +19,9 @@
 // paired across rows the same way, with nothing to dequantise.
 #include <type_traits>
 
-#include "act8.h"
 #include "common.h"
 #include "device.h"
+#include "shares.h"
 
 namespace nf4 {
 
@@ -67,15 +67,13 @@ struct BwdLora {
     const float* gpart;  // [parts][T][r] partials of g = dY.B
     int parts;
     const uint16_t* A;   // [r][K]
-    SavedInput x;
+    const uint16_t* x;   // [T][K]
     float* dapart;       // [token tiles][r][K] dA share of each token tile
     int r;
     float s;
 };
 
-// kAct8: x is an 8-bit checkpoint, and dA takes s.g as three bf16, so that it is off by fp32's
-// roundings alone (with two, by 2^-17 of each term).
-template <int BM, bool kDense, bool kAct8>
+template <int BM, bool kDense>
 __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
     const uint16_t* __restrict__ dy, const void* __restrict__ weights, const float* __restrict__ absmax, int T,
     int N, int K, BwdTiles tl, BwdLora lora, uint16_t* __restrict__ dx, float* __restrict__ partial, Tables tab) {
@@ -92,12 +90,11 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
     // table; LoRA epilogue: (s.g)^T hi/lo for up to 64 ranks and the x tile transposed
     // (one 64-column half at a time with 128 tokens, all 128 columns with 256).
     constexpr int kTP = BM + 8;  // pitch of the epilogue's [.][t] tiles
-    constexpr int kParts = kAct8 ? 3 : 2;         // bf16 values of an s.g
-    constexpr int kXHalves = BM == 256 && !kAct8 ? 1 : 2;
+    constexpr int kXHalves = BM == 256 ? 1 : 2;
     constexpr int kXCols = BK / kXHalves;         // x columns staged at once
     constexpr int kBuf = BM * kLds + BK * kLdsW;  // one buffer: dY tile, then weight tile
     constexpr int kMain = 2 * kBuf + 2 * 512;
-    constexpr int kEpi = (kParts * 64 + kXCols) * kTP;
+    constexpr int kEpi = (2 * 64 + kXCols) * kTP;
     __shared__ __align__(16) uint16_t smem[kMain > kEpi ? kMain : kEpi];
     float* const sLut = reinterpret_cast<float*>(smem + 2 * kBuf);
 
@@ -318,8 +315,7 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         if (nb_begin >= nb_end) __syncthreads();
         uint16_t* const sg_hi = smem;             // [64][kTP]
         uint16_t* const sg_lo = smem + 64 * kTP;  // [64][kTP]
-        uint16_t* const sg_rest = smem + 128 * kTP;  // kAct8: [64][kTP], what both leave
-        uint16_t* const sxt = smem + kParts * 64 * kTP;  // [kXCols][kTP]
+        uint16_t* const sxt = smem + 128 * kTP;   // [BK / 2][kTP]
         const int rp = (r + 15) & ~15;
         // one descriptor per partial over this tile's rows, so sizes and offsets stay
         // small for any token count; 12 bytes of slack keep the last 16-byte load (4-byte
@@ -329,10 +325,7 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         auto gpart_rsrc = [&](int p) {
             return make_rsrc(lora.gpart + (size_t(min(p, lora.parts - 1)) * T + m0) * r, gbytes);
         };
-        const auto rx = kAct8 ? make_rsrc(lora.x.codes + size_t(m0) * K, trows * uint32_t(K))
-                              : make_rsrc(lora.x.x + size_t(m0) * K, trows * uint32_t(K) * 2u);
-        const auto rxs = make_rsrc(kAct8 ? lora.x.scale + size_t(m0) * (K / 64) : nullptr,
-                                   kAct8 ? trows * uint32_t(K / 64) * 4u : 0u);
+        const auto rx = make_rsrc(lora.x + size_t(m0) * K, trows * uint32_t(K) * 2u);
         // every load of the staging is issued before the first is consumed (one memory
         // round trip at the end of the kernel, not one per loop trip)
         constexpr int XC = BM * (BK / 8) / NT;  // 16-byte x chunks per thread
@@ -357,18 +350,10 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         static_assert(XC == 8 && BM == 8 * (NT / 16) && BK == 16 * 8, "x tile: chunk blocks of 8 x 8, 16 across");
         const int xk8 = 8 * (tid & 15), xt0 = 8 * (tid >> 4);
         u32x4 xv[XC];
-        u32x2 xc[XC];
-        float xs[XC];
 #pragma unroll
         for (int i = 0; i < XC; ++i) {
             // rows past T read zero; columns past K only feed dA columns never stored
-            const uint32_t at = uint32_t(xt0 + i) * uint32_t(K) + uint32_t(k0 + xk8);
-            if constexpr (kAct8) {
-                xc[i] = buf_load8(rx, at);
-                xs[i] = buf_load_f32(rxs, at / 64 * 4u);
-            } else {
-                xv[i] = buf_load16(rx, at * 2u);
-            }
+            xv[i] = buf_load16(rx, (uint32_t(xt0 + i) * uint32_t(K) + uint32_t(k0 + xk8)) * 2u);
         }
         constexpr int GR = 8;  // partials loaded per round (registers are free after the main loop)
         for (int jb = 0; jb < rp / 16; ++jb) {
@@ -403,25 +388,10 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     __bf16 hh, ll;
-                    const float sg = j + c < r ? lora.s * v[c] : 0.0f;
-                    if constexpr (kAct8) {
-                        __bf16 rr;
-                        split_bf16(sg, hh, ll, rr);
-                        sg_rest[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, rr);
-                    } else {
-                        split_bf16(sg, hh, ll);
-                    }
+                    split_bf16(j + c < r ? lora.s * v[c] : 0.0f, hh, ll);
                     sg_hi[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, hh);
                     sg_lo[(j + c) * kTP + t] = __builtin_bit_cast(uint16_t, ll);
                 }
-            }
-        }
-        if constexpr (kAct8) {
-#pragma unroll
-            for (int i = 0; i < XC; ++i) {
-                float v[8];
-                act8_values8(xc[i], xs[i], v);
-                xv[i] = pack_octet(v);
             }
         }
         // x^T of columns kXCols h .. kXCols (h + 1) - 1 (with two halves a thread's chunks
@@ -473,11 +443,8 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
         }
 
         // dA share of this token tile: D[k][j] over t, 16x16x32 MFMAs; per staged group
-        // of kXCols columns, wave w owns the K sub-block w (16 columns) modulo their number, and
-        // where the waves are more, every kTurns-th block of 16 ranks
-        constexpr int kSubs = kXCols / 16, kTurns = NT / 64 / kSubs;
-        static_assert(kSubs * kTurns == NT / 64, "a whole number of waves per 16-column K sub-block");
-        const int sub = wave % kSubs;
+        // of kXCols columns, wave w owns the K sub-block w (16 columns)
+        static_assert(kXCols == 16 * (NT / 64), "one 16-column K sub-block per wave");
         const int l16 = lane & 15, t8 = 8 * (lane >> 4);
         float* dpart = lora.dapart + size_t(tm) * r * K;
         for (int h = 0; h < kXHalves; ++h) {
@@ -486,22 +453,19 @@ __global__ __launch_bounds__(2 * BM, BM == 128 ? 2 : 1) void k_nf4_gemm_bwd_dx(
                 stage_x(h);
                 __syncthreads();
             }
-            for (int jb = wave / kSubs; jb < rp / 16; jb += kTurns) {
+            for (int jb = 0; jb < rp / 16; ++jb) {
                 f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ts = 0; ts < BM / 32; ++ts) {
                     const int tt = 32 * ts + t8;
-                    const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[(16 * sub + l16) * kTP + tt]));
+                    const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[(16 * wave + l16) * kTP + tt]));
                     const bf16x8 gh = as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_hi[(16 * jb + l16) * kTP + tt]));
                     const bf16x8 gl = as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_lo[(16 * jb + l16) * kTP + tt]));
                     d = mfma16x16x32(xa, gh, d);
                     d = mfma16x16x32(xa, gl, d);
-                    if constexpr (kAct8)
-                        d = mfma16x16x32(
-                            xa, as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_rest[(16 * jb + l16) * kTP + tt])), d);
                 }
-                // lane holds D[k = kXCols h + 16 sub + 4 (lane / 16) + e][j = 16 jb + lane % 16]
-                const int j = 16 * jb + l16, kq = k0 + kXCols * h + 16 * sub + 4 * (lane >> 4);
+                // lane holds D[k = 64 h + 16 wave + 4 (lane / 16) + e][j = 16 jb + lane % 16]
+                const int j = 16 * jb + l16, kq = k0 + kXCols * h + 16 * wave + 4 * (lane >> 4);
                 if (j < r && kq < K) *reinterpret_cast<f32x4*>(&dpart[size_t(j) * K + kq]) = d;
             }
         }
@@ -548,21 +512,6 @@ struct BwdFinishDx {
     int T, K;
     int bal_a, bal_pa;  // balanced split: tiles below bal_a have bal_pa pieces
 };
-struct Shares {  // dst[i] = ((src[0][i] + src[1][i]) + src[2][i]) + ...
-    const float* src;
-    int count;
-    int64_t total;
-    float* dst;
-};
-
-__device__ __forceinline__ void sum_shares(const Shares& sh, int64_t block) {
-    const int64_t idx = (block * 256 + threadIdx.x) * 4;
-    if (idx >= sh.total) return;
-    f32x4 a = *reinterpret_cast<const f32x4*>(sh.src + idx);
-    for (int z = 1; z < sh.count; ++z) a += *reinterpret_cast<const f32x4*>(sh.src + size_t(z) * sh.total + idx);
-    *reinterpret_cast<f32x4*>(sh.dst + idx) = a;
-}
-
 __global__ __launch_bounds__(256) void k_bwd_finish(BwdFinishDx f, uint16_t* __restrict__ dx, int64_t dx_blocks,
                                                     Shares da, int64_t da_blocks, Shares db) {
     const int64_t b = blockIdx.x;
@@ -660,7 +609,7 @@ BwdPlan plan_bwd(int64_t T, int64_t N, int64_t K, int r, bool dense) {
 }
 
 hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* absmax, const uint16_t* wdense,
-                           const uint16_t* dy, const SavedInput& x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
+                           const uint16_t* dy, const uint16_t* x, const uint16_t* A, int64_t T, int64_t N, int64_t K,
                            int r, float s, uint16_t* dx, float* dA, float* dB, void* ws, hipStream_t stream) {
     char* w = static_cast<char*>(ws);
     // without dx only the LoRA part runs: one workgroup per tile, no contraction steps
@@ -671,16 +620,18 @@ hipError_t launch_gemm_bwd(const BwdPlan& p, const uint8_t* codes, const float* 
     float* dapart = reinterpret_cast<float*>(w + p.off_dapart);
     const BwdLora lora{reinterpret_cast<const float*>(w + p.off_gpart), p.gparts, A, x, dapart, r, s};
     if (dx) prof_gemm_begin(stream);
-    auto launch = [&](auto kernel, int threads, const void* weights) {
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, stream, dy, weights, absmax, int(T), int(N), int(K), tl, lora, dx,
-                           partial, tables());
-    };
     if (wdense)
-        launch(x.codes ? k_nf4_gemm_bwd_dx<128, true, true> : k_nf4_gemm_bwd_dx<128, true, false>, 256, wdense);
+        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<128, true>), grid, dim3(256), 0, stream, dy,
+                           static_cast<const void*>(wdense), nullptr, int(T), int(N), int(K), tl, lora, dx, partial,
+                           tables());
     else if (p.bm == 256)
-        launch(x.codes ? k_nf4_gemm_bwd_dx<256, false, true> : k_nf4_gemm_bwd_dx<256, false, false>, 512, codes);
+        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<256, false>), grid, dim3(512), 0, stream, dy,
+                           static_cast<const void*>(codes), absmax, int(T), int(N), int(K), tl, lora, dx, partial,
+                           tables());
     else
-        launch(x.codes ? k_nf4_gemm_bwd_dx<128, false, true> : k_nf4_gemm_bwd_dx<128, false, false>, 256, codes);
+        hipLaunchKernelGGL((k_nf4_gemm_bwd_dx<128, false>), grid, dim3(256), 0, stream, dy,
+                           static_cast<const void*>(codes), absmax, int(T), int(N), int(K), tl, lora, dx, partial,
+                           tables());
     if (dx) prof_gemm_end(stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

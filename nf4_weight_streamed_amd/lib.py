@@ -80,6 +80,8 @@ def _load() -> C.CDLL:
         "nf4_lora_linear_fwd_bf16_workspace": (sz, [i64, i64, i64, i32]),
         "nf4_lora_linear_fwd_bf16": (i32, [vp, i64, i64, vp, i64, vp, vp, i32, f32, vp, vp, vp, sz, vp]),
         "nf4_lora_linear_bwd_bf16_workspace": (sz, [i64, i64, i64, i32]),
+        "nf4_lora_linear_bwd_act8_workspace": (sz, [i64, i64, i64, i32]),
+        "nf4_lora_linear_bwd_bf16_act8_workspace": (sz, [i64, i64, i64, i32]),
         "nf4_lora_linear_bwd_bf16": (i32, [vp, i64, i64, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]),
         "nf4_lora_linear_bwd": (i32, [vp, vp, i64, i64, vp, vp, vp, i64, vp, vp, i32, f32, vp, vp, vp, vp, sz, vp]),
         "nf4_profile_next_gemm": (i32, [vp, vp]),
@@ -861,9 +863,17 @@ def _linear_bwd_act8(base, n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx
     return dx, dA, dB
 
 
+def bwd_act8_workspace_bytes(T: int, N: int, K: int, r: int) -> int:
+    return int(_lib.nf4_lora_linear_bwd_act8_workspace(T, N, K, r))
+
+
+def bwd_bf16_act8_workspace_bytes(T: int, N: int, K: int, r: int) -> int:
+    return int(_lib.nf4_lora_linear_bwd_bf16_act8_workspace(T, N, K, r))
+
+
 # of the sizes alone
-_bwd_ws = functools.lru_cache(maxsize=256)(bwd_workspace_bytes)
-_bwd_bf16_ws = functools.lru_cache(maxsize=256)(bwd_bf16_workspace_bytes)
+_bwd_act8_ws = functools.lru_cache(maxsize=256)(bwd_act8_workspace_bytes)
+_bwd_bf16_act8_ws = functools.lru_cache(maxsize=256)(bwd_bf16_act8_workspace_bytes)
 
 
 def lora_linear_bwd_act8(codes, absmax, x8: Act8, u, dy, A, B, alpha: float, dx=None, dA=None, dB=None, ws=None,
@@ -873,7 +883,7 @@ def lora_linear_bwd_act8(codes, absmax, x8: Act8, u, dy, A, B, alpha: float, dx=
     _need(codes, "codes", torch.uint8, (n, k // 2))
     _need(absmax, "absmax", torch.float32, (n, k // NF4_BLOCK))
     return _linear_bwd_act8((codes, absmax), n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream,
-                            _lib.nf4_lora_linear_bwd_act8, _bwd_ws)
+                            _lib.nf4_lora_linear_bwd_act8, _bwd_act8_ws)
 
 
 def lora_linear_bwd_bf16_act8(w, x8: Act8, u, dy, A, B, alpha: float, dx=None, dA=None, dB=None, ws=None,
@@ -882,7 +892,7 @@ def lora_linear_bwd_bf16_act8(w, x8: Act8, u, dy, A, B, alpha: float, dx=None, d
     n, k = _matrix(w, "w")
     _need(w, "w", torch.bfloat16, (n, k))
     return _linear_bwd_act8((w,), n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream,
-                            _lib.nf4_lora_linear_bwd_bf16_act8, _bwd_bf16_ws)
+                            _lib.nf4_lora_linear_bwd_bf16_act8, _bwd_bf16_act8_ws)
 
 
 class ResidualNorm(NamedTuple):

@@ -329,9 +329,11 @@ class NF4Stack:
         dev = "cuda"
         bf = dict(dtype=torch.bfloat16, device=dev)
         fws = lib.fwd_bf16_workspace_bytes if base.dense else lib.fwd_workspace_bytes
-        bws = lib.bwd_bf16_workspace_bytes if base.dense else lib.bwd_workspace_bytes
+        bws = [lib.bwd_bf16_workspace_bytes if base.dense else lib.bwd_workspace_bytes]
+        if self.int8:                    # some of its linears go from a checkpoint, some from bf16
+            bws.append(lib.bwd_bf16_act8_workspace_bytes if base.dense else lib.bwd_act8_workspace_bytes)
         self.ws_f = lib.workspace(max(fws(T, n, k, r) for n, k in shapes.values()))
-        self.ws_b = lib.workspace(max(bws(T, n, k, r) for n, k in shapes.values()))
+        self.ws_b = lib.workspace(max(b(T, n, k, r) for b in bws for n, k in shapes.values()))
         L = base.n_layers
         # activation sets: one per layer, or (remat) one per layer of a block, plus the
         # block-boundary hidden states

@@ -70,7 +70,7 @@ def test_linear_validation(L):
         return raw.nf4_lora_linear_bwd_bf16_act8(at(8), N, K, x, s, at(2), at(3), T, at(6), at(7), r, 32.0, at(10), at(11),
                                                  at(12), ws, ws_bytes, None)
 
-    for call, need in ((nf4, L.bwd_workspace_bytes), (dense, L.bwd_bf16_workspace_bytes)):
+    for call, need in ((nf4, L.bwd_act8_workspace_bytes), (dense, L.bwd_bf16_act8_workspace_bytes)):
         _err(L, call(K=100), L.NF4_E_SHAPE, "K=100")
         _err(L, call(N=100), L.NF4_E_SHAPE, "N=100")
         _err(L, call(T=(1 << 23) + 1), L.NF4_E_SHAPE, "T")

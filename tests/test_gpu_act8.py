@@ -7,7 +7,7 @@ import torch
 
 import oracle as O
 import synthetic_inputs as S
-from helpers import bits_of, check_linear, half_ulp_bf16, linear_mags, to_dev_bf16
+from helpers import bits_of, check_bf16_output, check_linear, half_ulp_bf16, linear_mags, to_dev_bf16
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -172,7 +172,8 @@ def _linear_inputs(t, n, k, r, seed=0):
 
 
 LINEARS = [(1, 128, 128, 16), (5, 3584, 512, 16), (17, 256, 704, 5), (32, 1024, 256, 64), (33, 128, 192, 8),
-           (130, 272, 320, 16), (257, 1104, 1024, 16), (300, 256, 4160, 33), (512, 512, 18944, 16)]
+           (130, 272, 320, 16), (257, 1104, 1024, 16), (300, 256, 4160, 33), (512, 512, 18944, 16),
+           (520, 128, 16512, 40), (1024, 64, 16384, 16), (1030, 1040, 16448, 64)]
 
 
 def _check_adapter(dA, dB, x, u, case, r, what):
@@ -191,26 +192,30 @@ def _check_adapter(dA, dB, x, u, case, r, what):
 
 @pytest.mark.parametrize("dense", [False, True])
 @pytest.mark.parametrize("t,n,k,r", LINEARS)
-def test_linear_beside_the_call_on_the_values(gpu_lib, t, n, k, r, dense):
-    """dX is bit for bit that of the bf16 call: it does not read the checkpoint. dA and dB against fp64."""
+def test_linear_element_by_element(gpu_lib, t, n, k, r, dense):
+    """dX, dA and dB against fp64 on the base's and the checkpoint's values, and the same twice."""
     lib = gpu_lib
     case, d = _linear_inputs(t, n, k, r)
     x8 = _act8(lib, case["x"])
     u = torch.randn(t, r, device="cuda")
     if dense:
-        base, old, new = (d["W"],), lib.lora_linear_bwd_bf16, lib.lora_linear_bwd_bf16_act8
+        base, call, w = (d["W"],), lib.lora_linear_bwd_bf16_act8, d["W"]
     else:
-        base, old, new = lib.quantize(d["W"]), lib.lora_linear_bwd, lib.lora_linear_bwd_act8
-    values = lib.act8_dequantize(x8)
-    want = old(*base, values, u, d["dY"], d["A"], d["B"], 32.0)[0]
-    dx, dA, dB = new(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
-    assert torch.equal(dx, want)
-    _check_adapter(dA, dB, bits_of(values), u.cpu().numpy(), case, r, "with dx")
-    again = new(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
-    assert all(torch.equal(a, b) for a, b in zip(again, (dx, dA, dB)))
-    dx, dA, dB = new(*base, x8, u, d["dY"], d["A"], d["B"], 32.0, need_dx=False)
-    assert dx is None
-    _check_adapter(dA, dB, bits_of(values), u.cpu().numpy(), case, r, "without dx")
+        base, call = lib.quantize(d["W"]), lib.lora_linear_bwd_act8
+        w = lib.dequantize(*base)
+    values = bits_of(lib.act8_dequantize(x8))
+    dx, dA, dB = call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
+    dy, wv, a, b = (O.bf16_bits_to_f64(v) for v in (case["dY"], bits_of(w), case["A"], case["B"]))
+    f = 32.0 / r
+    # N additions of dY W or dY B and r of g A; the helper has the slack of s.g in two bf16 parts
+    check_bf16_output(bits_of(dx), dy @ wv + f * (dy @ b) @ a, "dx",
+                      mag=np.abs(dy) @ np.abs(wv) + f * (np.abs(dy) @ np.abs(b)) @ np.abs(a), terms=n + r)
+    _check_adapter(dA, dB, values, u.cpu().numpy(), case, r, "with dx")
+    again = call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
+    assert all(torch.equal(p, q) for p, q in zip(again, (dx, dA, dB)))
+    none, dA, dB = call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0, need_dx=False)
+    assert none is None
+    _check_adapter(dA, dB, values, u.cpu().numpy(), case, r, "without dx")
 
 
 @pytest.mark.parametrize("t,n,k,r", [(1, 128, 128, 16), (20, 256, 704, 5), (130, 272, 320, 16), (600, 256, 1088, 16)])
@@ -229,13 +234,41 @@ def test_linear_against_oracle(gpu_lib, t, n, k, r):
     check_linear({"dx": bits_of(dx), "dA": dA.cpu().numpy(), "dB": dB.cpu().numpy()}, refs, mags, t, n, k, r, "act8")
 
 
-def test_linear_without_adapter(gpu_lib):
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("t,n,k", [(3, 64, 192), (33, 128, 320), (140, 1040, 1088), (300, 128, 4160), (1100, 64, 16448)])
+def test_linear_writes_nothing_else(gpu_lib, t, n, k, dense):
+    """What lies before and behind dX, dA, dB and the workspace stays."""
     lib = gpu_lib
-    _, d = _linear_inputs(40, 256, 128, 16)
-    codes, absmax = lib.quantize(d["W"])
-    dx, dA, dB = lib.lora_linear_bwd_act8(codes, absmax, None, None, d["dY"], None, None, 32.0)
-    want, _, _ = lib.lora_linear_bwd(codes, absmax, None, None, d["dY"], None, None, 32.0)
-    assert dA is None and dB is None and torch.equal(dx, want)
+    _, d = _linear_inputs(t, n, k, 16)
+    base = (d["W"],) if dense else lib.quantize(d["W"])
+    call, ws = ((lib.lora_linear_bwd_bf16_act8, lib.bwd_bf16_act8_workspace_bytes) if dense
+                else (lib.lora_linear_bwd_act8, lib.bwd_act8_workspace_bytes))
+    u = torch.randn(t, 16, device="cuda")
+    x8 = lib.act8_quantize(d["x"])
+    want = call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
+    outs, views = [], []
+    for shape, dtype in (((t, k), torch.bfloat16), ((16, k), torch.float32), ((n, 16), torch.float32), ((ws(t, n, k, 16),), torch.uint8)):
+        size, pad = int(np.prod(shape)), 1 << 18
+        buf = torch.full((size + 2 * pad,), 7, dtype=dtype, device="cuda")
+        outs.append((buf, pad, size))
+        views.append(buf[pad:pad + size].view(shape))
+    call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0, dx=views[0], dA=views[1], dB=views[2], ws=views[3])
+    assert all(torch.equal(a, b) for a, b in zip(views, want))
+    for buf, pad, size in outs:
+        assert torch.all(buf[:pad] == 7) and torch.all(buf[pad + size:] == 7)
+
+
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("t", [3, 40, 300])
+def test_linear_without_adapter(gpu_lib, t, dense):
+    lib = gpu_lib
+    case, d = _linear_inputs(t, 256, 128, 16)
+    base = (d["W"],) if dense else lib.quantize(d["W"])
+    call = lib.lora_linear_bwd_bf16_act8 if dense else lib.lora_linear_bwd_act8
+    dx, dA, dB = call(*base, None, None, d["dY"], None, None, 32.0)
+    w, dy = O.bf16_bits_to_f64(bits_of(d["W"] if dense else lib.dequantize(*base))), O.bf16_bits_to_f64(case["dY"])
+    assert dA is None and dB is None
+    check_bf16_output(bits_of(dx), dy @ w, "dx", mag=np.abs(dy) @ np.abs(w), terms=256)
 
 
 def test_linear_non_finite_block_reaches_its_columns(gpu_lib):
@@ -328,7 +361,7 @@ def _step_state(lib, t, c, n, seed):
     s["codes"], s["absmax"] = lib.quantize(normal(n, c))
     s["lu"] = torch.randn(t, 16, generator=g, device="cuda")
     s["dA"], s["dB"] = torch.empty(16, c, device="cuda"), torch.empty(n, 16, device="cuda")
-    s["ws"] = lib.workspace(lib.bwd_workspace_bytes(t, n, c, 16))
+    s["ws"] = lib.workspace(lib.bwd_act8_workspace_bytes(t, n, c, 16))
     return s
 
 
