@@ -159,8 +159,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_act8_adapter(const float* __res
             f32x4 d = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ts = 0; ts < kBT / 32; ++ts) {
-                const int tt = 32 * ts + t8;
-                const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[(16 * wave + l16) * kTP + (tt ^ ((16 * wave + l16) & ~7))]));
+                const int tt = 32 * ts + t8, c = 16 * wave + l16;
+                const bf16x8 xa = as_bf16x8(*reinterpret_cast<const u32x4*>(&sxt[c * kTP + (tt ^ (c & ~7))]));
                 const int g = (16 * jb + l16) * kTP + tt;
                 d = mfma16x16x32(xa, as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_hi[g])), d);
                 d = mfma16x16x32(xa, as_bf16x8(*reinterpret_cast<const u32x4*>(&sg_lo[g])), d);
@@ -285,7 +285,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_bwd_act8(const uint16_t* _
         for (int j = 0; j < FK; ++j)
             bw[set][j] = lds_frag_tr(wt + w_at[j][0] + 32 * kBK * kk, wt + w_at[j][1] + 32 * kBK * kk);
 #pragma unroll
-        for (int i = 0; i < FM; ++i) af[set][i] = as_bf16x8(*reinterpret_cast<const u32x4*>(at + (a_at ^ uint32_t(kk << 5)) + 32 * 128 * i));
+        for (int i = 0; i < FM; ++i)
+            af[set][i] = as_bf16x8(*reinterpret_cast<const u32x4*>(at + (a_at ^ uint32_t(kk << 5)) + 32 * 128 * i));
     };
     auto multiply = [&](int set) {
 #pragma unroll

@@ -8,6 +8,7 @@ There is no fallback: if the library is missing, importing this module raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import functools
 import os
@@ -836,7 +837,7 @@ def silu_mul_bwd_act8(gate8: Act8, up8: Act8, dm, dgate=None, dup=None, stream=N
 
 
 def _linear_bwd_act8(base, n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx, stream, call, ws_bytes):
-    """The two calls below after their base tensors' checks."""
+    """The two calls below after their base tensors' checks. No tokens leave zero gradients."""
     t = _matrix(dy, "dy")[0]
     r = 0 if A is None else A.shape[0]
     _need(dy, "dy", torch.bfloat16, (t, n))
@@ -849,6 +850,9 @@ def _linear_bwd_act8(base, n, k, x8, u, dy, A, B, alpha, dx, dA, dB, ws, need_dx
         dB = _empty((n, r), torch.float32, dy.device, stream) if dB is None else dB
         _need(dA, "dA", torch.float32, (r, k))
         _need(dB, "dB", torch.float32, (n, r))
+        if t == 0:
+            with contextlib.nullcontext() if stream is None else torch.cuda.stream(_as_stream(stream)):
+                dA.zero_(), dB.zero_()
     else:
         x8, u, A, B, dA, dB = Act8(None, None), None, None, None, None, None
     if need_dx and dx is None:
@@ -924,6 +928,8 @@ def _norm_params(t, c, post_norm, post_gain, gate, gain) -> int:
         _need(gain, "gain", torch.bfloat16, (c,))
     if gate is None:
         return NF4_GATE_NONE
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
     _need(gate, "gate", torch.bfloat16, (c,) if gate.dim() == 1 else (t, c))
     return NF4_GATE_CHANNEL if gate.dim() == 1 else NF4_GATE_TOKEN
 
@@ -978,8 +984,9 @@ def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=Non
                       stream=None) -> ResidualNormGrads:
     """Backward of residual_norm_fwd. dn: the gradient of n, or a list of up to three (one for each of
     its readers, added in fp32); dres: the gradient that reaches the stream past the norm; the stream as h
-    (the forward's result) or, without a gain, as n's checkpoint n8. With o (the block's output) the
-    branch's gradients come too: do, and dgate (bf16 [T, H], or float32 [H] for a gate a channel).
+    (the forward's result) or, without a gain, as n's checkpoint n8. With o (the block's output; leave it
+    out where nothing but dh and dgain is needed, as for a plain residual, whose do is dh) the branch's
+    gradients come too: do, and dgate (bf16 [T, H], or float32 [H] for a gate a channel).
     param_grads=False leaves out those of the gains and the gate (frozen parameters)."""
     dn = [dn] if isinstance(dn, torch.Tensor) else list(dn)
     if not 1 <= len(dn) <= 3:

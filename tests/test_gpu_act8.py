@@ -171,7 +171,8 @@ def _linear_inputs(t, n, k, r, seed=0):
     return case, d
 
 
-LINEARS = [(1, 128, 128, 16), (5, 3584, 512, 16), (17, 256, 704, 5), (32, 1024, 256, 64), (33, 128, 192, 8),
+LINEARS = [(1, 16, 64, 1), (1, 128, 128, 16), (5, 3584, 512, 16), (17, 256, 704, 5), (32, 1024, 256, 64),
+           (33, 128, 192, 8), (34, 16, 64, 1), (200, 48, 64, 64),
            (130, 272, 320, 16), (257, 1104, 1024, 16), (300, 256, 4160, 33), (512, 512, 18944, 16),
            (520, 128, 16512, 40), (1024, 64, 16384, 16), (1030, 1040, 16448, 64)]
 
@@ -247,7 +248,8 @@ def test_linear_writes_nothing_else(gpu_lib, t, n, k, dense):
     x8 = lib.act8_quantize(d["x"])
     want = call(*base, x8, u, d["dY"], d["A"], d["B"], 32.0)
     outs, views = [], []
-    for shape, dtype in (((t, k), torch.bfloat16), ((16, k), torch.float32), ((n, 16), torch.float32), ((ws(t, n, k, 16),), torch.uint8)):
+    for shape, dtype in (((t, k), torch.bfloat16), ((16, k), torch.float32), ((n, 16), torch.float32),
+                         ((ws(t, n, k, 16),), torch.uint8)):
         size, pad = int(np.prod(shape)), 1 << 18
         buf = torch.full((size + 2 * pad,), 7, dtype=dtype, device="cuda")
         outs.append((buf, pad, size))
@@ -269,6 +271,18 @@ def test_linear_without_adapter(gpu_lib, t, dense):
     w, dy = O.bf16_bits_to_f64(bits_of(d["W"] if dense else lib.dequantize(*base))), O.bf16_bits_to_f64(case["dY"])
     assert dA is None and dB is None
     check_bf16_output(bits_of(dx), dy @ w, "dx", mag=np.abs(dy) @ np.abs(w), terms=256)
+
+
+@pytest.mark.parametrize("dense", [False, True])
+def test_linear_no_tokens(gpu_lib, dense):
+    lib = gpu_lib
+    _, d = _linear_inputs(2, 64, 128, 16)
+    base = (d["W"],) if dense else lib.quantize(d["W"])
+    call = lib.lora_linear_bwd_bf16_act8 if dense else lib.lora_linear_bwd_act8
+    dA, dB = torch.full((16, 128), 7.0, device="cuda"), torch.full((64, 16), 7.0, device="cuda")
+    dx, dA, dB = call(*base, lib.act8_quantize(d["x"][:0]), torch.zeros(0, 16, device="cuda"), d["dY"][:0], d["A"], d["B"], 32.0,
+                      dA=dA, dB=dB)
+    assert dx.shape == (0, 128) and not torch.any(dA) and not torch.any(dB)
 
 
 def test_linear_non_finite_block_reaches_its_columns(gpu_lib):

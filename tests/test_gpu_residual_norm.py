@@ -279,6 +279,43 @@ def test_no_rows(gpu_lib):
         assert s.shape == (128,) and torch.all(s == 0)
 
 
+@pytest.mark.parametrize("block", [False, True])
+def test_more_rows_than_workgroups(gpu_lib, block):
+    """A row a workgroup, and past 2^21 of them: each takes several, in registers of their own."""
+    lib, t, c = gpu_lib, (1 << 21) + 77, 520
+    h = torch.randn(1, c, device="cuda").to(torch.bfloat16).repeat(t, 1)
+    h[-80:] = torch.randn(80, c, device="cuda").to(torch.bfloat16)
+    o = h if block else None
+    r = lib.residual_norm_fwd(h, o, scale=0.5)
+    for rows in (slice(0, 64), slice(-80, None)):
+        want = lib.residual_norm_fwd(h[rows].contiguous(), h[rows].contiguous() if block else None, scale=0.5)
+        assert torch.equal(r.n[rows], want.n) and torch.equal(r.rstd[rows], want.rstd) and torch.equal(r.h[rows], want.h)
+    assert torch.equal(r.n[:-80].amax(0), r.n[0]) and torch.equal(r.n[:-80].amin(0), r.n[0])
+    g = lib.residual_norm_bwd(r.n, r.rstd, h=r.h)
+    for rows in (slice(0, 64), slice(-80, None)):
+        want = lib.residual_norm_bwd(r.n[rows].contiguous(), r.rstd[rows].contiguous(), h=r.h[rows].contiguous())
+        assert torch.equal(g.dh[rows], want.dh)
+    assert torch.equal(g.dh[:-80].amax(0), g.dh[0]) and torch.equal(g.dh[:-80].amin(0), g.dh[0])
+
+
+@pytest.mark.parametrize("t,c", [(5, 64), (130, 576), (40, 4096), (3, 12288)])
+def test_checkpoint_beside_tensors_off_alignment(gpu_lib, t, c):
+    """bf16 tensors at 2 bytes past 16, the checkpoint aligned: the same results."""
+    lib = gpu_lib
+
+    def off(x):
+        return torch.cat([torch.zeros(1, dtype=x.dtype, device="cuda"), x.flatten()])[1:].view(x.shape)
+
+    h, o, d = (torch.randn(t, c, device="cuda").to(torch.bfloat16) for _ in range(3))
+    want = lib.residual_norm_fwd(h, o, post_norm=True, checkpoint=True)
+    got = lib.residual_norm_fwd(off(h), off(o), post_norm=True, checkpoint=True, n=off(torch.empty_like(h)))
+    for a, b in zip((got.h, got.n, *got.n8, got.rstd, got.rstd_o), (want.h, want.n, *want.n8, want.rstd, want.rstd_o)):
+        assert torch.equal(a, b)
+    want = lib.residual_norm_bwd(d, want.rstd, n8=want.n8, dres=h, o=o, post_norm=True, rstd_o=want.rstd_o)
+    got = lib.residual_norm_bwd(off(d), got.rstd, n8=got.n8, dres=off(h), o=off(o), post_norm=True, rstd_o=got.rstd_o)
+    assert torch.equal(got.dh, want.dh) and torch.equal(got.do, want.do)
+
+
 def test_rows_past_32_bits(gpu_lib):
     """270000 rows of 16384 (over 8 GiB): the last rows equal a call on them alone."""
     lib, t, c, n = gpu_lib, 270000, 16384, 5
@@ -350,6 +387,9 @@ def test_other_stream(gpu_lib):
 
 def test_refusals(gpu_lib):
     lib = gpu_lib
+    with pytest.raises(TypeError, match="gate"):
+        lib.residual_norm_fwd(torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"),
+                              torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda"), gate=0.5)
     h = torch.randn(8, 128, device="cuda").to(torch.bfloat16)
     v = torch.ones(128, dtype=torch.bfloat16, device="cuda")
     rstd = torch.ones(8, device="cuda")
