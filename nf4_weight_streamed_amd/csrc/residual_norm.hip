@@ -40,7 +40,10 @@ struct Place {
 
 // A thread's octets of one row, zeros past its end. Rows of whole, aligned 16-byte pieces go through
 // a descriptor over the row, which also stands for an absent tensor (p NULL: zeros, nothing stored)
-// without a branch, so that the loads of a row are issued back to back. kRagged: any others.
+// without a branch, so that the loads of a row are issued back to back. kRagged: any others, by loads at
+// 2-byte alignment that stay within the row: octets that pass its end are loaded from its last whole one, and
+// `settle` moves them into place, later, where they are used (with a branch at each octet that is not whole, and
+// elements loaded one by one, 4096 x 3583 backward with everything takes 185 us instead of 80).
 struct __attribute__((packed, aligned(2))) LooseOctet {
     u32x4 w;
 };
@@ -53,18 +56,33 @@ __device__ __forceinline__ void load_line(const uint16_t* p, int64_t base, int H
         for (int n = 0; n < N; ++n) x[n] = kStream ? buf_load16_nt(r, uint32_t(pl.at(n)) * 2u) : buf_load16(r, uint32_t(pl.at(n)) * 2u);
     } else {
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int at = pl.at(n);
-            x[n] = u32x4{0, 0, 0, 0};
-            if (!p) continue;
-            if (at + 8 <= H) {
-                x[n] = reinterpret_cast<const LooseOctet*>(p + base + at)->w;
-                continue;
-            }
+        for (int n = 0; n < N; ++n) x[n] = u32x4{0, 0, 0, 0};
+        if (!p) return;
+        if (H >= 8) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (at + e < H) x[n][e / 2] |= uint32_t(p[base + at + e]) << (16 * (e % 2));
+            for (int n = 0; n < N; ++n) x[n] = reinterpret_cast<const LooseOctet*>(p + base + min(pl.at(n), H - 8))->w;
+        } else if (pl.t == 0) {  // a row's elements where an octet that ends with it has them
+#pragma unroll
+            for (int e = 1; e < 8; ++e)
+                if (e >= 8 - H) x[0][e / 2] |= uint32_t(p[base + e - (8 - H)]) << (16 * (e % 2));
         }
+    }
+}
+
+template <bool kRagged, int N, bool kWave>
+__device__ __forceinline__ void settle(int H, const Place<kWave>& pl, u32x4 (&x)[N]) {
+    if constexpr (!kRagged) return;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int by = max(0, pl.at(n) - (H - 8));  // elements that lie before the octet
+        if (!__ballot(by > 0)) continue;
+        u32x4 y = x[n];
+        if (by & 2) y = u32x4{y[1], y[2], y[3], 0};
+        if (by & 4) y = u32x4{y[2], y[3], 0, 0};
+        if (by & 1)
+            y = u32x4{__builtin_amdgcn_alignbit(y[1], y[0], 16), __builtin_amdgcn_alignbit(y[2], y[1], 16),
+                      __builtin_amdgcn_alignbit(y[3], y[2], 16), y[3] >> 16};
+        x[n] = by >= 8 ? u32x4{0, 0, 0, 0} : y;
     }
 }
 
@@ -175,12 +193,15 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_fwd(FwdArgs a) {
     auto load = [&](int row) { a.stream ? load_as(row, std::true_type{}) : load_as(row, std::false_type{}); };
     u32x4 fw[N], pw[kBlock > 1 ? N : 1];  // the same for all rows
     if (p.first < a.T) load(p.first);
-    if constexpr (kBlock > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw);
+    if constexpr (kBlock > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw), settle<kRagged>(H, p, pw);
     load_line<kRagged>(a.gain, 0, H, p, fw);
+    settle<kRagged>(H, p, fw);
     for (int row = p.first; row < a.T; row += p.step) {
         const int64_t base = int64_t(row) * H;
         if (!kAhead && row != p.first) load(row);
-        const auto in = next;
+        auto in = next;
+        if constexpr (kBlock > 0) settle<kRagged>(H, p, in.o), settle<kRagged>(H, p, in.gate);
+        settle<kRagged>(H, p, in.h);
         u32x4 out[N];
         if (kAhead && row + p.step < a.T) load(row + p.step);
         float s[N][8];
@@ -352,11 +373,18 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
     u32x4 fw[N], pw[kBranch > 1 ? N : 1];  // the same for all rows
     if (p.first < a.T) load_row<N, kRagged>(a, p, p.first, next);
     load_line<kRagged>(a.gain, 0, H, p, fw);
-    if constexpr (kBranch > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw);
+    settle<kRagged>(H, p, fw);
+    if constexpr (kBranch > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw), settle<kRagged>(H, p, pw);
     for (int row = p.first; row < a.T; row += p.step) {
         const int64_t base = int64_t(row) * H;
         if (!kAhead && row != p.first) load_row<N, kRagged>(a, p, row, next);
-        const RowIn<N, kBranch> in = next;
+        RowIn<N, kBranch> in = next;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            if (i < a.n_dn) settle<kRagged>(H, p, in.d[i]);
+        if (!a.codes) settle<kRagged>(H, p, in.h);
+        settle<kRagged>(H, p, in.res);
+        if constexpr (kBranch > 0) settle<kRagged>(H, p, in.o), settle<kRagged>(H, p, in.gate);
         float g[N][8], b[N][8];
         u32x4 out[N];
 #pragma unroll
@@ -623,8 +651,11 @@ struct Bwd {
 };
 
 // Workgroups of a row, or of four rows of a wave each. loop: as many as the card holds.
-unsigned rows_grid(int64_t T, int64_t H, bool loop) {
+unsigned rows_grid(int64_t T, int64_t H, bool loop, bool ragged) {
     const Split p = split_of(H);
+    // (at two octets a thread of ragged rows the next row's loads cost registers: 2000 x 7001 47 -> 54 us; at one
+    // they gain: 8192 x 1021, a gate a token, 21.4 -> 19.4)
+    loop = loop && !(ragged && p.octets == 2);
     const int64_t most = loop ? (p.octets == 2 ? 131072 : 262144) / std::min(p.threads, kRows) : kMaxGrid;
     return unsigned(std::min(cdiv(T, p.kind == kWaveRows ? 4 : 1), most));
 }
@@ -670,7 +701,7 @@ extern "C" int nf4_residual_norm_fwd(const uint16_t* h, const uint16_t* o, int64
     const FwdArgs a{h, o, post_gain, gate, gain, h_out, n, n_codes, n_scale, rstd_o, rstd, int(T), int(H), gate_kind,
                     large, scale, gain_offset, eps};
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const unsigned grid = rows_grid(T, H, post_norm && !ragged);
+    const unsigned grid = rows_grid(T, H, post_norm, ragged);
     if (!o)
         launch<Fwd<0>::Kernel>(a, H, ragged, grid, s);
     else if (!post_norm)
@@ -750,7 +781,7 @@ extern "C" int nf4_residual_norm_bwd(const uint16_t* const* dn, int n_dn, const 
     a.n_dn = n_dn, a.stream = all * (n_dn + 3 + (branch ? 2 : 0)) > kLastLevelCache, a.scale = scale, a.offset = gain_offset;
     hipStream_t s = static_cast<hipStream_t>(stream);
     const int64_t groups = T > 0 ? sum_groups(T, H) : 0;
-    const unsigned grid = sums ? unsigned(groups) : rows_grid(T, H, branch && post_norm && !ragged);
+    const unsigned grid = sums ? unsigned(groups) : rows_grid(T, H, branch && post_norm, ragged);
     const int kind = !branch ? 0 : post_norm ? 2 : 1;
     if (T > 0 && sums) {
         if (kind == 0)

@@ -235,6 +235,23 @@ def test_in_place(gpu_lib):
     assert torch.equal(k.dh, g.dh) and torch.equal(k.do, g.do)
 
 
+@pytest.mark.parametrize("c", [5, 100, 333, 1001, 4099, 8191])
+def test_in_place_odd_widths(gpu_lib, c):
+    """Rows whose last octet is not whole, several a workgroup, results over their inputs."""
+    lib, t = gpu_lib, 3000
+    h, o, d, e = (torch.randn(t, c, device="cuda").to(torch.bfloat16) for _ in range(4))
+    gate = torch.randn(t, c, device="cuda").to(torch.bfloat16)
+    want = lib.residual_norm_fwd(h, o, post_norm=True, gate=gate)
+    h2, o2 = h.clone(), o.clone()
+    got = lib.residual_norm_fwd(h2, o2, post_norm=True, gate=gate, h_out=h2, n=o2)
+    assert all(torch.equal(getattr(got, n), getattr(want, n)) for n in ("h", "n", "rstd", "rstd_o"))
+    args = dict(h=want.h, dres=e, post_norm=True, rstd_o=want.rstd_o, gate=gate)
+    ref = lib.residual_norm_bwd(d, want.rstd, o=o, **args)
+    d2, o2 = d.clone(), o.clone()
+    g = lib.residual_norm_bwd(d2, want.rstd, o=o2, dh=d2, do=o2, **args)
+    assert torch.equal(g.dh, ref.dh) and torch.equal(g.do, ref.do) and torch.equal(g.dgate, ref.dgate)
+
+
 def test_non_finite_rows_stay_alone(gpu_lib):
     lib = gpu_lib
     p = _case(9, 192, True, "token", False)
