@@ -247,15 +247,17 @@ int stream_pool_streams(nf4_stream* compute_out, nf4_stream* copy_out) {
         return fail(NF4_E_ARG, "stream_pool_streams: device %d beyond the %d the library tracks", dev, kMaxDevices);
     std::lock_guard<std::mutex> lock(mu);
     if (!pairs[dev][0]) {
-        // back to back, so that HIP gives them different hardware queues
-        hipStream_t c = nullptr, k = nullptr;
-        st = hip_ok(hipStreamCreateWithFlags(&c, hipStreamNonBlocking), "stream_pool_streams: create compute stream");
-        if (st == NF4_OK)
-            st = hip_ok(hipStreamCreateWithFlags(&k, hipStreamNonBlocking), "stream_pool_streams: create copy stream");
-        if (st != NF4_OK) {
-            if (c) (void)hipStreamDestroy(c);
-            return st;
-        }
+        // HIP puts a new stream on the hardware queue that has the fewest. Back to back, two are on different
+        // ones where the queues are level; where streams made and destroyed before left one short, both
+        // would join it. So several are made first, which levels the queues, and the last two kept.
+        constexpr int kMade = 16;
+        hipStream_t made[kMade] = {};
+        for (int i = 0; i < kMade && st == NF4_OK; ++i)
+            st = hip_ok(hipStreamCreateWithFlags(&made[i], hipStreamNonBlocking), "stream_pool_streams: create streams");
+        for (int i = 0; i < kMade - 2 || (st != NF4_OK && i < kMade); ++i)
+            if (made[i]) (void)hipStreamDestroy(made[i]);
+        if (st != NF4_OK) return st;
+        const hipStream_t c = made[kMade - 2], k = made[kMade - 1];
         pairs[dev][0] = c;
         pairs[dev][1] = k;
     }
