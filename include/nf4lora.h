@@ -592,7 +592,8 @@ int stream_pool_create(const nf4_host_block* blocks, int n_blocks, void* device_
  * compute then run one after the other (measured: 66 ms against 41 ms for 8 blocks
  * of 256 MiB, for every fourth stream created). The two streams are created one right
  * after the other, non-blocking, at the default priority, on the first call for a
- * device, so they take different queues, and are kept until the process ends; later
+ * device, after others that level the queues and are destroyed, so they take different
+ * queues, and are kept until the process ends; later
  * calls return the same pair. Errors: NF4_E_ARG for NULL arguments, NF4_E_HIP if a
  * stream cannot be created.
  */

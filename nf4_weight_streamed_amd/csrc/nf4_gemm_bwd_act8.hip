@@ -236,8 +236,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gemm_bwd_act8(const uint16_t* _
         l.s = buf_load_f32(rsc, (n * uint32_t(K / 64) + k / 64) * 4u);
     };
     // ... and stores them as bf16: the 16 scaled levels once, as two tables of bytes in registers, then a
-    // byte permute of each table's halves for four codes at a time. (From a table in LDS, whose random
-    // reads meet in banks, the lookups take more LDS cycles than the products' operands.)
+    // byte permute of each table's halves for four codes at a time: no reads of LDS, which the products'
+    // operands keep busy
     uint32_t lo[4], hi[4];
     auto scale_levels = [&](float scale) {
 #pragma unroll
