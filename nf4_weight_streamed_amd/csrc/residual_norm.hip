@@ -12,6 +12,9 @@
 // written once; that traffic is the bound. All arithmetic is fp32. Sums over rows (gains, a
 // gate a channel) are kept per column in registers over a workgroup's rows, then added over
 // the workgroups by a second kernel, in a fixed order.
+// Measured, 8192 x 8192 (what it has to move): norm alone 46 us (5.8 TB/s), add 88 (6.1), both norms, a gate a
+// channel and the checkpoint 97 (6.3); backward of one reader 87 (6.2), both norms, a gate a token, three readers
+// and the gains' sums 233 (5.8). 4096 x 16384 the same 269 (5.0), 4096 x 3583 80 (3.7), 2731 x 5120 60 (4.6).
 #include <cmath>
 
 #include "../../include/nf4lora.h"
@@ -125,6 +128,11 @@ __device__ __forceinline__ float lane_sum(float v) {
 // Threads of a workgroup by the widths it takes: 256, a wave a row, up to 512 elements; up to 512, a row
 // of at most 8192; up to 1024 for wider ones.
 constexpr int kWaveRows = 256, kRows = 512, kWideRows = 1024;
+// With a branch's sums over rows, wide rows take four octets a thread of half as many threads: what a thread holds
+// besides its octets it holds once (1024 x 12288, gains and a gate a channel, 57 us against 62 at two, a gate a token
+// and three readers 69 against 79; 4096 x 16384 193 against 201, 269 against 275).
+constexpr int kManyOctets = 4;
+__host__ __device__ constexpr int threads_of(int kind, int octets) { return octets == kManyOctets ? kind / 2 : kind; }
 constexpr int kMaxWaves = 16;  // of a workgroup
 
 // Sum over a row's threads - a wave's lanes, or the whole workgroup - in a fixed order. Two slots
@@ -326,10 +334,12 @@ __device__ __forceinline__ void load_row(const BwdArgs& a, const Place<kWave>& p
 }
 
 // kBranch: gradients of the block's side are wanted, 2 with its norm. kSums: sums over rows are; a
-// workgroup then takes many rows, and the next row's loads are under way while a row is reduced.
-template <int N, bool kRagged, int kThreads, int kBranch, bool kSums>
-__global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
-    constexpr bool kWave = kThreads == kWaveRows, kWide = kThreads == kWideRows;
+// workgroup then takes many rows, and (but for wide ones, which fill the registers) the next row's loads are
+// under way while a row is reduced. kRowKind: kWaveRows, kRows or kWideRows.
+template <int N, bool kRagged, int kRowKind, int kBranch, bool kSums>
+__global__ __launch_bounds__(threads_of(kRowKind, N)) void k_residual_norm_bwd(BwdArgs a) {
+    constexpr bool kWave = kRowKind == kWaveRows, kWide = kRowKind == kWideRows;
+    constexpr int kThreads = threads_of(kRowKind, N);
     constexpr bool kAhead = (kSums || kBranch > 1) && !kWide;
     constexpr int kKinds = !kSums ? 1 : kBranch ? 3 : 1;
     __shared__ float slots[2][kMaxWaves];
@@ -337,8 +347,8 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
     const Place<kWave> p;
     const int H = a.H;
     const float mean = 1.0f / float(H);
-    // the sums over rows: dgain, and with a branch dpost_gain and dgate. At four octets a thread the
-    // latter two are kept in LDS (in registers, which they overflow, 4096 rows of 16384 took 792 us)
+    // the sums over rows: dgain, and with a branch dpost_gain and dgate. Of wide rows the latter two are
+    // kept in LDS
     constexpr bool kInLds = kKinds > 1 && kWide;
     constexpr int kHeld = kInLds ? 1 : kKinds;
     float acc[kHeld][N][8];
@@ -371,13 +381,15 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
     }
     RowIn<N, kBranch> next;
     u32x4 fw[N], pw[kBranch > 1 ? N : 1];  // the same for all rows
-    if (p.first < a.T) load_row<N, kRagged>(a, p, p.first, next);
-    load_line<kRagged>(a.gain, 0, H, p, fw);
-    settle<kRagged>(H, p, fw);
-    if constexpr (kBranch > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw), settle<kRagged>(H, p, pw);
+    if (kAhead && p.first < a.T) load_row<N, kRagged>(a, p, p.first, next);
+    auto load_gain = [&]() { load_line<kRagged>(a.gain, 0, H, p, fw), settle<kRagged>(H, p, fw); };
+    auto load_post_gain = [&]() {
+        if constexpr (kBranch > 1) load_line<kRagged>(a.post_gain, 0, H, p, pw), settle<kRagged>(H, p, pw);
+    };
+    if constexpr (!kInLds) load_gain(), load_post_gain();
     for (int row = p.first; row < a.T; row += p.step) {
         const int64_t base = int64_t(row) * H;
-        if (!kAhead && row != p.first) load_row<N, kRagged>(a, p, row, next);
+        if constexpr (!kAhead) load_row<N, kRagged>(a, p, row, next);
         RowIn<N, kBranch> in = next;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
@@ -407,6 +419,9 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
             }
         }
         if (kAhead && row + p.step < a.T) load_row<N, kRagged>(a, p, row + p.step, next);
+        // gains of wide rows where they are used: held over the rows, and unpacked there, they overflow the
+        // registers (4096 x 16384, gains and a gate a channel, 464 us)
+        if constexpr (kInLds) load_gain();
         float dot = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -419,6 +434,7 @@ __global__ __launch_bounds__(kThreads) void k_residual_norm_bwd(BwdArgs a) {
                 dot = __builtin_fmaf(g[n][e], b[n][e], dot);
             }
         }
+        if constexpr (kInLds) load_post_gain();
         const float c = row_sum(dot) * mean;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
@@ -623,15 +639,16 @@ struct Buffers {
 };
 
 // kernel<octets a thread, ragged, kind of rows>, picked by width and alignment.
-template <template <int, bool, int> class Kernel, typename Args>
+template <int kWideOctets, template <int, bool, int> class Kernel, typename Args>
 void launch(const Args& a, int64_t H, bool ragged, unsigned grid, hipStream_t s) {
     const Split p = split_of(H);
     const auto kernel =
         p.kind == kWaveRows   ? (ragged ? Kernel<1, true, kWaveRows>::get() : Kernel<1, false, kWaveRows>::get())
-        : p.kind == kWideRows ? (ragged ? Kernel<2, true, kWideRows>::get() : Kernel<2, false, kWideRows>::get())
+        : p.kind == kWideRows ? (ragged ? Kernel<kWideOctets, true, kWideRows>::get() : Kernel<kWideOctets, false, kWideRows>::get())
         : p.octets == 1       ? (ragged ? Kernel<1, true, kRows>::get() : Kernel<1, false, kRows>::get())
                               : (ragged ? Kernel<2, true, kRows>::get() : Kernel<2, false, kRows>::get());
-    hipLaunchKernelGGL(kernel, dim3(grid), dim3(p.threads), 0, s, a);
+    const int threads = p.kind == kWideRows ? int(cdiv(cdiv(H, 8 * kWideOctets), 64) * 64) : p.threads;
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(threads), 0, s, a);
 }
 
 template <int kBlock>
@@ -703,11 +720,11 @@ extern "C" int nf4_residual_norm_fwd(const uint16_t* h, const uint16_t* o, int64
     hipStream_t s = static_cast<hipStream_t>(stream);
     const unsigned grid = rows_grid(T, H, post_norm, ragged);
     if (!o)
-        launch<Fwd<0>::Kernel>(a, H, ragged, grid, s);
+        launch<2, Fwd<0>::Kernel>(a, H, ragged, grid, s);
     else if (!post_norm)
-        launch<Fwd<1>::Kernel>(a, H, ragged, grid, s);
+        launch<2, Fwd<1>::Kernel>(a, H, ragged, grid, s);
     else
-        launch<Fwd<2>::Kernel>(a, H, ragged, grid, s);
+        launch<2, Fwd<2>::Kernel>(a, H, ragged, grid, s);
     return check_launch(fn);
 }
 
@@ -785,18 +802,18 @@ extern "C" int nf4_residual_norm_bwd(const uint16_t* const* dn, int n_dn, const 
     const int kind = !branch ? 0 : post_norm ? 2 : 1;
     if (T > 0 && sums) {
         if (kind == 0)
-            launch<Bwd<0, true>::Kernel>(a, H, ragged, grid, s);
+            launch<2, Bwd<0, true>::Kernel>(a, H, ragged, grid, s);
         else if (kind == 1)
-            launch<Bwd<1, true>::Kernel>(a, H, ragged, grid, s);
+            launch<kManyOctets, Bwd<1, true>::Kernel>(a, H, ragged, grid, s);
         else
-            launch<Bwd<2, true>::Kernel>(a, H, ragged, grid, s);
+            launch<kManyOctets, Bwd<2, true>::Kernel>(a, H, ragged, grid, s);
     } else if (T > 0) {
         if (kind == 0)
-            launch<Bwd<0, false>::Kernel>(a, H, ragged, grid, s);
+            launch<2, Bwd<0, false>::Kernel>(a, H, ragged, grid, s);
         else if (kind == 1)
-            launch<Bwd<1, false>::Kernel>(a, H, ragged, grid, s);
+            launch<2, Bwd<1, false>::Kernel>(a, H, ragged, grid, s);
         else
-            launch<Bwd<2, false>::Kernel>(a, H, ragged, grid, s);
+            launch<2, Bwd<2, false>::Kernel>(a, H, ragged, grid, s);
     }
     if (sums) {
         const SumArgs q{a.part, {dgain, dpost_gain, channel ? static_cast<float*>(dgate) : nullptr}, int(groups), int(H)};
