@@ -390,6 +390,15 @@ __global__ __launch_bounds__(threads_of(kRowKind, N)) void k_residual_norm_bwd(B
     for (int row = p.first; row < a.T; row += p.step) {
         const int64_t base = int64_t(row) * H;
         if constexpr (!kAhead) load_row<N, kRagged>(a, p, row, next);
+        // where registers are short the gains stay packed: made opaque here, their factors are not formed once, before
+        // the rows (2000 x 7001, gains and a gate a channel, 83 us, spilling, for 63; 8192 x 8192, which does not
+        // spill, 149 us for 156 without this)
+        if constexpr (kRagged && kAhead && kSums && kBranch > 1 && N > 1) {
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(fw[n][i]), "+v"(pw[n][i]));
+        }
         RowIn<N, kBranch> in = next;
 #pragma unroll
         for (int i = 0; i < 3; ++i)
