@@ -431,8 +431,7 @@ __global__ __launch_bounds__(256) void k_gemm_bwd_act8_finish(const float* __res
     const int tile = tl.full + q, row = tile % tl.mtiles * BM + (wave >> 2) * (BM / 2) + 32 * i + lane % 32;
     const int col = tile / tl.mtiles * kBK + 64 * (wave & 3) + 32 * j + 8 * sub + 4 * (lane >> 5);
     if (row >= T || col >= K) return;  // K % 64 == 0: the four columns are all in or all out
-    f32x4 a = {0.f, 0.f, 0.f, 0.f};
-    for (int w = q; w < tl.pieces; w += tl.tail) a += *reinterpret_cast<const f32x4*>(partial + size_t(w) * (BM * kBK) + loc);
+    const f32x4 a = sum_slots(partial + size_t(q) * (BM * kBK) + loc, tl.pieces / tl.tail, size_t(tl.tail) * (BM * kBK));
     *reinterpret_cast<u32x2*>(dx + size_t(row) * K + col) = u32x2{pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3])};
 }
 
