@@ -285,6 +285,64 @@ def test_linear_no_tokens(gpu_lib, dense):
     assert dx.shape == (0, 128) and not torch.any(dA) and not torch.any(dB)
 
 
+@pytest.mark.parametrize("t", [3, 40, 300])
+def test_checkpoints_at_their_least_alignment(gpu_lib, t):
+    """Codes at 16 bytes past 32, scales at 4 bytes past 8: every call that reads or writes them."""
+    lib, n, k = gpu_lib, 128, 320
+
+    def off():
+        codes = torch.empty(t * k + 16, dtype=torch.uint8, device="cuda")[16:].view(t, k)
+        return lib.Act8(codes, torch.empty(t * (k // 64) + 1, device="cuda")[1:].view(t, k // 64))
+
+    _, d = _linear_inputs(t, n, k, 16)
+    x, base, u = d["x"], lib.quantize(d["W"]), torch.randn(t, 16, device="cuda")
+    x8, y8 = lib.act8_quantize(x), lib.act8_quantize(x, out=off())
+    up = torch.randn(t, k, device="cuda").to(torch.bfloat16)
+    m = lib.silu_mul_fwd_act8(x, up, gate8=off(), up8=off())
+    want = lib.silu_mul_fwd_act8(x, up)
+    r, s = lib.residual_norm_fwd(x, up, n8=off()), lib.residual_norm_fwd(x, up, checkpoint=True)
+    pairs = list(zip((*y8, lib.act8_dequantize(y8), m[0], *m[1], *m[2], r.n, *r.n8),
+                     (*x8, lib.act8_dequantize(x8), want[0], *want[1], *want[2], s.n, *s.n8)))
+    pairs += zip((lib.silu_mul_act8(*m[1:]), *lib.silu_mul_bwd_act8(*m[1:], x)),
+                 (lib.silu_mul_act8(*want[1:]), *lib.silu_mul_bwd_act8(*want[1:], x)))
+    pairs.append((lib.residual_norm_bwd(up, r.rstd, n8=r.n8).dh, lib.residual_norm_bwd(up, s.rstd, n8=s.n8).dh))
+    for call, b in ((lib.lora_linear_bwd_act8, base), (lib.lora_linear_bwd_bf16_act8, (d["W"],))):
+        args = (u, d["dY"], d["A"], d["B"], 32.0)
+        pairs += zip(call(*b, y8, *args), call(*b, x8, *args))
+    assert all(torch.equal(p, q) for p, q in pairs)
+
+
+@pytest.mark.parametrize("dense,n", [(False, 32768), (True, 16368)])
+def test_linear_largest_base(gpu_lib, dense, n):
+    """The most weights that the call takes: dX's first and last columns, and dA's."""
+    lib, t, k = gpu_lib, 40, 65536
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    dy, x = (torch.randn(t, c, generator=g, device="cuda").to(torch.bfloat16) for c in (n, k))
+    A, B = (torch.randn(*c, generator=g, device="cuda").to(torch.bfloat16) for c in ((16, k), (n, 16)))
+    u, x8 = torch.randn(t, 16, generator=g, device="cuda"), lib.act8_quantize(x)
+    if dense:
+        base = (torch.randn(n, k, generator=g, device="cuda", dtype=torch.bfloat16),)
+        call = lib.lora_linear_bwd_bf16_act8
+    else:
+        base = (torch.randint(0, 256, (n, k // 2), generator=g, device="cuda", dtype=torch.uint8),
+                torch.rand(n, k // 64, generator=g, device="cuda"))
+        call = lib.lora_linear_bwd_act8
+    dx, dA, dB = call(*base, x8, u, dy, A, B, 32.0)
+    values = lib.act8_dequantize(x8)
+    d64, b64 = dy.double().cpu().numpy(), B.double().cpu().numpy()
+    for at in (0, k - 64):
+        w = base[0][:, at:at + 64] if dense else lib.dequantize(base[0][:, at // 2:at // 2 + 32].contiguous(),
+                                                                 base[1][:, at // 64:at // 64 + 1].contiguous())
+        wv, a = w.double().cpu().numpy(), A[:, at:at + 64].double().cpu().numpy()
+        check_bf16_output(bits_of(dx[:, at:at + 64].contiguous()), d64 @ wv + 2 * (d64 @ b64) @ a, "dx",
+                          mag=np.abs(d64) @ np.abs(wv) + 2 * (np.abs(d64) @ np.abs(b64)) @ np.abs(a), terms=n + 16)
+        xv = values[:, at:at + 64].double().cpu().numpy()
+        mag = 2 * (np.abs(d64) @ np.abs(b64)).T @ np.abs(xv)
+        err = np.abs(dA[:, at:at + 64].double().cpu().numpy() - 2 * (d64 @ b64).T @ xv)
+        assert np.all(err <= (n + t + 64) * U * mag)
+
+
 def test_linear_non_finite_block_reaches_its_columns(gpu_lib):
     lib = gpu_lib
     for t in (7, 200):
@@ -382,7 +440,7 @@ def _step_state(lib, t, c, n, seed):
 OUTS = ("m", "m2", "dg", "du", "dx", "dA", "dB")
 
 
-@pytest.mark.parametrize("t", [3, 150])
+@pytest.mark.parametrize("t", [3, 150, 700])
 def test_graph_replays_equal_eager(gpu_lib, t):
     """Two graphs captured over buffers of their own, replayed in turn with eager work between."""
     lib = gpu_lib
