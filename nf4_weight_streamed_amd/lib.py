@@ -562,6 +562,11 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(x, stream):
+    """_empty of x's own shape, type and device (1.2 us against 1.7)."""
+    return torch.empty_like(x) if stream is None else _empty(x.shape, x.dtype, x.device, stream)
+
+
 def rope_inv_freq(head_dim: int, theta: float = 1e6, device="cuda") -> torch.Tensor:
     """theta^(-2i/head_dim), i < head_dim/2, fp64: the frequencies of plain rotary positions."""
     return float(theta) ** (-torch.arange(0, head_dim, 2, dtype=torch.float64, device=device) / head_dim)
@@ -797,7 +802,7 @@ def silu_mul_fwd_act8(gate, up, out=None, gate8: Act8 | None = None, up8: Act8 |
     shape = t, c = _matrix(gate, "gate")
     _need(gate, "gate", torch.bfloat16, shape)
     _need(up, "up", torch.bfloat16, shape)
-    out = _empty(shape, torch.bfloat16, gate.device, stream) if out is None else out
+    out = _like(gate, stream) if out is None else out
     gate8 = act8_empty(t, c, gate.device, stream) if gate8 is None else gate8
     up8 = act8_empty(t, c, gate.device, stream) if up8 is None else up8
     _need(out, "out", torch.bfloat16, shape)
@@ -826,8 +831,8 @@ def silu_mul_bwd_act8(gate8: Act8, up8: Act8, dm, dgate=None, dup=None, stream=N
     _need_act8(gate8, "gate8", shape)
     _need_act8(up8, "up8", shape)
     _need(dm, "dm", torch.bfloat16, shape)
-    dgate = _empty(shape, torch.bfloat16, dm.device, stream) if dgate is None else dgate
-    dup = _empty(shape, torch.bfloat16, dm.device, stream) if dup is None else dup
+    dgate = _like(dm, stream) if dgate is None else dgate
+    dup = _like(dm, stream) if dup is None else dup
     _need(dgate, "dgate", torch.bfloat16, shape)
     _need(dup, "dup", torch.bfloat16, shape)
     _enqueue(_device(dm, dgate, dup, *gate8, *up8), stream, _lib.nf4_silu_mul_bwd_act8, gate8.codes.data_ptr(),
@@ -950,9 +955,9 @@ def residual_norm_fwd(h, o=None, post_norm: bool = False, post_gain=None, gate=N
             raise ValueError("post_norm, gate and h_out need a block's output o")
     else:
         _need(o, "o", torch.bfloat16, shape)
-        h_out = _empty(shape, torch.bfloat16, dev, stream) if h_out is None else h_out
+        h_out = _like(h, stream) if h_out is None else h_out
         _need(h_out, "h_out", torch.bfloat16, shape)
-    n = _empty(shape, torch.bfloat16, dev, stream) if n is None else n
+    n = _like(h, stream) if n is None else n
     _need(n, "n", torch.bfloat16, shape)
     if n8 is None and checkpoint:
         n8 = act8_empty(t, c, dev, stream)
@@ -976,6 +981,9 @@ def residual_norm_fwd(h, o=None, post_norm: bool = False, post_gain=None, gate=N
 @functools.lru_cache(maxsize=256)
 def residual_norm_bwd_workspace_bytes(T: int, H: int, sums: bool = True) -> int:
     return int(_lib.nf4_residual_norm_bwd_workspace(T, H, int(bool(sums))))
+
+
+_POINTERS = [C.c_void_p * i for i in (1, 2, 3)]
 
 
 def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=None, post_norm: bool = False, rstd_o=None,
@@ -1006,13 +1014,13 @@ def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=Non
     for x, name in ((h, "h"), (dres, "dres"), (o, "o")):
         if x is not None:
             _need(x, name, torch.bfloat16, shape)
-    dh = _empty(shape, torch.bfloat16, dev, stream) if dh is None else dh
+    dh = _like(dn[0], stream) if dh is None else dh
     _need(dh, "dh", torch.bfloat16, shape)
     if o is None:
         if post_norm or gate is not None or do is not None:
             raise ValueError("post_norm, gate and do need the block's output o")
     else:
-        do = _empty(shape, torch.bfloat16, dev, stream) if do is None else do
+        do = _like(dn[0], stream) if do is None else do
         _need(do, "do", torch.bfloat16, shape)
     if post_norm:
         _need(rstd_o, "rstd_o", torch.float32, (t,))
@@ -1036,7 +1044,7 @@ def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=Non
     if ws is None and sums:
         ws = _empty(max(residual_norm_bwd_workspace_bytes(t, c), 256), torch.uint8, dev, stream)
     codes, step = n8 or (None, None)
-    arr = (C.c_void_p * len(dn))(*(d.data_ptr() for d in dn))
+    arr = _POINTERS[len(dn) - 1](*[d.data_ptr() for d in dn])
     _enqueue(_device(*dn, dres, h, codes, step, rstd, o, rstd_o, post_gain, gate, gain, dh, do, dgate, dpost_gain, dgain, ws),
              stream, _lib.nf4_residual_norm_bwd, arr, len(dn), _opt(dres), _opt(h), _opt(codes), _opt(step), rstd.data_ptr(),
              _opt(o), _opt(rstd_o), t, c, int(bool(post_norm)), _opt(post_gain), kind, _opt(gate), float(scale), _opt(gain),
