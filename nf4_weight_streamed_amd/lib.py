@@ -923,6 +923,11 @@ class ResidualNormGrads(NamedTuple):
     dgain: torch.Tensor | None
 
 
+def _checked(t, name: str, dtype: torch.dtype, shape: tuple):
+    _need(t, name, dtype, shape)
+    return t
+
+
 def _norm_params(t, c, post_norm, post_gain, gate, gain) -> int:
     """Checks them; returns the gate's kind."""
     if post_gain is not None:
@@ -955,10 +960,8 @@ def residual_norm_fwd(h, o=None, post_norm: bool = False, post_gain=None, gate=N
             raise ValueError("post_norm, gate and h_out need a block's output o")
     else:
         _need(o, "o", torch.bfloat16, shape)
-        h_out = _like(h, stream) if h_out is None else h_out
-        _need(h_out, "h_out", torch.bfloat16, shape)
-    n = _like(h, stream) if n is None else n
-    _need(n, "n", torch.bfloat16, shape)
+        h_out = _like(h, stream) if h_out is None else _checked(h_out, "h_out", torch.bfloat16, shape)
+    n = _like(h, stream) if n is None else _checked(n, "n", torch.bfloat16, shape)
     if n8 is None and checkpoint:
         n8 = act8_empty(t, c, dev, stream)
     if n8 is not None:
@@ -966,10 +969,8 @@ def residual_norm_fwd(h, o=None, post_norm: bool = False, post_gain=None, gate=N
     if not post_norm:
         rstd_o = None
     else:
-        rstd_o = _empty((t,), torch.float32, dev, stream) if rstd_o is None else rstd_o
-        _need(rstd_o, "rstd_o", torch.float32, (t,))
-    rstd = _empty((t,), torch.float32, dev, stream) if rstd is None else rstd
-    _need(rstd, "rstd", torch.float32, (t,))
+        rstd_o = _empty((t,), torch.float32, dev, stream) if rstd_o is None else _checked(rstd_o, "rstd_o", torch.float32, (t,))
+    rstd = _empty((t,), torch.float32, dev, stream) if rstd is None else _checked(rstd, "rstd", torch.float32, (t,))
     codes, step = n8 or (None, None)
     _enqueue(_device(h, o, post_gain, gate, gain, h_out, n, codes, step, rstd_o, rstd), stream, _lib.nf4_residual_norm_fwd,
              h.data_ptr(), _opt(o), t, c, int(bool(post_norm)), _opt(post_gain), kind, _opt(gate), float(scale), _opt(gain),
@@ -1014,14 +1015,12 @@ def residual_norm_bwd(dn, rstd, h=None, n8: Act8 | None = None, dres=None, o=Non
     for x, name in ((h, "h"), (dres, "dres"), (o, "o")):
         if x is not None:
             _need(x, name, torch.bfloat16, shape)
-    dh = _like(dn[0], stream) if dh is None else dh
-    _need(dh, "dh", torch.bfloat16, shape)
+    dh = _like(dn[0], stream) if dh is None else _checked(dh, "dh", torch.bfloat16, shape)
     if o is None:
         if post_norm or gate is not None or do is not None:
             raise ValueError("post_norm, gate and do need the block's output o")
     else:
-        do = _like(dn[0], stream) if do is None else do
-        _need(do, "do", torch.bfloat16, shape)
+        do = _like(dn[0], stream) if do is None else _checked(do, "do", torch.bfloat16, shape)
     if post_norm:
         _need(rstd_o, "rstd_o", torch.float32, (t,))
     else:
