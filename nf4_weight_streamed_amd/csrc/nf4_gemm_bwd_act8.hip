@@ -38,9 +38,12 @@ constexpr int64_t kCUs = kChipCUs;
 
 // What the plan weighs, in steps of a 256 x 256 tile (1.8 us with a dense base, 2.0 with NF4, all CUs at work):
 // a step of a 128 x 256 tile, a tile's sums written and read again (14 steps for 256 of them), and the launch that
-// reads them, where dA has one share and it reads nothing else. Over 32 sizes (64 to 3000 tokens, both bases)
-// the choice is within 3 % of the better of the two tiles.
-constexpr double kStep128 = 0.57, kStep128Nf4 = 0.75, kSlot = 14.0 / kCUs, kLaunch = 2.0;
+// reads them, where dA has one share and it reads nothing else. The narrower tile costs more where its weights take
+// decoding or come from memory: a dense base of 283 MB, 245 tokens, 134 us in tiles of 128 tokens, 115 in 256;
+// one of 52 MB, 1291 tokens, 105 and 107. Over 88 sizes (40 to 3000 tokens, both bases) the choice is
+// within 6 % of the best of both tiles and all cuts.
+constexpr double kStep128 = 0.57, kStep128Far = 0.75, kSlot = 14.0 / kCUs, kLaunch = 2.0;
+constexpr int64_t kLastLevelCache = int64_t(256) << 20;
 
 // The adapter's steps: s.g as hi and lo parts of 32 ranks each side by side, or of 64 each in steps of their own.
 __host__ __device__ constexpr int adapter_steps(int r) { return r == 0 ? 0 : r <= 32 ? 1 : 2; }
@@ -443,7 +446,7 @@ BwdPlan plan_bwd_act8(int64_t T, int64_t N, int64_t K, int r, bool dense) {
     double best = 0;
     const int64_t steps = cdiv(N, kBN);
     for (int bm : {128, 256}) {
-        const double step = bm == 256 ? 1.0 : dense ? kStep128 : kStep128Nf4, slot = kSlot * bm / 256;
+        const double step = bm == 256 ? 1.0 : dense && N * K * 2 <= kLastLevelCache ? kStep128 : kStep128Far, slot = kSlot * bm / 256;
         const int64_t tiles = cdiv(T, bm) * cdiv(K, kBK), full = tiles / kCUs * kCUs, tail = tiles - full;
         for (int64_t cut = 1; cut <= (tail > 0 ? std::min(kCUs / tail, steps) : 1); ++cut) {
             const int64_t per = tail > 0 ? cdiv(steps, cut) : 0, pieces = tail > 0 ? cdiv(steps, per) * tail : 0;
