@@ -393,9 +393,9 @@ int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* 
  *   value = RN32((code - 128) scale)
  * so that a value is off by at most a / 254 and 2^-23 of itself. (For a < 2^-64 the code is that
  * of 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The
- * calls below take rows * cols <= 2^34; rows == 0 is a no-op; cols % 64 != 0 -> NF4_E_SHAPE.
- * bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input of the call itself, any
- * other overlap of an output is refused (NF4_E_ARG).
+ * calls of the codec and of the SiLU product take rows * cols <= 2^34; rows == 0 is a no-op;
+ * cols % 64 != 0 -> NF4_E_SHAPE. bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input
+ * of the call itself, any other overlap of an output is refused (NF4_E_ARG).
  */
 
 /* codes and scale of x. */
@@ -424,7 +424,9 @@ int nf4_silu_mul_bwd_act8(const uint8_t* gate_codes, const float* gate_scale, co
  * (x_codes [T][K], x_scale [T][K/64]): dA = s . g^T . RNbf(value), everything else as there but the
  * sizes of the workspace, which are the two functions' below. The products of dA and dB take
  * their fp32 operands (s.g, s.u) as three bf16 values instead of two, so that both are off by fp32's
- * roundings alone; dX is rounded to bf16 from sums in fp32 there and here, in other orders.
+ * roundings alone; dX is rounded to bf16 from sums in fp32 there and here, in other orders. An output
+ * or workspace that shares memory with any other argument is refused (NF4_E_ARG), dx over dy too: rows of
+ * dy are read until the last tile is done.
  */
 size_t nf4_lora_linear_bwd_act8_workspace(int64_t T, int64_t N, int64_t K, int r);
 size_t nf4_lora_linear_bwd_bf16_act8_workspace(int64_t T, int64_t N, int64_t K, int r);

@@ -315,6 +315,37 @@ int linear_fwd(const char* fn, const uint8_t* codes, const float* absmax, const 
 
 namespace {
 
+// The backward from a checkpoint reads its inputs and the workspace until its last launch: no output may meet anything.
+int check_bwd_overlaps(const char* fn, const uint8_t* codes, const float* absmax, const uint16_t* wdense, size_t N, size_t K,
+                       const SavedInput& x, const float* u_save, const uint16_t* dy, size_t T, const uint16_t* A,
+                       const uint16_t* B, size_t r, const uint16_t* dx, const float* dA, const float* dB, const void* ws,
+                       size_t ws_bytes) {
+    const bool adapter = r > 0;
+    const struct {
+        const char* name;
+        ByteRange at;
+    } all[] = {
+        {"ws", {ws, ws_bytes}},
+        {"dx", {dx, dx ? T * K * 2 : 0}},
+        {"dA", {dA, r * K * 4}},
+        {"dB", {dB, N * r * 4}},
+        {"the base", {wdense, wdense ? N * K * 2 : 0}},
+        {"codes", {codes, wdense ? 0 : N * K / 2}},
+        {"absmax", {absmax, wdense ? 0 : N * (K / NF4_BLOCK) * 4}},
+        {"dy", {dy, T * N * 2}},
+        {"x_codes", {x.codes, adapter ? T * K : 0}},
+        {"x_scale", {x.scale, adapter ? T * (K / NF4_BLOCK) * 4 : 0}},
+        {"u_save", {u_save, T * r * 4}},
+        {"A", {A, r * K * 2}},
+        {"B", {B, N * r * 2}},
+    };
+    constexpr size_t kWritten = 4;
+    for (size_t i = 0; i < kWritten; ++i)
+        for (size_t j = i + 1; j < sizeof all / sizeof all[0]; ++j)
+            if (all[i].at.meets(all[j].at)) return fail(NF4_E_ARG, "%s: %s overlaps %s", fn, all[i].name, all[j].name);
+    return NF4_OK;
+}
+
 // The backward after the base-specific checks; act8: the input is a checkpoint (with r = 0 there is none).
 int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const uint16_t* wdense, int64_t N, int64_t K,
                bool act8, const SavedInput& x, const float* u_save, const uint16_t* dy, int64_t T, const uint16_t* A,
@@ -332,6 +363,11 @@ int linear_bwd(const char* fn, const uint8_t* codes, const float* absmax, const 
     if (!ws || ws_bytes < p.ws_bytes || !aligned(ws, 256))
         return fail(NF4_E_ARG, "%s: workspace of %zu bytes (256-byte aligned) needed for T=%lld N=%lld K=%lld r=%d, got %zu",
                     fn, p.ws_bytes, (long long)T, (long long)N, (long long)K, r, ws_bytes);
+    if (act8) {
+        const int st = check_bwd_overlaps(fn, codes, absmax, wdense, size_t(N), size_t(K), x, u_save, dy, size_t(T), A, B,
+                                          size_t(r), dx, dA, dB, ws, p.ws_bytes);
+        if (st != NF4_OK) return st;
+    }
     hipStream_t s = static_cast<hipStream_t>(stream);
     const float scale = lora_scale(alpha, r);
     if (r == 0 && !dx) return NF4_OK;

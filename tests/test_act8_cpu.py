@@ -200,3 +200,33 @@ def test_binding_refusals(L):
         L.residual_norm_fwd(x)
     with pytest.raises(ValueError, match="one to three"):
         L.residual_norm_bwd([], torch.zeros(4))
+
+
+@pytest.mark.parametrize("dense", [False, True])
+@pytest.mark.parametrize("T", [4, 128])
+def test_linear_refuses_overlaps(L, dense, T):
+    """No output of the linear may share memory with an input or another output: not dx with dy either, whose rows
+    other tiles still read."""
+    raw, N, K, r = L.raw(), 128, 128, 16
+    names = ("x", "s", "u", "dy", "A", "B", "dx", "dA", "dB", "ws", "base") + (() if dense else ("absmax",))
+    good = {n: at(i) for i, n in enumerate(names)}
+    call = raw.nf4_lora_linear_bwd_bf16_act8 if dense else raw.nf4_lora_linear_bwd_act8
+    need = (L.bwd_bf16_act8_workspace_bytes if dense else L.bwd_act8_workspace_bytes)(T, N, K, r)
+
+    def run(rank=r, **kw):
+        p = dict(good, **kw)
+        base = (p["base"],) if dense else (p["base"], p["absmax"])
+        return call(*base, N, K, p["x"], p["s"], p["u"], p["dy"], T, p["A"], p["B"], rank, 32.0, p["dx"], p["dA"], p["dB"],
+                    p["ws"], need, None)
+
+    for name in ("dx", "dA", "dB", "ws"):
+        for i, other in enumerate(names):
+            if other != name:
+                _err(L, run(**{name: at(i)}), L.NF4_E_ARG, "overlaps")
+                if name != "ws":
+                    _err(L, run(**{name: at(i, 16)}), L.NF4_E_ARG, "overlaps")
+    # the last bytes of the one before
+    _err(L, run(dx=C.c_void_p(good["dy"].value + T * N * 2 - 16)), L.NF4_E_ARG, "dx overlaps")
+    _err(L, run(dx=C.c_void_p(good["dy"].value - T * K * 2 + 16)), L.NF4_E_ARG, "dx overlaps")
+    # without adapters the rest takes no part
+    _err(L, run(rank=0, x=None, s=None, u=None, A=None, B=None, dA=None, dB=None, dx=good["dy"]), L.NF4_E_ARG, "dx overlaps")
