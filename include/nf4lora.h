@@ -391,8 +391,8 @@ int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* 
  *   scale = RN32(a / 127)
  *   code  = 128 + rne(x RN32(127 / a))        (the product exact; 1..255; a == 0: all 128)
  *   value = RN32((code - 128) scale)
- * so that a value is off by at most a / 254 and 2^-23 of itself. (For a < 2^-64 the code is that
- * of 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The
+ * so that a value is off by at most a / 254 and 2^-23 of itself; where a / 127 is below fp32's normal
+ * numbers, the step's own rounding adds at most 127 * 2^-150. (For a < 2^-64 the code is that of 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The
  * calls of the codec and of the SiLU product take rows * cols <= 2^34; rows == 0 is a no-op;
  * cols % 64 != 0 -> NF4_E_SHAPE. bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input
  * of the call itself, any other overlap of an output is refused (NF4_E_ARG).

@@ -2,7 +2,8 @@
 // row share one step,
 //   a = max |x|,  scale = RN32(a / 127),  code = 128 + rne(x RN32(127 / a)),
 //   value = RN32((code - 128) scale),
-// so that a value is off by at most half a step, a / 254 (and an ulp of fp32).
+// so that a value is off by at most half a step, a / 254, and 2^-23 of itself (a subnormal step's rounding adds up
+// to 127 2^-150).
 #pragma once
 
 #include <type_traits>

@@ -114,3 +114,26 @@ def test_stack_backward_with_exact_checkpoints_is_the_plain_one():
     for a, b in zip(grads8, grads):
         for key in b:
             assert O.rel_l2(a[key], b[key]) <= 8 * 2.0 ** -9, key
+
+
+@pytest.mark.parametrize("a", [range(0x3F80, 0x4000), range(0x0001, 0x0480)])
+def test_values_within_the_stated_bound(a):
+    """|value - x| <= a / 254 + 2^-23 |value| over every largest a of one binade beside every bf16 value down to
+    code 0, and over every a up to past where the step a / 127 is a normal fp32 number (a = 127 2^-126) beside every
+    value below it: there the step's own rounding, by up to 2^-150, adds at most 127 of those."""
+    passed = 0
+    for top in a:
+        x = np.arange(max(0, top - 10 * 128), top + 1).astype(np.uint16)
+        blocks = np.zeros((-(-len(x) // 63), 64), np.uint16)
+        blocks[:, 0] = top
+        blocks[:, 1:].flat[:len(x)] = x
+        codes, scale = O.act8_quantize(blocks)
+        v, got = O.bf16_bits_to_f64(blocks), O.act8_values(codes, scale).astype(np.float64)
+        largest = v[0, 0]
+        err = np.abs(got - v) - (largest / 254 * (1 + 2.0 ** -50) + 2.0 ** -23 * np.abs(got))
+        if largest >= 127 * 2.0 ** -126:
+            assert np.all(err <= 0)
+        else:
+            assert np.all(err <= 127 * 2.0 ** -150)
+            passed += bool(np.any(err > 0))
+    assert (passed > 0) == (a[0] == 1)                            # the addition is needed, and for subnormal steps alone
