@@ -435,3 +435,59 @@ def test_refusals(gpu_lib):
         lib.residual_norm_bwd([h] * 4, rstd, h=h)
     with pytest.raises(TypeError, match="rstd_o"):
         lib.residual_norm_bwd(h, rstd, h=h, o=h, post_norm=True)
+
+
+@pytest.mark.parametrize("t,c", [(300, 8200), (520, 12288), (300, 16383), (400, 7001), (700, 1001), (1100, 333)])
+def test_many_rows_of_wide_and_odd_widths(gpu_lib, t, c):
+    """Several rows a workgroup where the sums over them lie in LDS and the gains are read again for each row (above 8192),
+    and where rows are ragged: the next row's loads under way, gains kept packed."""
+    for post, gate, gain, offset in ((True, "token", True, 1.0), (True, "channel", True, 0.0), (False, "token", True, 0.0),
+                                     (False, "channel", False, 0.0)):
+        p = _case(t, c, post, gate, gain, offset, dns=3)
+        _check_fwd(gpu_lib, p, post, 0.5, offset)
+        _check_bwd(gpu_lib, p, post, 0.5, offset)
+        _check_bwd(gpu_lib, p, post, 0.5, offset, param_grads=False, dres=False)
+    _check_bwd(gpu_lib, _case(t, c, False, "none", True, 1.0, dns=3), False, 1.0, 1.0, block=False)
+
+
+@pytest.mark.parametrize("trained", [True, False])
+@pytest.mark.parametrize("t,c", [(5300, 5120), (6600, 5119), (2700, 10240)])
+def test_calls_that_no_cache_holds(gpu_lib, t, c, trained):
+    """Forward and backward of more than 256 MB, whose inputs are loaded past the caches: every row's results are those
+    of a call on some of the rows."""
+    lib = gpu_lib
+    g = torch.Generator(device="cuda")
+    g.manual_seed(c)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    h, o, gate, dres = (normal(t, c) for _ in range(4))
+    dn = [normal(t, c) for _ in range(3)]
+    params = dict(post_norm=True, post_gain=normal(c), gain=normal(c), gain_offset=1.0, scale=0.5)
+    fwd = lib.residual_norm_fwd(h, o, gate=gate, checkpoint=c % 64 == 0, **params)
+    back = lib.residual_norm_bwd(dn, fwd.rstd, h=fwd.h, dres=dres, o=o, rstd_o=fwd.rstd_o, gate=gate, param_grads=trained, **params)
+    sums = torch.zeros(2, c, dtype=torch.float64, device="cuda")
+    for at in range(0, t, 500):
+        def part(x):
+            return x[at:at + 500].contiguous()
+
+        f = lib.residual_norm_fwd(part(h), part(o), gate=part(gate), checkpoint=c % 64 == 0, **params)
+        pairs = [(f.h, fwd.h), (f.n, fwd.n), (f.rstd, fwd.rstd), (f.rstd_o, fwd.rstd_o)]
+        pairs += list(zip(f.n8 or (), fwd.n8 or ()))
+        b = lib.residual_norm_bwd([part(d) for d in dn], f.rstd, h=f.h, dres=part(dres), o=part(o), rstd_o=f.rstd_o,
+                                  gate=part(gate), param_grads=trained, **params)
+        pairs += [(b.dh, back.dh), (b.do, back.do)] + ([(b.dgate, back.dgate)] if trained else [])
+        assert all(torch.equal(x, y[at:at + 500]) for x, y in pairs), at
+        if trained:
+            sums += torch.stack([b.dgain, b.dpost_gain]).double()
+    if trained:
+        # both sides sum the same rounded products, with at most t additions in fp32 on either
+        u = o.double() * fwd.rstd_o.double()[:, None]
+        mag = [(sum(d.double().abs() for d in dn) * fwd.h.double().abs() * fwd.rstd.double()[:, None]).sum(0)]
+        w = sum(d.double() for d in dn) * (params["gain"].double() + 1)
+        b = fwd.h.double() * fwd.rstd.double()[:, None]
+        ds = dres.double() + fwd.rstd.double()[:, None] * (w - b * (w * b).mean(1, keepdim=True))
+        mag.append((0.5 * ds.abs() * gate.double().abs() * u.abs()).sum(0) * 1.01)      # the kernel's ds is off by far less
+        for got, want, m in zip((back.dgain, back.dpost_gain), sums, mag):
+            assert torch.all((got.double() - want).abs() <= 2 * t * U * m)
