@@ -478,3 +478,23 @@ def test_other_stream(gpu_lib):
     got = lib.act8_dequantize(lib.act8_quantize(y, stream=side), stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_calls_that_no_cache_holds(gpu_lib):
+    """Codec and SiLU product of more than 256 MB, whose inputs are loaded past the caches: every row's results are those of a
+    call on some of the rows."""
+    lib, t, c = gpu_lib, 12900, 7040
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    gate, up, dm = (torch.randn(t, c, generator=g, device="cuda").to(torch.bfloat16) for _ in range(3))
+    m, g8, u8 = lib.silu_mul_fwd_act8(gate, up)
+    again, back = lib.silu_mul_act8(g8, u8), lib.silu_mul_bwd_act8(g8, u8, dm)
+    values = lib.act8_dequantize(u8, out=torch.empty_like(up))
+    for at in range(0, t, 600):
+        def part(x):
+            return x[at:at + 600].contiguous()
+
+        n, p8, q8 = lib.silu_mul_fwd_act8(part(gate), part(up))
+        pairs = [(n, m), *zip(p8, g8), *zip(q8, u8), (lib.silu_mul_act8(p8, q8), again), (lib.act8_dequantize(q8), values)]
+        pairs += zip(lib.silu_mul_bwd_act8(p8, q8, part(dm)), back)
+        assert all(torch.equal(x, y[at:at + 600]) for x, y in pairs), at
