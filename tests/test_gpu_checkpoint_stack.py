@@ -136,3 +136,48 @@ def test_refusals_and_scratch(ST):
         torch.cuda.synchronize()
         assert [n for n, t in scratch.items() if bool((t.view(torch.int16) == 0x7FA5).any())] == []
         st.close()
+
+
+@pytest.mark.parametrize("t,lens", [(41, None), (150, [100, 1, 49])])
+def test_backward_at_the_stacks_own_checkpoints(ST, t, lens):
+    """The oracle's backward from what the stack itself kept: its checkpoints' values, a, rotated q and k, v, lse and
+    1 / rms. What is left to differ are the backward's roundings, as in the bf16 stack with attention (the linears' 2e-3
+    bar, four more of 2^-8 / sqrt(3) rms), and one of those for dB, whose u comes from the forward's own x: 1.15e-2,
+    a third of what a test has to allow where each side rounds to steps of its own."""
+    L, alpha = 2, 32.0
+    dims = ST.StackDims(**TINY)
+    w, lo, base, lora = _stack(ST, L, 1, dims)
+    h0, dh = S.activations(t, dims.hidden, tensor="h0"), S.activations(t, dims.hidden, tensor="dH")
+    st = ST.NF4Stack(base, lora, t, alpha, mode="resident", mixing="attention", seq_lens=lens, checkpoints="int8")
+    _, dh0 = st.step(to_dev_bf16(h0), to_dev_bf16(dh))
+    torch.cuda.synchronize()
+    od = O.StackLayerDims(dims.hidden, dims.q, dims.kv, dims.inter, dims.head_dim)
+    layers = [{p: (O.dequantize(*O.quantize(O.bf16_bits_to_f64(w[(l, p)]).astype(np.float32))), *lo[(l, p)])
+               for p in PROJS} for l in range(L)]
+    pos = np.concatenate([np.arange(n) for n in (lens or [t])])
+    inv = 1e6 ** (-np.arange(0, dims.head_dim, 2) / dims.head_dim)
+    _, saved = O.decoder_forward(h0, layers, od, alpha, pos, inv, lens)
+    kept = []
+    for l in reversed(range(L)):
+        A = st.acts[l]
+        for name in ("ha", "hm", "gate", "up"):                     # the order in which the backward reads them
+            x8 = A[name + "8"]
+            kept.append(O.act8_values(x8.codes.cpu().numpy(), x8.scale.cpu().numpy()).astype(np.float64))
+            # half a step, 0.0075 rms, and the forward's own bar, doubled: what it says it is
+            assert O.rel_l2(kept[-1], saved[l][name]) <= 2 * (0.0075 + 2e-3), (l, name)
+        for name in ("a", "q", "k", "v"):
+            saved[l][name] = O.bf16_bits_to_f64(bits_of(A[name]))
+        saved[l]["lse"] = f32_of(A["lse"]).astype(np.float64)
+        for name, rs in (("h", "rs_h"), ("h1", "rs_h1")):            # rows of that 1 / rms: nothing else is read of them
+            ms = 1 / f32_of(A[rs]).astype(np.float64) ** 2 - O.RMS_EPS
+            saved[l][name] = np.sqrt(ms)[:, None] * np.ones((1, dims.hidden))
+    values = iter(kept)
+    dh0_ref, grads = O.decoder_backward_act8(dh, layers, od, alpha, saved, pos, inv, lens, keep=lambda x: next(values))
+    assert next(values, None) is None
+    bar = float(np.hypot(2e-3, 5 * 2.0 ** -8 / np.sqrt(3)))
+    assert O.rel_l2(O.bf16_bits_to_f64(bits_of(dh0)), dh0_ref) <= bar
+    for l in range(L):
+        for p in PROJS:
+            for got, key in zip(st.grads[l][p], ("_dA", "_dB")):
+                assert O.rel_l2(f32_of(got), grads[l][p + key]) <= bar, (l, p, key)
+    st.close()
