@@ -392,10 +392,11 @@ int nf4_grad_clip(const nf4_grad_list* list, float max_norm, float* norm, void* 
  *   code  = 128 + rne(x RN32(127 / a))        (the product exact; 1..255; a == 0: all 128)
  *   value = RN32((code - 128) scale)
  * so that a value is off by at most a / 254 and 2^-23 of itself; where a / 127 is below fp32's normal
- * numbers, the step's own rounding adds at most 127 * 2^-150. (For a < 2^-64 the code is that of 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The
- * calls of the codec and of the SiLU product take rows * cols <= 2^34; rows == 0 is a no-op;
- * cols % 64 != 0 -> NF4_E_SHAPE. bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input
- * of the call itself, any other overlap of an output is refused (NF4_E_ARG).
+ * numbers, the step's own rounding adds at most 127 * 2^-150. (For a < 2^-64 the code is that of
+ * 2^64 x.) A run that holds an infinity or a NaN has scale NaN: all its values are NaN. The calls of
+ * the codec and of the SiLU product take rows * cols <= 2^34; rows == 0 is a no-op; cols % 64 != 0 ->
+ * NF4_E_SHAPE. bf16 tensors are 16-byte aligned; a bf16 output may be a bf16 input of the call
+ * itself, any other overlap of an output is refused (NF4_E_ARG).
  */
 
 /* codes and scale of x. */
@@ -594,10 +595,12 @@ int stream_pool_create(const nf4_host_block* blocks, int n_blocks, void* device_
  * compute then run one after the other (measured: 66 ms against 41 ms for 8 blocks
  * of 256 MiB, for every fourth stream created). The two streams are created one right
  * after the other, non-blocking, at the default priority, on the first call for a
- * device, after others that level the queues and are destroyed, so they take different
- * queues, and are kept until the process ends; later
- * calls return the same pair. Errors: NF4_E_ARG for NULL arguments, NF4_E_HIP if a
- * stream cannot be created.
+ * device, after 14 others that level the queues and are destroyed, and are kept until the
+ * process ends; later calls return the same pair. They take different queues as long as
+ * streams that the process destroyed before left the queues at most 14 short of being
+ * level (HIP offers no choice of a queue: past that the two may share one, which costs
+ * overlap, not results). Errors: NF4_E_ARG for NULL arguments, NF4_E_HIP if a stream cannot
+ * be created.
  */
 int stream_pool_streams(nf4_stream* compute_out, nf4_stream* copy_out);
 

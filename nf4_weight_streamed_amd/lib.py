@@ -1105,8 +1105,8 @@ _POOL_STREAMS: dict = {}
 
 def pool_streams():
     """The current device's (compute, copy) stream pair for streamed passes
-    (stream_pool_streams): created back to back so that they sit on different
-    hardware queues, kept for the life of the process."""
+    (stream_pool_streams): created back to back, after others that level the hardware
+    queues, so that they sit on different ones, and kept for the life of the process."""
     dev = torch.cuda.current_device()
     if dev not in _POOL_STREAMS:
         c, k = C.c_void_p(), C.c_void_p()
