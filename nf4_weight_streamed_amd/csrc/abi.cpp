@@ -117,7 +117,7 @@ int check_linear_common(const char* fn, const uint8_t* codes, const float* absma
     if (N % 16 != 0) return fail(NF4_E_SHAPE, "%s: N=%lld is not a multiple of 16", fn, (long long)N);
     // The kernels address one weight matrix with 32-bit byte offsets (within 2^30
     // bytes) and every activation or partial through descriptors over at most one
-    // 128-row tile; T <= 2^23 keeps the tile counts of the 1-D grids below 2^31.
+    // tile of 256 rows; T <= 2^23 keeps the tile counts of the 1-D grids below 2^31.
     if (N > (int64_t(1) << 21) || K > (int64_t(1) << 21) || N * K > (int64_t(1) << 31) || T > (int64_t(1) << 23))
         return fail(NF4_E_SHAPE, "%s: sizes beyond the limits N, K <= 2^21, N*K <= 2^31, T <= 2^23 (N=%lld K=%lld T=%lld)",
                     fn, (long long)N, (long long)K, (long long)T);

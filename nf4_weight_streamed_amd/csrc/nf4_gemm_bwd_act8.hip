@@ -17,9 +17,9 @@
 // 287 (NF4). Of those 230 and 250 are this kernel's, 1195 and 1100 TFLOP/s; its products and barriers alone,
 // without copies and operand reads, take 180, and a large library product of bf16 reaches 1370 TFLOP/s. 56 %
 // of the cycles have a matrix instruction under way (NF4 in the loop's first form: 42 %).
-// 512 x 18944 x 3584 with NF4 (a 7B gate projection's backward) takes 103-105 us: 13 for g and dB, 6 for
-// the adapter, 70 here, 13 for the sums of the pieces, whose 2 x 66 MB are the price of cutting 28 tiles
-// for 256 CUs. 1291 x 5120 x 5120 dense: 103.
+// 512 x 18944 x 3584 with NF4 (a 7B gate projection's backward) takes 103-105 us in a row; a kernel trace, one launch at a
+// time, has 14 for g and dB, 6 for the adapter, 74-76 here, 13 for the sums of the pieces, whose 2 x 66 MB are the price of
+// cutting 28 tiles for 256 CUs. 1291 x 5120 x 5120 dense: 100-105.
 #include "act8.h"
 #include "common.h"
 #include "device.h"

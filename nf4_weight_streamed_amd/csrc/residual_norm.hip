@@ -12,8 +12,8 @@
 // written once; that traffic is the bound. All arithmetic is fp32. Sums over rows (gains, a
 // gate a channel) are kept per column in registers over a workgroup's rows, then added over
 // the workgroups by a second kernel, in a fixed order.
-// Measured, 8192 x 8192 (what it has to move): norm alone 46 us (5.8 TB/s), add 88 (6.1), both norms, a gate a
-// channel and the checkpoint 97 (6.3); backward of one reader 87 (6.2), both norms, a gate a token, three readers
+// Measured, calls in a row, 8192 x 8192 (what it has to move): norm alone 46 us (5.8 TB/s), add 88 (6.1), both norms, a gate
+// a channel and the checkpoint 97-103 (6.3-5.9; 101-106 in a kernel trace); backward of one reader 87 (6.2), both norms, a gate a token, three readers
 // and the gains' sums 233 (5.8). 4096 x 16384 the same 269 (5.0), 4096 x 3583 80 (3.7), 2731 x 5120 60 (4.6).
 #include <cmath>
 

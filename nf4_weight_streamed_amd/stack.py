@@ -39,9 +39,9 @@ With checkpoints="int8" what a layer keeps for its backward is held in 8 bits wh
 backward allows it: h_a and h_m (which serve the projections' adapter gradients and the
 norms' own backward), gate and up; the down projection's input is rebuilt from the latter
 two, and no hidden state is kept. Rotated q and k, v, a and the softmax statistics stay as
-they are. The forward's residual add and norm are one pass, which normalises h' before
-its rounding to bf16 (the bf16 stack after it), so that the two forwards differ by that
-rounding; the gradients are those at the checkpoints' values. Streamed, resident and
+they are. In the forward the add after L_o and the norm behind it are one pass, which
+normalises h' before its rounding to bf16 (the bf16 stack after it), so that the two forwards
+differ by that rounding (the add after L_down is a call of its own); the gradients are those at the checkpoints' values. Streamed, resident and
 rematerialised runs stay bitwise equal to one another.
 """
 
