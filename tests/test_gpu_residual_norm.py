@@ -491,3 +491,24 @@ def test_calls_that_no_cache_holds(gpu_lib, t, c, trained):
         mag.append((0.5 * ds.abs() * gate.double().abs() * u.abs()).sum(0) * 1.01)      # the kernel's ds is off by far less
         for got, want, m in zip((back.dgain, back.dpost_gain), sums, mag):
             assert torch.all((got.double() - want).abs() <= 2 * t * U * m)
+
+
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("c", [7, 515, 1001, 1032, 4099, 8200, 12291])
+def test_results_over_either_input(gpu_lib, c, post):
+    """h_out over o and n over h as well as the other way round, plain adds (whose stream is stored before any sum of the
+    row) too; one gradient given for all readers, and dh or do over it."""
+    lib, t = gpu_lib, 700
+    h, o, gate, d, e = (torch.randn(t, c, device="cuda").to(torch.bfloat16) for _ in range(5))
+    kw = dict(post_norm=post, gate=gate, scale=0.5)
+    want = lib.residual_norm_fwd(h, o, **kw)
+    for swap in (False, True):
+        h2, o2 = h.clone(), o.clone()
+        got = lib.residual_norm_fwd(h2, o2, h_out=o2 if swap else h2, n=h2 if swap else o2, **kw)
+        assert all(torch.equal(getattr(got, n), getattr(want, n)) for n in ("h", "n", "rstd"))
+    back = dict(kw, h=want.h, rstd_o=want.rstd_o, dres=e, param_grads=False)
+    ref = lib.residual_norm_bwd([d.clone(), d.clone(), d.clone()], want.rstd, o=o, **back)
+    for dh, do in ((True, False), (False, True)):
+        d2 = d.clone()
+        g = lib.residual_norm_bwd([d2, d2, d2], want.rstd, o=o, dh=d2 if dh else None, do=d2 if do else None, **back)
+        assert torch.equal(g.dh, ref.dh) and torch.equal(g.do, ref.do)
